@@ -1,7 +1,8 @@
-"""ctypes binding of the C ABI in include/splitzip.h.
+"""ctypes binding of the C ABI in include/splitzip.h and include/splitzip_kv.h.
 
 Argument marshalling only: every step of calibrate / encode / decode runs in
-the HIP kernels of ``_lib/libsplitzip.so``.  The library must have been built
+the HIP kernels of ``_lib/libsplitzip.so``, every step of the key-value cache
+in those of ``_lib/libsplitzip_kv.so``.  They must have been built
 (``python -m lossless_bf16_tensor_splitzip_amd._build`` or
 ``__graft_entry__.build()``); there is no fallback of any kind.
 """
@@ -10,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from ._build import CEILING_LIB_PATH, LIB_PATH
+from ._build import CEILING_LIB_PATH, KV_LIB_PATH, LIB_PATH
 
 CHUNK = 1024
 MAX_N = 1 << 36
@@ -160,6 +161,101 @@ def ceiling_lib():
     return handle
 
 
+# include/splitzip_kv.h (strides as single fields: the same layout as the
+# header's arrays, cheaper to fill)
+
+KV_BF16 = 0
+KV_FP16 = 1
+KV_ALL = 0xFFFFFFFF
+
+# status bits of the key-value cache calls
+KV_BAD_PAGE = 1
+KV_BAD_LEN = 2
+KV_BAD_ROWS = 4
+
+_U32 = ctypes.c_uint32
+
+
+class KVCacheArgs(ctypes.Structure):
+    """Mirror of splitzip_kv_cache."""
+    _fields_ = [
+        ("k", _P), ("v", _P),
+        ("k_stride0", _U64), ("k_stride1", _U64), ("k_stride2", _U64),
+        ("v_stride0", _U64), ("v_stride1", _U64), ("v_stride2", _U64),
+        ("table", _P), ("table_stride", _U64), ("lens", _P),
+        ("num_pages", _U32), ("page_size", _U32), ("kv_heads", _U32), ("head_dim", _U32),
+        ("batch", _U32), ("max_pages", _U32), ("dtype", _U32), ("reserved", _U32),
+    ]
+
+
+class KVRows(ctypes.Structure):
+    """Mirror of splitzip_kv_rows."""
+    _fields_ = [
+        ("k", _P), ("v", _P),
+        ("k_stride0", _U64), ("k_stride1", _U64), ("v_stride0", _U64), ("v_stride1", _U64),
+        ("rows", _U32), ("reserved", _U32), ("cu", _P), ("start", _P),
+    ]
+
+
+class KVQuery(ctypes.Structure):
+    """Mirror of splitzip_kv_query."""
+    _fields_ = [
+        ("q", _P), ("q_stride0", _U64), ("q_stride1", _U64),
+        ("out", _P), ("out_stride0", _U64), ("out_stride1", _U64),
+        ("lse", _P), ("mass", _P), ("mass_out", _P),
+        ("mass_stride0", _U64), ("mass_stride1", _U64),
+        ("mass_out_stride0", _U64), ("mass_out_stride1", _U64),
+        ("heads", _U32), ("window", _U32), ("sinks", _U32), ("scale", ctypes.c_float),
+        ("mass_len", _U32), ("reserved", _U32),
+    ]
+
+
+class KVBudget(ctypes.Structure):
+    """Mirror of splitzip_kv_budget."""
+    _fields_ = [
+        ("mass", _P), ("mass_out", _P),
+        ("mass_stride0", _U64), ("mass_stride1", _U64),
+        ("mass_out_stride0", _U64), ("mass_out_stride1", _U64),
+        ("kept", _P), ("budget", _U32), ("sinks", _U32), ("recent", _U32), ("mass_len", _U32),
+    ]
+
+
+KV_STRUCTS = (KVCacheArgs, KVRows, KVQuery, KVBudget)
+
+KV_SIGNATURES = {
+    "splitzip_kv_struct_sizes": (None, [ctypes.POINTER(ctypes.c_size_t)]),
+    "splitzip_kv_append": (ctypes.c_int, [_P, _P, _P, _P]),
+    "splitzip_kv_gather": (ctypes.c_int, [_P, _P, _P, _P]),
+    "splitzip_kv_attend_workspace_size": (_SZ, [_P, _U32, _U32]),
+    "splitzip_kv_attend": (ctypes.c_int, [_P, _P, _P, _SZ, _P, _P]),
+    "splitzip_kv_evict": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+}
+
+_kv = None
+
+
+def kv_lib():
+    """Load the key-value cache library (raises if it has not been built)."""
+    global _kv
+    if _kv is not None:
+        return _kv
+    if not os.path.exists(KV_LIB_PATH):
+        raise RuntimeError(
+            "SplitZip key-value cache library not built (%s missing): run "
+            "`python -m lossless_bf16_tensor_splitzip_amd._build`" % KV_LIB_PATH)
+    handle = ctypes.CDLL(KV_LIB_PATH)
+    for name, (res, args) in KV_SIGNATURES.items():
+        fn = getattr(handle, name)
+        fn.restype = res
+        fn.argtypes = args
+    sizes = (ctypes.c_size_t * len(KV_STRUCTS))()
+    handle.splitzip_kv_struct_sizes(sizes)
+    if list(sizes) != [ctypes.sizeof(t) for t in KV_STRUCTS]:
+        raise RuntimeError("struct layout mismatch between the library and the binding")
+    _kv = handle
+    return handle
+
+
 def lib():
     """Load the HIP library (raises if it has not been built)."""
     global _lib
@@ -288,3 +384,27 @@ def splitzip_encode_batch(items, count: int, d_ws: int, ws_bytes: int, stream: i
 
 def splitzip_decode_batch(items, count: int, d_status: int, stream: int) -> int:
     return lib().splitzip_decode_batch(_items_ptr(items), count, d_status, stream)
+
+
+# Key-value cache (structs by reference, raw pointers / ints in, status out).
+
+def splitzip_kv_append(cache, rows, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_append(ctypes.byref(cache), ctypes.byref(rows), d_status, stream)
+
+
+def splitzip_kv_gather(cache, rows, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_gather(ctypes.byref(cache), ctypes.byref(rows), d_status, stream)
+
+
+def splitzip_kv_attend_workspace_size(cache, heads: int, mass_len: int) -> int:
+    return kv_lib().splitzip_kv_attend_workspace_size(ctypes.byref(cache), heads, mass_len)
+
+
+def splitzip_kv_attend(cache, query, d_ws: int, ws_bytes: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_attend(ctypes.byref(cache), ctypes.byref(query), d_ws, ws_bytes,
+                                       d_status, stream)
+
+
+def splitzip_kv_evict(cache, to, budget, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_evict(ctypes.byref(cache), ctypes.byref(to), ctypes.byref(budget),
+                                      d_status, stream)

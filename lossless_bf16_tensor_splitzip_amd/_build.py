@@ -1,5 +1,6 @@
 """Build of the HIP libraries (gfx950 only): ``_lib/libsplitzip.so``, the
-codec, and ``_lib/libsplitzip_ceiling.so``, the reference memory streams its
+codec, ``_lib/libsplitzip_kv.so``, the paged key-value cache, and
+``_lib/libsplitzip_ceiling.so``, the reference memory streams the codec's
 kernels are measured against."""
 from __future__ import annotations
 
@@ -12,6 +13,8 @@ SRC = os.path.join(PKG, "csrc", "splitzip.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsplitzip.so")
+KV_SRC = os.path.join(PKG, "csrc", "kv.hip")
+KV_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_kv.so")
 CEILING_SRC = os.path.join(PKG, "csrc", "ceiling.hip")
 CEILING_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_ceiling.so")
 
@@ -49,8 +52,9 @@ def _compile(src: str, lib_path: str, verbose: bool) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile both libraries (always recompiles); returns the codec's path."""
+    """Compile the libraries (always recompiles); returns the codec's path."""
     _compile(CEILING_SRC, CEILING_LIB_PATH, verbose)
+    _compile(KV_SRC, KV_LIB_PATH, verbose)
     return _compile(SRC, LIB_PATH, verbose)
 
 

@@ -1,0 +1,299 @@
+"""Tensor-level calls of the paged key-value cache: marshalling of torch
+tensors (device memory and streams only) into the C ABI of
+include/splitzip_kv.h.  Copies, attention and eviction run entirely in the HIP
+kernels.
+
+    cache = KVCache(k_pages, v_pages, table, lens)
+    ws = KVWorkspace(cache, heads)
+    lens += 1                              # the step's tokens
+    cache.append(k, v, cu)                 # their K and V
+    out = cache.attend(q, ws)              # one new token per sequence
+
+The pools are [pages, kv_heads, page_size, head_dim]; a pool stored
+[pages, page_size, kv_heads, head_dim] is passed as its transpose(1, 2).
+Nothing here computes gradients: a cache is what a serving step keeps.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _abi
+from .codec import _device_or_pinned, _same_gpu, _status_ptr, _stream
+
+_DTYPES = {torch.bfloat16: _abi.KV_BF16, torch.float16: _abi.KV_FP16}
+
+
+def _on(device):
+    """The call's device as the current one (kernels go to the current one)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _strides(t: torch.Tensor, what: str, multiple: int = 8):
+    """Strides of all dimensions but the last, which must be contiguous; those
+    of a dimension of one entry are never used and given as 0."""
+    size, stride = t.shape, t.stride()
+    if stride[-1] != 1 and size[-1] > 1:
+        raise ValueError("the last dimension of the %s must be contiguous" % what)
+    out = [st if n > 1 else 0 for n, st in zip(size[:-1], stride[:-1])]
+    if multiple > 1:
+        if t.data_ptr() % (2 * multiple):
+            raise ValueError("the %s must be %d-byte aligned" % (what, 2 * multiple))
+        for st in out:
+            if st % multiple:
+                raise ValueError("the strides of the %s must be multiples of %d elements, got %s"
+                                 % (what, multiple, tuple(stride)))
+    return out
+
+
+def _no_overlap(t: torch.Tensor, what: str) -> None:
+    """Refuses a written tensor two of whose elements share memory (an
+    expanded one)."""
+    reach = 0
+    for st, n in sorted((st, n) for n, st in zip(t.shape, t.stride()) if n > 1):
+        if st <= reach:
+            raise ValueError("elements of the %s overlap in memory" % what)
+        reach += st * (n - 1)
+
+
+def _span(t: torch.Tensor):
+    first = t.data_ptr()
+    return first, first + t.element_size() * (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())))
+
+
+def _plain(t: torch.Tensor, dtype, dims: int, what: str) -> None:
+    if not t.is_cuda:
+        raise ValueError("the %s must be on the GPU" % what)
+    if t.dtype is not dtype:
+        raise ValueError("the %s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.dim() != dims:
+        raise ValueError("the %s must have %d dimensions, got %d" % (what, dims, t.dim()))
+
+
+def _no_grad(t: torch.Tensor, what: str) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the %s requires a gradient, and the cache computes none" % what)
+
+
+class KVCache:
+    """A paged cache: K and V pools [pages, kv_heads, page_size, head_dim]
+    (bfloat16 or float16, last dimension contiguous, other strides multiples
+    of 8), ``table`` int32 [batch, max_pages] and ``lens`` int32 [batch].  It
+    holds the caller's tensors and allocates nothing; table and lens may be
+    changed between calls."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+        if k_pages.dtype not in _DTYPES:
+            raise ValueError("the pools must be bfloat16 or float16, got %s" % k_pages.dtype)
+        _plain(k_pages, k_pages.dtype, 4, "K pool")
+        _plain(v_pages, k_pages.dtype, 4, "V pool")
+        _plain(table, torch.int32, 2, "page table")
+        _plain(lens, torch.int32, 1, "lengths")
+        if k_pages.shape != v_pages.shape:
+            raise ValueError("the pools differ in shape: %s and %s" % (tuple(k_pages.shape), tuple(v_pages.shape)))
+        if table.shape[0] != lens.shape[0] or not lens.is_contiguous():
+            raise ValueError("one contiguous length per row of the page table")
+        pages, kv_heads, page_size, dim = k_pages.shape
+        if pages < 1 or kv_heads < 1 or page_size < 1:
+            raise ValueError("the pools are empty: %s" % (tuple(k_pages.shape),))
+        if dim % 8 or not 8 <= dim <= 256:
+            raise ValueError("head_dim must be a multiple of 8 in 8..256, got %d" % dim)
+        if table.shape[1] * page_size >= 1 << 31:
+            raise ValueError("a sequence's table reaches 2^31 tokens")
+        for t, what in ((k_pages, "K pool"), (v_pages, "V pool")):
+            _no_overlap(t, what)
+            _no_grad(t, what)
+        _same_gpu(k_pages.device, v_pages, table, lens)
+        self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
+        self.device, self.dtype = k_pages.device, k_pages.dtype
+        self.batch, self.max_pages = table.shape
+        self.kv_heads, self.page_size, self.head_dim = kv_heads, page_size, dim
+        ks, vs = _strides(k_pages, "K pool"), _strides(v_pages, "V pool")
+        self.args = _abi.KVCacheArgs(k_pages.data_ptr(), v_pages.data_ptr(), *ks, *vs, table.data_ptr(),
+                                     max(_strides(table, "page table", 1)[0], self.max_pages), lens.data_ptr(),
+                                     pages, page_size, kv_heads, dim, self.batch, self.max_pages,
+                                     _DTYPES[self.dtype], 0)
+
+    def _call(self, fn: str, stream, *args):
+        with _on(self.device):
+            _abi._check(fn, getattr(_abi, fn)(self.args, *args, _stream(stream, self.device)))
+
+    def _rows(self, k, v, cu, start, written: bool):
+        for t, what in ((k, "K rows"), (v, "V rows")):
+            _device_or_pinned(t, what)
+            if t.dtype is not self.dtype or t.dim() != 3 or tuple(t.shape[1:]) != (self.kv_heads, self.head_dim):
+                raise ValueError("the %s must be %s [rows, %d, %d], got %s %s"
+                                 % (what, self.dtype, self.kv_heads, self.head_dim, t.dtype, tuple(t.shape)))
+            _no_grad(t, what)
+            if written:
+                _no_overlap(t, what)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("K and V must have the same number of rows")
+        _plain(cu, torch.int32, 1, "row ranges")
+        if cu.shape[0] != self.batch + 1 or not cu.is_contiguous():
+            raise ValueError("the row ranges need %d contiguous entries" % (self.batch + 1))
+        if start is not None:
+            _plain(start, torch.int32, 1, "first positions")
+            if start.shape[0] != self.batch or not start.is_contiguous():
+                raise ValueError("one contiguous first position per sequence")
+        _same_gpu(self.device, k, v, cu, start)
+        return _abi.KVRows(k.data_ptr(), v.data_ptr(), *_strides(k, "K rows"), *_strides(v, "V rows"), k.shape[0], 0,
+                           cu.data_ptr(), start.data_ptr() if start is not None else None)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> None:
+        """Write rows ``k`` and ``v`` [rows, kv_heads, head_dim] (device or
+        pinned host memory) into the cache.  Rows cu[b] .. cu[b+1]-1 (``cu``
+        int32 [batch + 1]) go to positions start[b], start[b]+1, ... of
+        sequence b; with ``start`` None they are its last ones: ``lens``
+        counts them already.  Rows behind cu[batch] are not read."""
+        rows = self._rows(k, v, cu, start, False)
+        self._call("splitzip_kv_append", stream, rows, self._status(status))
+
+    def gather(self, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> None:
+        """Copy cached tokens into rows ``k`` and ``v``, placed as in
+        ``append``.  Rows behind cu[batch] are left as they are."""
+        rows = self._rows(k, v, cu, start, True)
+        self._call("splitzip_kv_gather", stream, rows, self._status(status))
+
+    def _status(self, status):
+        _same_gpu(self.device, status)
+        return _status_ptr(status)
+
+    def _mass(self, mass, what: str, written: bool):
+        _plain(mass, torch.float32, 3, what)
+        _same_gpu(self.device, mass)
+        if mass.shape[0] != self.batch or mass.shape[1] != self.kv_heads:
+            raise ValueError("the %s must be [%d, %d, tokens], got %s"
+                             % (what, self.batch, self.kv_heads, tuple(mass.shape)))
+        _no_grad(mass, what)
+        if written:
+            _no_overlap(mass, what)
+        return _strides(mass, what, 1)
+
+    def _mass_pair(self, mass, mass_out):
+        """Pointers, strides and entries of a mass that is read and one that
+        is written (the same one, or one apart from it)."""
+        if mass_out is None:
+            mass_out = mass
+        if mass_out is None:
+            return None, None, (0, 0), (0, 0), 0
+        out_strides = self._mass(mass_out, "mass output", True)
+        if mass is None:
+            return None, mass_out.data_ptr(), (0, 0), out_strides, mass_out.shape[2]
+        strides = out_strides if mass is mass_out else self._mass(mass, "mass", False)
+        if mass.shape[2] != mass_out.shape[2]:
+            raise ValueError("the masses differ in length: %d and %d" % (mass.shape[2], mass_out.shape[2]))
+        (a0, a1), (b0, b1) = _span(mass), _span(mass_out)
+        if a0 < b1 and b0 < a1 and (a0, strides) != (b0, out_strides):
+            raise ValueError("the mass and its output overlap without being the same")
+        return mass.data_ptr(), mass_out.data_ptr(), strides, out_strides, mass.shape[2]
+
+    def attend(self, q: torch.Tensor, ws: "KVWorkspace", out: torch.Tensor | None = None, scale: float | None = None,
+               window: int | None = None, sinks: int = 0, lse: torch.Tensor | None = None,
+               mass: torch.Tensor | None = None, mass_out: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of one new token per sequence, ``q`` [batch, heads,
+        head_dim], over its cached tokens: all, or with ``window`` the last
+        ``window`` and the first ``sinks``.  ``scale`` defaults to
+        head_dim ** -0.5.  Returns ``out``, shaped like q; a sequence with
+        nothing visible gives zeros.
+
+        ``lse`` (float32 [batch, heads]) receives the log of the sum of
+        exponentials.  With ``mass`` (float32 [batch, kv_heads, tokens]) the
+        weight every token received, summed over its KV head's query heads, is
+        added to it: in place, or into ``mass_out``, whose entries up to the
+        length are all written (with ``mass_out`` alone, starting from 0)."""
+        if not q.is_cuda:
+            raise ValueError("the queries must be on the GPU")
+        if q.dtype is not self.dtype or q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != self.head_dim:
+            raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
+                             % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(q.shape)))
+        _no_grad(q, "queries")
+        heads = q.shape[1]
+        if heads < 1 or heads % self.kv_heads:
+            raise ValueError("%d query heads do not divide over %d KV heads" % (heads, self.kv_heads))
+        if window is None:
+            window = _abi.KV_ALL
+        elif not 0 <= window < 1 << 31:
+            raise ValueError("the window must be in 0..2^31-1, got %d" % window)
+        if not 0 <= sinks < 1 << 31:
+            raise ValueError("the sinks must be in 0..2^31-1, got %d" % sinks)
+        if out is None:
+            pass
+        elif not out.is_cuda or out.dtype is not q.dtype or out.shape != q.shape:
+            raise ValueError("the output must be on the GPU and shaped like the queries")
+        else:
+            _no_overlap(out, "output")
+            _no_grad(out, "output")
+        if lse is not None:
+            _plain(lse, torch.float32, 2, "lse")
+            if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))
+        mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
+        _same_gpu(self.device, q, out, lse, ws.buf)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        query = _abi.KVQuery(q.data_ptr(), *_strides(q, "queries"), out.data_ptr(), *_strides(out, "output"),
+                             lse.data_ptr() if lse is not None else None, mass_in, mass_to, *ms, *mos, heads, window,
+                             sinks, self.head_dim ** -0.5 if scale is None else scale, mass_len, 0)
+        self._call("splitzip_kv_attend", stream, query, ws.buf.data_ptr(), ws.nbytes, self._status(status))
+        return out
+
+    def evict(self, mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, to: "KVCache | None" = None,
+              kept: torch.Tensor | None = None, mass_out: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Keep ``budget`` tokens per KV head of every sequence longer than
+        that: the first ``sinks``, the last ``recent`` and those of the
+        largest ``mass`` between them (equal masses: the earlier token), in
+        their order.  In place, or into the pages and lengths of ``to``, which
+        share no memory with this cache; ``lens`` (of ``to``) becomes
+        min(length, budget), and the mass moves along (in place, or into
+        ``mass_out``), 0 behind it.  Returns ``kept``, int32 [batch, kv_heads,
+        budget]: the old position of each kept token, -1 behind them."""
+        if budget < 1 or budget >= 1 << 31 or sinks < 0 or recent < 0 or sinks + recent > budget:
+            raise ValueError("the budget %d must be positive and hold %d sinks and %d recent tokens"
+                             % (budget, sinks, recent))
+        if to is None:
+            to = self
+        elif (to.batch, to.kv_heads, to.head_dim, to.dtype, to.device) != \
+                (self.batch, self.kv_heads, self.head_dim, self.dtype, self.device):
+            raise ValueError("the destination cache differs in batch, heads, dtype or device")
+        if to.max_pages * to.page_size < min(budget, self.max_pages * self.page_size):
+            raise ValueError("the destination's table cannot hold %d tokens" % budget)
+        shape = (self.batch, self.kv_heads, budget)
+        if mass is None:
+            raise ValueError("an eviction needs the mass")
+        if kept is not None:
+            _plain(kept, torch.int32, 3, "kept positions")
+            if tuple(kept.shape) != shape or not kept.is_contiguous():
+                raise ValueError("the kept positions must be contiguous %s" % (shape,))
+        mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
+        _same_gpu(self.device, kept)
+        if kept is None:
+            with torch.cuda.stream(stream):
+                kept = torch.empty(shape, dtype=torch.int32, device=self.device)
+        args = _abi.KVBudget(mass_in, mass_to, *ms, *mos, kept.data_ptr(), budget, sinks, recent, mass_len)
+        self._call("splitzip_kv_evict", stream, to.args, args, self._status(status))
+        return kept
+
+
+class KVWorkspace:
+    """Device scratch for ``KVCache.attend`` on caches shaped like ``cache``
+    with ``heads`` query heads (``mass``: also for calls that ask for the
+    mass).  One workspace per stream that runs such calls concurrently."""
+
+    def __init__(self, cache: KVCache, heads: int, mass: bool = False):
+        mass_len = cache.max_pages * cache.page_size if mass else 0
+        self.nbytes = _abi.splitzip_kv_attend_workspace_size(cache.args, heads, mass_len)
+        if not self.nbytes:
+            raise ValueError("%d query heads do not divide over %d KV heads" % (heads, cache.kv_heads))
+        self.buf = self._buffer(self.nbytes, cache.device)
+
+    def _buffer(self, nbytes: int, device) -> torch.Tensor:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)

@@ -197,3 +197,62 @@ def unpack(entry: dict, blob, out=None, stream=None):
         raise ValueError("stored payload of %s is corrupt (decode status %d)"
                          % (entry.get("name", "?"), bad))
     return res.reshape(shape) if out is None else out
+
+
+def pack_sequence(name: str, cache, b: int, ws, threshold: float = COVERAGE_GATE):
+    """``pack`` the cached K and V of sequence ``b`` of a ``KVCache`` (bfloat16):
+    gathered from their pages as [kv_heads, tokens, head_dim], each with a
+    codebook of its own.  Returns ((K entry, blob), (V entry, blob)), named
+    ``name``.k and ``name``.v; the cache is left as it is.  ``ws`` is a
+    ``Workspace`` for kv_heads * tokens * head_dim elements.  Reads the
+    sequence's length back, so it synchronises with the device."""
+    import torch
+
+    _check_sequence(cache, b)
+    n = min(max(int(cache.lens[b].item()), 0), cache.max_pages * cache.page_size)
+    k, v = (torch.empty(cache.kv_heads, n, cache.head_dim, dtype=cache.dtype, device=cache.device)
+            for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device=cache.device)
+    cache.gather(k.transpose(0, 1), v.transpose(0, 1), _only(cache, b, n), status=status)
+    if int(status.item()):
+        raise ValueError("the table of sequence %d names pages outside the pool" % b)
+    return pack(name + ".k", k, ws, threshold), pack(name + ".v", v, ws, threshold)
+
+
+def unpack_sequence(packed, cache, b: int) -> int:
+    """Rebuild what ``pack_sequence`` returned as the tokens of sequence ``b``
+    of a cache whose table row names enough pages for them; its length is set.
+    Returns the number of tokens."""
+    import torch
+
+    _check_sequence(cache, b)
+    (k_entry, k_blob), (v_entry, v_blob) = packed
+    shape = tuple(k_entry["shape"])
+    if shape != tuple(v_entry["shape"]) or len(shape) != 3 or (shape[0], shape[2]) != (cache.kv_heads, cache.head_dim):
+        raise ValueError("a packed sequence of %s and %s does not fit %d heads of %d"
+                         % (shape, tuple(v_entry["shape"]), cache.kv_heads, cache.head_dim))
+    n = shape[1]
+    if n > cache.max_pages * cache.page_size:
+        raise ValueError("the table holds %d tokens, the packed sequence %d" % (cache.max_pages * cache.page_size, n))
+    k, v = unpack(k_entry, k_blob), unpack(v_entry, v_blob)
+    status = torch.zeros(1, dtype=torch.int32, device=cache.device)
+    start = torch.zeros(cache.batch, dtype=torch.int32, device=cache.device)
+    cache.append(k.transpose(0, 1), v.transpose(0, 1), _only(cache, b, n), start=start, status=status)
+    if int(status.item()):
+        raise ValueError("the table of sequence %d names pages outside the pool" % b)
+    cache.lens[b] = n
+    return n
+
+
+def _check_sequence(cache, b: int) -> None:
+    if not 0 <= b < cache.batch:
+        raise ValueError("sequence %d of a batch of %d" % (b, cache.batch))
+
+
+def _only(cache, b: int, n: int):
+    """Row ranges of which sequence b has n rows and no other has any."""
+    import torch
+
+    cu = torch.zeros(cache.batch + 1, dtype=torch.int32)
+    cu[b + 1:] = n
+    return cu.to(cache.device)

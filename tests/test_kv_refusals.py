@@ -1,0 +1,46 @@
+"""The refusals of the key-value cache's tensor-level calls without a GPU: host
+tensors that say they are on one, and the real library, in which a call that
+is accepted gets as far as the launch (no device: a HIP error) and no further."""
+import contextlib
+
+import pytest
+import torch
+
+import lossless_bf16_tensor_splitzip_amd as S
+from lossless_bf16_tensor_splitzip_amd import _abi, kv
+import kv_checks
+import kv_reference as R
+
+
+class SaysGpu(torch.Tensor):
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda:0"))
+
+    def cpu(self):
+        return torch.Tensor.cpu(self).as_subclass(torch.Tensor)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would launch on host memory")
+@pytest.mark.parametrize("part", ["caches", "rows", "queries", "budgets"])
+def test_refusals(part, monkeypatch):
+    monkeypatch.setattr(kv, "_stream", lambda stream, device: 0)
+    monkeypatch.setattr(kv, "_on", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(S.KVWorkspace, "_buffer", lambda self, nbytes, device: put(torch.empty(nbytes, dtype=torch.uint8)))
+
+    def put(t):
+        return t.as_subclass(SaysGpu)
+
+    def to_gpu(m):
+        m.gk, m.gv, m.gtable = put(m.k.clone()), put(m.v.clone()), put(m.table)
+        m.glens = put(torch.tensor(m.lens, dtype=torch.int32))
+        m.cache = S.KVCache(m.gk, m.gv, m.gtable, m.glens)
+        if hasattr(m, "q"):
+            m.gq = put(m.q)
+        return m
+
+    def runs(fn, *args, **kw):
+        with pytest.raises(S.SplitZipError) as e:
+            fn(*args, **kw)
+        assert e.value.status == _abi.ERR_HIP
+
+    getattr(kv_checks, part)(lambda make, *a, **kw: put(make(*a, **kw)), to_gpu, runs)
