@@ -144,33 +144,464 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
 // ---------------------------------------------------------------------------
 // attend
 // ---------------------------------------------------------------------------
+//
+// Per KV head: logits x = scale q k for its group of query heads, weights
+// p = exp(x - lse), out = sum p v, over the visible tokens, which are numbered
+// 0, 1, ... (the sinks first, then the window).  Each K and V row is read
+// once and meets at most a few dozen query rows, so memory bounds it: the
+// matrix cores do both products, with the operands loaded from memory straight
+// into their registers.
+//
+//   x^T = K q^T    mfma 16x16x32: 16 tokens by 16 query rows.  A lane loads
+//                  8 elements of a K row (16 bytes); it receives 4 tokens'
+//                  logits of one query row.
+//   out^T = V^T p^T  32 tokens a time.  The lane's 8 weights (of two 16-token
+//                  products) are the operand's 8 in the order it has them, so
+//                  no weight moves between lanes; its V operand is those 8
+//                  tokens' values of one column, which it gets from whole
+//                  16-byte pieces of their rows by exchanging halves of words.
+//
+// The work of a launch -- every sequence's tokens in units of kUnit, for every
+// KV head -- is cut into equal runs, one a workgroup, whatever the lengths.  A
+// run that begins or ends inside a KV head's tokens leaves its share (maximum,
+// sum, unnormalised output) in the workspace, and k_join joins the shares.
+
+constexpr int kWaves = 4;
+constexpr int kAttendThreads = 64 * kWaves;
+constexpr uint32_t kTile = 32;                  // tokens a wave takes at a time
+constexpr uint32_t kUnit = kTile * kWaves;      // tokens a workgroup takes at a time
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct AttendArgs {
     Cache c;
     const uint16_t *q;
     uint16_t *out;
     float *lse;
+    uint64_t qs[2], os[2];
+    uint32_t heads, group, window, sinks;
+    uint32_t row_tiles, rows;     // row tiles a group is cut into, query rows a tile
+    float scale2;                 // scale * log2(e): logits in base 2
+    uint32_t runs;                // workgroups of k_attend
+    float *share_o, *share_ml;    // [runs][2] shares of [rows][dim] and [rows][2]
+    float *logits;                // [batch][heads][logit_stride], by visible number (mass only)
+    float *lse2;                  // [batch][heads] (mass only)
+    uint64_t logit_stride;
+    uint32_t logit_len;
     const float *mass;
     float *mass_out;
-    uint64_t qs[2], os[2], ms[2], mos[2];
-    uint32_t heads, group, window, sinks, mass_len;
-    float scale;
-    float *weights;
+    uint64_t ms[2], mos[2];
+    uint32_t mass_len;
     int32_t *status;
 };
 
-template <bool BF16>
-__device__ inline float to_float(uint16_t x) {
-    if (BF16) return __uint_as_float((uint32_t)x << 16);
-    return (float)__builtin_bit_cast(_Float16, x);
-}
-template <bool BF16>
-__device__ inline uint16_t from_float(float x) {
-    if (BF16) return __builtin_bit_cast(uint16_t, (__bf16)x);
-    return __builtin_bit_cast(uint16_t, (_Float16)x);
+struct Seen {
+    uint32_t sinks, shift, count;    // token of visible number v: v < sinks ? v : v + shift
+};
+
+__device__ inline Seen seen_of(uint32_t n, uint32_t window, uint32_t sinks) {
+    const uint32_t first = window >= n ? 0 : n - window;
+    const uint32_t s = min(sinks, first);
+    return Seen{s, first - s, s + (n - first)};
 }
 
-constexpr int kAttendThreads = 256;
+__device__ inline uint32_t units_of(uint32_t n, uint32_t window, uint32_t sinks) {
+    const uint32_t seen = seen_of(n, window, sinks).count;
+    return seen ? (seen - 1) / kUnit + 1 : 1;    // an empty sequence's outputs are one unit's work
+}
+
+// The sequences in blocks of 64, one a lane: lengths and running sums of units.
+struct Block64 {
+    uint32_t first, len, before, upto;     // first sequence; the lane's length, units before and with it
+    uint32_t total;                        // units with the block's last
+};
+
+__device__ inline void load_block(const AttendArgs &a, uint32_t first, uint32_t carry, Block64 &k,
+                                  int32_t *status) {
+    const uint32_t lane = threadIdx.x & 63, b = first + lane;
+    k.first = first;
+    k.len = b < a.c.batch ? seq_len(a.c, b, status) : 0;
+    const uint32_t units = b < a.c.batch ? units_of(k.len, a.window, a.sinks) : 0;
+    const uint32_t n = min(64u, a.c.batch - first);
+    uint32_t sum = units;
+    for (uint32_t d = 1; d < n; d <<= 1) {
+        const uint32_t y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+    }
+    k.before = carry + sum - units;
+    k.upto = carry + sum;
+    k.total = __builtin_amdgcn_readlane(k.upto, n - 1);
+}
+
+// Units of a launch, and how they are cut into runs: the first `extra` runs
+// have size + 1 of them, the others size.
+struct Cut {
+    uint32_t units, runs, size, extra;
+    __device__ uint32_t begin(uint32_t run) const { return run * size + min(run, extra); }
+    __device__ uint32_t owner(uint32_t u) const {
+        const uint32_t big = extra * (size + 1);
+        return u < big ? u / (size + 1) : extra + (u - big) / size;
+    }
+};
+
+__device__ inline Cut cut_of(uint32_t units, uint32_t runs) {
+    Cut c;
+    c.units = units;
+    c.runs = min(units, runs);
+    c.size = units / c.runs;
+    c.extra = units - c.size * c.runs;
+    return c;
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <bool BF16>
+__device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <bool BF16>
+__device__ inline uint32_t pack2(float x, float y) {
+    if constexpr (BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
+    else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)x, (_Float16)y});
+}
+
+template <bool BF16>
+__device__ inline void unpack2(uint32_t w, float &x, float &y) {
+    if constexpr (BF16) {
+        x = __uint_as_float(w << 16);
+        y = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        x = (float)h[0];
+        y = (float)h[1];
+    }
+}
+
+// Over the four lanes that hold a query row's tokens (16 apart).
+template <bool MAX>
+__device__ inline float row_reduce(float x) {
+    const u32x2 a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    const float y0 = __uint_as_float(a[0]), y1 = __uint_as_float(a[1]);
+    x = MAX ? fmaxf(y0, y1) : y0 + y1;
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    const float z0 = __uint_as_float(b[0]), z1 = __uint_as_float(b[1]);
+    return MAX ? fmaxf(z0, z1) : z0 + z1;
+}
+
+// DP: head_dim rounded up to a multiple of 64.  NT: blocks of 16 query rows a
+// workgroup takes.  EXACT: head_dim is DP.
+template <bool BF16, int DP, int NT, bool EXACT>
+__global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
+    constexpr int KS = DP / 32;             // steps of the K product
+    constexpr int P16 = DP / 128;           // 16-byte pieces of a V row a lane takes: columns 128 i + 8 (lane % 16)
+    constexpr int P8 = (DP % 128) / 64;     // and an 8-byte one: 128 P16 + 4 (lane % 16)
+    constexpr int VW = 4 * P16 + 2 * P8;    // words of them
+    constexpr int VC = 2 * VW;              // columns
+    constexpr int LD = DP + 4;
+    // fp16 weights are held times 2^15: their smallest normal step then lies 2^-29
+    // below the largest weight instead of 2^-14.
+    constexpr float kLift = BF16 ? 0.f : 15.f;
+    __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
+    __shared__ float s_o[kWaves][16][LD];
+    __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t D = EXACT ? DP : a.c.dim;
+    const uint32_t pairs = a.c.kv_heads * a.row_tiles;     // of a sequence
+
+    // this workgroup's run of units
+    Block64 blk;
+    int32_t *status0 = blockIdx.x == 0 && wave == 0 ? a.status : nullptr;
+    load_block(a, 0, 0, blk, status0);
+    uint32_t total = blk.total;
+    for (uint32_t f = 64; f < a.c.batch; f += 64) {
+        Block64 k;
+        load_block(a, f, total, k, status0);
+        total = k.total;
+    }
+    const Cut cut = cut_of(total * pairs, a.runs);
+    if (blockIdx.x >= cut.runs) return;
+    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = cut.begin(blockIdx.x + 1);
+    while (blk.total * pairs <= u_begin) load_block(a, blk.first + 64, blk.total, blk, nullptr);
+    uint32_t at = (uint32_t)__builtin_ctzll(__ballot(blk.upto * pairs > u_begin));    // the sequence's lane
+
+    for (uint32_t u = u_begin; u < u_end;) {
+        while (at >= 64) {
+            load_block(a, blk.first + 64, blk.total, blk, nullptr);
+            at -= 64;
+        }
+        const uint32_t b = blk.first + at;
+        const uint32_t n = __builtin_amdgcn_readlane(blk.len, at), before = __builtin_amdgcn_readlane(blk.before, at);
+        const uint32_t units = __builtin_amdgcn_readlane(blk.upto, at) - before;
+        const uint32_t rel = u - before * pairs, pair = rel / units, unit0 = rel - pair * units;
+        const uint32_t count = min(units - unit0, u_end - u);
+        const bool whole = count == units;
+        const uint32_t h = pair / a.row_tiles, row0 = (pair - h * a.row_tiles) * a.rows;     // rows of the group
+        const uint32_t rows = min(a.rows, a.group - row0), head0 = h * a.group + row0;
+        const Seen seen = seen_of(n, a.window, a.sinks);
+        const uint32_t v_end = min(seen.count, (unit0 + count) * kUnit);
+        const int32_t *table = a.c.table + b * a.c.table_stride;
+
+        u32x4 q[NT][KS];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                q[t][j] = u32x4{0, 0, 0, 0};
+                const uint32_t d = j * 32 + g * 8;
+                if (t * 16 + c16 < rows && (EXACT || d < D))
+                    q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + t * 16 + c16) * a.qs[1] + d);
+            }
+        f32x4 o[NT][VC];
+        float m[NT], l[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            m[t] = -INFINITY;
+            l[t] = 0.f;
+#pragma unroll
+            for (int j = 0; j < VC; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        // Bases of this lane's pieces; columns behind head_dim (EXACT false)
+        // are read from column 0 and stay unused.
+        const uint16_t *k_lane[EXACT ? 1 : KS], *v_lane[P16 + P8];
+        const uint16_t *k_head = a.c.k + h * a.c.ks[1], *v_head = a.c.v + h * a.c.vs[1];
+#pragma unroll
+        for (int j = 0; j < (EXACT ? 1 : KS); ++j) {
+            const uint32_t d = j * 32 + g * 8;
+            k_lane[j] = k_head + (EXACT || d < D ? d : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < P16 + P8; ++i) {
+            const uint32_t d = i < P16 ? i * 128 + c16 * 8 : P16 * 128 + c16 * 4;
+            v_lane[i] = v_head + (EXACT || d < D ? d : 0);
+        }
+
+        // The page number of lane t's token of the wave's tile at v0 (lanes
+        // 32.. repeat 0..31), and from it the places of K and V.
+        auto token = [&](uint32_t v) { return v < seen.sinks ? v : v + seen.shift; };
+        auto page_of = [&](uint32_t v0) {
+            const uint32_t v = v0 + (lane & 31);
+            return v < v_end ? (uint32_t)table[div(token(v), a.c.page)] : 0xffffffffu;
+        };
+        auto place = [&](uint32_t v0, uint32_t page, int buf) {
+            const uint32_t v = v0 + (lane & 31), t = token(v);
+            const bool in = v < v_end, ok = in && page < a.c.num_pages;
+            if (in && !ok) report(a.status, SPLITZIP_KV_BAD_PAGE);
+            const uint32_t p = ok ? page : 0, slot = ok ? t - div(t, a.c.page) * a.c.page.d : 0;
+            if (lane < 32) {
+                off_k[wave][buf][lane] = p * a.c.ks[0] + slot * a.c.ks[2];
+                off_v[wave][buf][lane] = p * a.c.vs[0] + slot * a.c.vs[2];
+            }
+            __builtin_amdgcn_wave_barrier();      // the wave's own LDS: in order without a wait
+            return (uint32_t)__ballot(ok);
+        };
+        u32x4 kr[2][KS];
+        u32x4 v16[8][P16 ? P16 : 1];
+        u32x2 v8[8];
+        auto word = [&](int i, int w) { return w < 4 * P16 ? v16[i][w / 4][w % 4] : v8[i][w - 4 * P16]; };
+        auto load_k = [&](int buf) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint64_t off = off_k[wave][buf][s * 16 + c16];
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+                    kr[s][j] = *(const u32x4 *)(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
+            }
+        };
+        auto load_v = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t off = off_v[wave][buf][(i >> 2) * 16 + g * 4 + (i & 3)];
+#pragma unroll
+                for (int p = 0; p < P16; ++p) v16[i][p] = *(const u32x4 *)(v_lane[p] + off);
+                if (P8) v8[i] = *(const u32x2 *)(v_lane[P16] + off);
+            }
+        };
+
+        uint32_t v0 = unit0 * kUnit + wave * kTile;
+        uint32_t page = 0xffffffffu, valid = 0, valid_next = 0;
+        int buf = 0;
+        if (v0 < v_end) {
+            page = page_of(v0);
+            valid = place(v0, page, 0);
+            load_k(0);
+            load_v(0);
+            page = page_of(v0 + kUnit);
+        }
+        for (; v0 < v_end; v0 += kUnit) {
+            const bool more = v0 + kUnit < v_end;
+            if (more) {
+                valid_next = place(v0 + kUnit, page, buf ^ 1);
+                page = page_of(v0 + 2 * kUnit);
+            }
+            if (!EXACT) {
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+                    if (j * 32 + g * 8 >= D) kr[0][j] = kr[1][j] = u32x4{0, 0, 0, 0};
+            }
+            f32x4 x[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    x[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) x[t][s] = mfma<BF16>(kr[s][j], q[t][j], x[t][s]);
+                }
+            if (more) load_k(buf ^ 1);
+
+            u32x4 hi[NT], lo[NT];
+            const uint32_t mine = (valid >> (g * 4) & 15u) | (valid >> (16 + g * 4) & 15u) << 4;     // of its 8 tokens
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float y[8], top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = x[t][i >> 2][i & 3] * a.scale2;
+                    if (valid != 0xffffffffu && !(mine >> i & 1)) y[i] = -INFINITY;
+                    top = fmaxf(top, y[i]);
+                }
+                if (a.logits && t * 16 + c16 < rows) {
+                    float *to = a.logits + (b * (uint64_t)a.heads + head0 + t * 16 + c16) * a.logit_stride;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t v = v0 + s * 16 + g * 4;
+                        if (v < a.logit_len) *(f32x4 *)(to + v) = f32x4{y[4 * s], y[4 * s + 1], y[4 * s + 2], y[4 * s + 3]};
+                    }
+                }
+                const float m_new = fmaxf(m[t], row_reduce<true>(top) - kLift);
+                const float use = m_new == -INFINITY ? 0.f : m_new;
+                if (__any(m_new > m[t])) {
+                    const float r = __builtin_amdgcn_exp2f(m[t] - use);
+                    l[t] *= r;
+#pragma unroll
+                    for (int j = 0; j < VC; ++j) o[t][j] *= r;
+                    m[t] = m_new;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    // The weight as a sum of two 16-bit numbers: one alone would
+                    // add an error as large as the output's own rounding.
+                    const float p0 = __builtin_amdgcn_exp2f(y[i] - use), p1 = __builtin_amdgcn_exp2f(y[i + 1] - use);
+                    l[t] += p0 + p1;
+                    float r0, r1;
+                    hi[t][i / 2] = pack2<BF16>(p0, p1);
+                    unpack2<BF16>(hi[t][i / 2], r0, r1);
+                    lo[t][i / 2] = pack2<BF16>(p0 - r0, p1 - r1);
+                }
+            }
+            if (valid != 0xffffffffu) {
+                // weight 0 does not silence an infinity or a NaN
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(mine >> i & 1)) {
+#pragma unroll
+                        for (int p = 0; p < P16; ++p) v16[i][p] = u32x4{0, 0, 0, 0};
+                        if (P8) v8[i] = u32x2{0, 0};
+                    }
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    u32x4 col;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        col[i] = __builtin_amdgcn_perm(word(2 * i + 1, w), word(2 * i, w), odd ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        o[t][2 * w + odd] = mfma<BF16>(col, hi[t], o[t][2 * w + odd]);
+                        o[t][2 * w + odd] = mfma<BF16>(col, lo[t], o[t][2 * w + odd]);
+                    }
+                }
+            if (more) load_v(buf ^ 1);
+            buf ^= 1;
+            valid = valid_next;
+        }
+
+        // The waves' shares joined: common maximum, rescaled sums.
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            l[t] = row_reduce<false>(l[t]);
+            if (lane < 16) {
+                s_m[wave][t * 16 + lane] = m[t];
+                s_l[wave][t * 16 + lane] = l[t];
+            }
+        }
+        __syncthreads();
+        const uint32_t slot = blockIdx.x * 2 + (u != u_begin);
+        for (int t = 0; t < NT && t * 16 < (int)rows; ++t) {
+            float top = s_m[0][t * 16 + c16];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_m[w][t * 16 + c16]);
+            // o[t] is indexed by a constant: one of the NT blocks is taken
+            float r = 0.f;
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+                if (tt == t) {
+                    r = m[tt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[tt] - top);
+#pragma unroll
+                    for (int p = 0; p < P16 + P8; ++p) {
+                        const int wide = p < P16 ? 8 : 4;      // columns of the piece
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < wide; j += 4) {
+                                const int at_col = p * 8 + j;
+                                f32x4 y;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) y[e] = o[tt][at_col + e][i] * r;
+                                *(f32x4 *)&s_o[wave][c16][p * 128 + (g * 4 + i) * wide + j] = y;
+                            }
+                    }
+                }
+            __syncthreads();
+            for (uint32_t item = tid; item < 16 * (DP / 4); item += kAttendThreads) {
+                const uint32_t row = item / (DP / 4), d = item % (DP / 4) * 4, gr = t * 16 + row;
+                if (gr >= rows || d >= D) continue;
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) M = fmaxf(M, s_m[w][gr]);
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) L += s_m[w][gr] == -INFINITY ? s_l[w][gr] : s_l[w][gr] * __builtin_amdgcn_exp2f(s_m[w][gr] - M);
+                f32x4 y = *(const f32x4 *)&s_o[0][row][d];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) y += *(const f32x4 *)&s_o[w][row][d];
+                if (whole) {
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
+                    *(u32x2 *)(a.out + b * a.os[0] + (head0 + gr) * a.os[1] + d) = z;
+                    if (d == 0) {
+                        const float e = L == 0.f ? -INFINITY : M + log2f(L);
+                        if (a.lse) a.lse[b * (uint64_t)a.heads + head0 + gr] = e * kLn2;
+                        if (a.lse2) a.lse2[b * (uint64_t)a.heads + head0 + gr] = e;
+                    }
+                } else {
+                    *(f32x4 *)(a.share_o + ((uint64_t)slot * a.rows + gr) * D + d) = y;
+                    if (d == 0) {
+                        a.share_ml[((uint64_t)slot * a.rows + gr) * 2] = M;
+                        a.share_ml[((uint64_t)slot * a.rows + gr) * 2 + 1] = L;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        u += count;
+        if (pair == pairs - 1 && unit0 + count == units) ++at;
+    }
+}
+
+constexpr int kJoinThreads = 256;
 
 template <bool MAX>
 __device__ inline float block_reduce(float x, float *part) {
@@ -182,82 +613,102 @@ __device__ inline float block_reduce(float x, float *part) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
     __syncthreads();
     x = part[0];
-    for (int w = 1; w < kAttendThreads / 64; ++w) x = MAX ? fmaxf(x, part[w]) : x + part[w];
+    for (int w = 1; w < kJoinThreads / 64; ++w) x = MAX ? fmaxf(x, part[w]) : x + part[w];
     return x;
 }
+constexpr uint32_t kMaxRuns = 2048;
 
-// One workgroup per sequence and KV head, the group's query heads one after
-// another: a thread takes a token's logit, then an element of the output.
+// One workgroup per query head of a sequence: nothing to do where one run
+// held all of its tokens; else the runs' shares, rescaled to their common
+// maximum.
 template <bool BF16>
-__global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
-    __shared__ float q[SPLITZIP_KV_MAX_DIM], p[kAttendThreads], part[kAttendThreads / 64];
-    __shared__ uint64_t at[kAttendThreads];
-    const uint32_t b = blockIdx.x, h = blockIdx.y, D = a.c.dim;
-    const uint32_t n = seq_len(a.c, b, threadIdx.x == 0 && h == 0 ? a.status : nullptr);
-    const uint32_t first = a.window >= n ? 0 : n - a.window;
-    const uint32_t s = min(a.sinks, first), seen = s + (n - first);
-    for (uint32_t g = 0; g < a.group; ++g) {
-        const uint32_t head = h * a.group + g;
-        __syncthreads();
-        for (uint32_t d = threadIdx.x; d < D; d += kAttendThreads)
-            q[d] = to_float<BF16>(a.q[b * a.qs[0] + head * a.qs[1] + d]);
-        __syncthreads();
-        auto logit = [&](uint32_t i, uint64_t &v_at) {
-            if (i >= seen) return -INFINITY;
-            const uint32_t t = i < s ? i : first + (i - s);
-            uint32_t page, slot;
-            if (!locate(a.c, b, t, page, slot)) {
-                report(a.status, SPLITZIP_KV_BAD_PAGE);
-                return -INFINITY;
+__global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
+    __shared__ float s_w[kMaxRuns], s_part[kJoinThreads / 64];
+    __shared__ f32x4 s_o[kJoinThreads];
+    const uint32_t tid = threadIdx.x, b = blockIdx.y, head = blockIdx.x;
+    const uint32_t pairs = a.c.kv_heads * a.row_tiles;
+    // units before the sequence, its own, and all
+    uint32_t before = 0, units = 0, total = 0;
+    for (uint32_t f = 0; f < a.c.batch; f += 64) {
+        Block64 k;
+        load_block(a, f, total, k, nullptr);
+        if (b >= f && b < f + 64) {
+            before = __builtin_amdgcn_readlane(k.before, b - f);
+            units = __builtin_amdgcn_readlane(k.upto, b - f) - before;
+        }
+        total = k.total;
+    }
+    const Cut cut = cut_of(total * pairs, a.runs);
+    const uint32_t h = head / a.group, in_group = head - h * a.group, tile = in_group / a.rows, row = in_group - tile * a.rows;
+    const uint32_t u0 = before * pairs + (h * a.row_tiles + tile) * units;
+    const uint32_t first = cut.owner(u0), last = cut.owner(u0 + units - 1);
+    if (first == last) return;
+    const uint32_t n = last - first + 1;
+    auto slot = [&](uint32_t j) { return (uint64_t)(first + j) * 2 + (j == 0 && cut.begin(first) != u0); };
+    float top = -INFINITY;
+    for (uint32_t j = tid; j < n; j += kJoinThreads) {
+        const float m = a.share_ml[(slot(j) * a.rows + row) * 2];
+        s_w[j] = m;
+        top = fmaxf(top, m);
+    }
+    top = block_reduce<true>(top, s_part);
+    float sum = 0.f;
+    for (uint32_t j = tid; j < n; j += kJoinThreads) {
+        const float l = a.share_ml[(slot(j) * a.rows + row) * 2 + 1];
+        const float w = s_w[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_w[j] - top);
+        s_w[j] = w;
+        sum += s_w[j] == 0.f && l == l ? 0.f : l * w;
+    }
+    sum = block_reduce<false>(sum, s_part);
+    const uint32_t pieces = a.c.dim / 4;                // 4-column pieces of a row
+    const uint32_t ways = kJoinThreads / pieces;        // shares summed side by side
+    f32x4 y{0.f, 0.f, 0.f, 0.f};
+    const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
+    if (way < ways) {
+#pragma unroll 8
+        for (uint32_t j = way; j < n; j += ways)
+            y += *(const f32x4 *)(a.share_o + (slot(j) * a.rows + row) * a.c.dim + d) * s_w[j];
+    }
+    s_o[tid] = y;
+    __syncthreads();
+    if (tid < pieces) {
+        for (uint32_t w = 1; w < ways; ++w) y += s_o[w * pieces + tid];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
+        *(u32x2 *)(a.out + b * a.os[0] + head * a.os[1] + d) = z;
+        if (tid == 0) {
+            const float e = sum == 0.f ? -INFINITY : top + log2f(sum);
+            if (a.lse) a.lse[b * (uint64_t)a.heads + head] = e * kLn2;
+            if (a.lse2) a.lse2[b * (uint64_t)a.heads + head] = e;
+        }
+    }
+}
+
+constexpr int kMassThreads = 256;
+
+// mass_out = mass + the group's weights, four tokens a thread.
+__global__ __launch_bounds__(kMassThreads) void k_mass(AttendArgs a) {
+    const uint32_t h = blockIdx.y, b = blockIdx.z;
+    uint32_t n = seq_len(a.c, b);
+    const Seen seen = seen_of(n, a.window, a.sinks);
+    if (n > a.mass_len) {
+        if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) report(a.status, SPLITZIP_KV_BAD_LEN);
+        n = a.mass_len;
+    }
+    const float *in = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
+    float *out = a.mass_out + b * a.mos[0] + h * a.mos[1];
+    const float *x = a.logits + (b * (uint64_t)a.heads + h * a.group) * a.logit_stride;
+    const float *lse2 = a.lse2 + b * (uint64_t)a.heads + h * a.group;
+    for (uint64_t t = blockIdx.x * kMassThreads + threadIdx.x; t < n; t += (uint64_t)gridDim.x * kMassThreads) {
+        float w = 0.f;
+        if (t < seen.sinks || t >= (uint64_t)seen.sinks + seen.shift) {
+            const uint64_t v = t < seen.sinks ? t : t - seen.shift;
+            for (uint32_t i = 0; i < a.group; ++i) {
+                const float e = lse2[i];
+                w += e == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x[i * a.logit_stride + v] - e);
             }
-            const uint16_t *k = a.c.k + page * a.c.ks[0] + h * a.c.ks[1] + slot * a.c.ks[2];
-            v_at = page * a.c.vs[0] + h * a.c.vs[1] + slot * a.c.vs[2];
-            float x = 0.f;
-            for (uint32_t d = 0; d < D; ++d) x = fmaf(q[d], to_float<BF16>(k[d]), x);
-            return x * a.scale;
-        };
-        float m = -INFINITY, l = 0.f, o = 0.f;
-        for (uint32_t i0 = 0; i0 < seen; i0 += kAttendThreads) {
-            uint64_t v_at = ~0ull;
-            const float x = logit(i0 + threadIdx.x, v_at);
-            const float m1 = fmaxf(m, block_reduce<true>(x, part));
-            const float e = v_at == ~0ull || m1 == -INFINITY ? 0.f : expf(x - m1);
-            const float r = m == -INFINITY ? 0.f : expf(m - m1);
-            l = l * r + block_reduce<false>(e, part);
-            __syncthreads();
-            p[threadIdx.x] = e;
-            at[threadIdx.x] = v_at;
-            __syncthreads();
-            o *= r;
-            if (threadIdx.x < D)
-                for (uint32_t j = 0; j < kAttendThreads; ++j)
-                    if (at[j] != ~0ull) o = fmaf(p[j], to_float<BF16>(a.c.v[at[j] + threadIdx.x]), o);
-            m = m1;
         }
-        const float lse = l == 0.f ? -INFINITY : m + logf(l);   // NaN stays NaN
-        if (threadIdx.x < D)
-            a.out[b * a.os[0] + head * a.os[1] + threadIdx.x] = from_float<BF16>(l == 0.f ? 0.f : o / l);
-        if (a.lse && threadIdx.x == 0) a.lse[b * (uint64_t)a.heads + head] = lse;
-        if (!a.mass_out) continue;
-        const uint32_t nm = min(n, a.mass_len);
-        if (n > a.mass_len && g == 0 && h == 0 && threadIdx.x == 0) report(a.status, SPLITZIP_KV_BAD_LEN);
-        // the weights are summed over the group first, then added to the mass
-        float *w = a.weights + ((uint64_t)b * a.c.kv_heads + h) * min(a.mass_len, a.c.max_len);
-        if (g == 0)
-            for (uint32_t t = threadIdx.x; t < nm; t += kAttendThreads) w[t] = 0.f;
-        __syncthreads();
-        for (uint32_t i0 = 0; i0 < seen; i0 += kAttendThreads) {
-            uint64_t v_at = ~0ull;
-            const uint32_t i = i0 + threadIdx.x;
-            const float x = logit(i, v_at);
-            const uint32_t t = i < s ? i : first + (i - s);
-            if (v_at != ~0ull && l != 0.f && t < nm) w[t] += expf(x - lse);
-        }
-        __syncthreads();
-        if (g + 1 < a.group) continue;
-        const float *mi = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
-        float *mo = a.mass_out + b * a.mos[0] + h * a.mos[1];
-        for (uint32_t t = threadIdx.x; t < nm; t += kAttendThreads) mo[t] = (mi ? mi[t] : 0.f) + w[t];
+        out[t] = (in ? in[t] : 0.f) + w;
     }
 }
 
@@ -569,6 +1020,62 @@ int copy_rows(const splitzip_kv_cache *cache, const splitzip_kv_rows *r, int32_t
     return launched();
 }
 
+// How an attention is laid out: query rows a workgroup, runs, workspace.
+struct AttendPlan {
+    uint32_t group, row_tiles, rows, blocks, runs;
+    uint64_t logit_stride;
+    size_t ml_at, lse2_at, logits_at, bytes;
+};
+
+constexpr uint32_t kRuns = 768;      // three workgroups on each of 256 compute units
+static_assert(kRuns <= kMaxRuns, "the join holds one weight per run");
+
+inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, AttendPlan &p) {
+    if (heads == 0 || heads > SPLITZIP_KV_MAX_HEADS || heads % c->kv_heads) return false;
+    p.group = heads / c->kv_heads;
+    p.row_tiles = (p.group - 1) / 32 + 1;
+    p.rows = (p.group - 1) / p.row_tiles + 1;
+    p.row_tiles = (p.group - 1) / p.rows + 1;
+    p.blocks = p.rows > 16 ? 2 : 1;
+    const uint32_t all = c->max_pages * c->page_size;
+    const uint64_t units = (uint64_t)(all ? (all - 1) / kUnit + 1 : 1) * c->batch * c->kv_heads * p.row_tiles;
+    if (units >> 31) return false;
+    p.runs = units < kRuns ? (uint32_t)units : kRuns;
+    if (mass_len > all) mass_len = all;      // no sequence is longer
+    p.logit_stride = ((uint64_t)mass_len + 3) & ~3ull;
+    if ((double)p.logit_stride * c->batch * heads > 1e15) return false;
+    p.ml_at = up16((size_t)p.runs * 2 * p.rows * c->head_dim * 4);
+    p.lse2_at = up16(p.ml_at + (size_t)p.runs * 2 * p.rows * 8);
+    p.logits_at = up16(p.lse2_at + (p.logit_stride ? (size_t)c->batch * heads * 4 : 0));
+    p.bytes = p.logits_at + 4 * p.logit_stride * c->batch * heads;
+    if (p.bytes < 16) p.bytes = 16;
+    return true;
+}
+
+template <bool BF16, int DP, int NT>
+void launch_attend(const AttendArgs &a, hipStream_t s) {
+    if (a.c.dim == DP) k_attend<BF16, DP, NT, true><<<a.runs, kAttendThreads, 0, s>>>(a);
+    else k_attend<BF16, DP, NT, false><<<a.runs, kAttendThreads, 0, s>>>(a);
+}
+
+template <bool BF16>
+void launch_attend(const AttendArgs &a, uint32_t blocks, hipStream_t s) {
+    const uint32_t d = (a.c.dim + 63) / 64;
+    if (blocks == 1) {
+        if (d == 1) launch_attend<BF16, 64, 1>(a, s);
+        else if (d == 2) launch_attend<BF16, 128, 1>(a, s);
+        else if (d == 3) launch_attend<BF16, 192, 1>(a, s);
+        else launch_attend<BF16, 256, 1>(a, s);
+    } else {
+        if (d == 1) launch_attend<BF16, 64, 2>(a, s);
+        else if (d == 2) launch_attend<BF16, 128, 2>(a, s);
+        else if (d == 3) launch_attend<BF16, 192, 2>(a, s);
+        else launch_attend<BF16, 256, 2>(a, s);
+    }
+}
+
 bool mass_strides_ok(const uint64_t s[2]) { return s[0] <= kMaxOffset / 65536 && s[1] <= kMaxOffset / 65536; }
 
 }  // namespace
@@ -593,20 +1100,18 @@ int splitzip_kv_gather(const splitzip_kv_cache *cache, const splitzip_kv_rows *r
 }
 
 size_t splitzip_kv_attend_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t mass_len) {
-    if (!shape_ok(cache) || heads == 0 || heads > SPLITZIP_KV_MAX_HEADS || heads % cache->kv_heads) return 0;
-    const uint32_t all = cache->max_pages * cache->page_size;
-    if (mass_len > all) mass_len = all;      // no sequence is longer
-    const double logits = 4.0 * cache->batch * heads * mass_len;
-    if (logits > 1e15) return 0;
-    return 16 + 4ull * cache->batch * heads * mass_len;
+    AttendPlan p;
+    if (!shape_ok(cache) || !attend_plan(cache, heads, mass_len, p)) return 0;
+    return p.bytes;
 }
 
 int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *query, void *d_ws,
                        size_t ws_bytes, int32_t *d_status, void *stream) {
     if (!cache_ok(cache) || !query || (d_status && !aligned(d_status, 4))) return SPLITZIP_ERR_INVALID;
     const splitzip_kv_query &Q = *query;
-    const size_t need = splitzip_kv_attend_workspace_size(cache, Q.heads, Q.mass_out ? Q.mass_len : 0);
-    if (!need || !(Q.scale - Q.scale == 0.f)) return SPLITZIP_ERR_INVALID;
+    AttendPlan P;
+    if (!attend_plan(cache, Q.heads, Q.mass_out ? Q.mass_len : 0, P) || !(Q.scale - Q.scale == 0.f))
+        return SPLITZIP_ERR_INVALID;      // also a scale that is not finite
     for (int i = 0; i < 2; ++i)
         if (Q.q_stride[i] % 8 || Q.out_stride[i] % 8 || Q.q_stride[i] > kMaxOffset / 65536 || Q.out_stride[i] > kMaxOffset / 65536)
             return SPLITZIP_ERR_INVALID;
@@ -616,7 +1121,7 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     if (cache->batch == 0) return SPLITZIP_OK;
     if (!Q.q || !Q.out || !aligned(Q.q, 16) || !aligned(Q.out, 16) || !d_ws || !aligned(d_ws, 16))
         return SPLITZIP_ERR_INVALID;
-    if (ws_bytes < need) return SPLITZIP_ERR_WORKSPACE;
+    if (ws_bytes < P.bytes) return SPLITZIP_ERR_WORKSPACE;
     AttendArgs a{};
     a.c = view(cache);
     a.q = Q.q;
@@ -631,18 +1136,48 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
         a.mos[i] = Q.mass_out_stride[i];
     }
     a.heads = Q.heads;
-    a.group = Q.heads / cache->kv_heads;
+    a.group = P.group;
+    a.row_tiles = P.row_tiles;
+    a.rows = P.rows;
     a.window = Q.window;
     a.sinks = Q.sinks;
-    a.scale = Q.scale;
+    a.scale2 = Q.scale * kLog2e;
     a.mass_len = Q.mass_len;
-    a.weights = reinterpret_cast<float *>(d_ws);
     a.status = d_status;
+    uint8_t *ws = reinterpret_cast<uint8_t *>(d_ws);
+    a.share_o = reinterpret_cast<float *>(ws);
+    a.share_ml = reinterpret_cast<float *>(ws + P.ml_at);
+    if (Q.mass_out && P.logit_stride) {
+        a.lse2 = reinterpret_cast<float *>(ws + P.lse2_at);
+        a.logits = reinterpret_cast<float *>(ws + P.logits_at);
+        a.logit_stride = P.logit_stride;
+        a.logit_len = (uint32_t)P.logit_stride;
+    }
+    // no sequence sees more than this
+    const uint64_t window = (uint64_t)Q.window + Q.sinks;
+    const uint64_t seen = Q.window == SPLITZIP_KV_ALL || window > a.c.max_len ? a.c.max_len : window;
+    const uint32_t units = seen ? (uint32_t)((seen - 1) / kUnit + 1) : 1;
+    const uint64_t most = (uint64_t)units * cache->batch * cache->kv_heads * P.row_tiles;
+    a.runs = most < P.runs ? (uint32_t)most : P.runs;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const dim3 grid(cache->batch, cache->kv_heads);
-    if (cache->dtype == SPLITZIP_KV_BF16) k_attend<true><<<grid, kAttendThreads, 0, s>>>(a);
-    else k_attend<false><<<grid, kAttendThreads, 0, s>>>(a);
-    return launched();
+    const bool bf16 = cache->dtype == SPLITZIP_KV_BF16;
+    if (bf16) launch_attend<true>(a, P.blocks, s);
+    else launch_attend<false>(a, P.blocks, s);
+    int rc = launched();
+    if (rc) return rc;
+    if (units > 1) {      // else every KV head is one run's
+        const dim3 grid(Q.heads, cache->batch);
+        if (bf16) k_join<true><<<grid, kJoinThreads, 0, s>>>(a);
+        else k_join<false><<<grid, kJoinThreads, 0, s>>>(a);
+        rc = launched();
+        if (rc) return rc;
+    }
+    if (a.logits) {
+        const uint32_t parts = (uint32_t)((P.logit_stride - 1) / kMassThreads + 1);
+        k_mass<<<dim3(parts < 65536 ? parts : 65536, cache->kv_heads, cache->batch), kMassThreads, 0, s>>>(a);
+        rc = launched();
+    }
+    return rc;
 }
 
 int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *to,
