@@ -209,6 +209,18 @@ __device__ inline uint32_t units_of(uint32_t n, uint32_t window, uint32_t sinks)
     return seen ? (seen - 1) / kUnit + 1 : 1;    // an empty sequence's outputs are one unit's work
 }
 
+// Running sum over the wave's lanes: within rows of 16 by shifts, then the
+// rows before.
+__device__ inline uint32_t wave_scan(uint32_t x) {
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, false);    // row_shr:1
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, false);    // row_shr:2
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, false);    // row_shr:4
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, false);    // row_shr:8
+    const uint32_t r0 = __builtin_amdgcn_readlane(x, 15), r1 = __builtin_amdgcn_readlane(x, 31),
+                   r2 = __builtin_amdgcn_readlane(x, 47), row = (threadIdx.x & 63) >> 4;
+    return x + (row == 0 ? 0 : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2);
+}
+
 // The sequences in blocks of 64, one a lane: lengths and running sums of units.
 struct Block64 {
     uint32_t first, len, before, upto;     // first sequence; the lane's length, units before and with it
@@ -221,15 +233,10 @@ __device__ inline void load_block(const AttendArgs &a, uint32_t first, uint32_t 
     k.first = first;
     k.len = b < a.c.batch ? seq_len(a.c, b, status) : 0;
     const uint32_t units = b < a.c.batch ? units_of(k.len, a.window, a.sinks) : 0;
-    const uint32_t n = min(64u, a.c.batch - first);
-    uint32_t sum = units;
-    for (uint32_t d = 1; d < n; d <<= 1) {
-        const uint32_t y = __shfl_up(sum, d);
-        if (lane >= d) sum += y;
-    }
+    const uint32_t sum = wave_scan(units);
     k.before = carry + sum - units;
     k.upto = carry + sum;
-    k.total = __builtin_amdgcn_readlane(k.upto, n - 1);
+    k.total = __builtin_amdgcn_readlane(k.upto, 63);
 }
 
 // Units of a launch, and how they are cut into runs: the first `extra` runs
@@ -601,31 +608,31 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     }
 }
 
-constexpr int kJoinThreads = 256;
-
+// Over all lanes of the wave.
 template <bool MAX>
-__device__ inline float block_reduce(float x, float *part) {
-    for (int k = 32; k; k >>= 1) {
-        const float y = __shfl_xor(x, k);
-        x = MAX ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = part[0];
-    for (int w = 1; w < kJoinThreads / 64; ++w) x = MAX ? fmaxf(x, part[w]) : x + part[w];
-    return x;
+__device__ inline float wave_reduce(float x) {
+    auto with = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+    x = with(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xf, 0xf, false)));    // row_ror:8
+    x = with(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x124, 0xf, 0xf, false)));    // row_ror:4
+    x = with(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x122, 0xf, 0xf, false)));    // row_ror:2
+    x = with(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x121, 0xf, 0xf, false)));    // row_ror:1
+    return row_reduce<MAX>(x);
 }
-constexpr uint32_t kMaxRuns = 2048;
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 12;      // shares a thread loads before their weights are known
+constexpr uint32_t kMaxRuns = 1024;
 
 // One workgroup per query head of a sequence: nothing to do where one run
 // held all of its tokens; else the runs' shares, rescaled to their common
-// maximum.
+// maximum.  It is a chain of three loads (lengths; maxima and sums; outputs),
+// so the outputs are asked for together with the maxima, and every wave works
+// the weights out for itself instead of waiting for another.
 template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
-    __shared__ float s_w[kMaxRuns], s_part[kJoinThreads / 64];
+    __shared__ float s_w[kJoinThreads / 64][kMaxRuns];
     __shared__ f32x4 s_o[kJoinThreads];
-    const uint32_t tid = threadIdx.x, b = blockIdx.y, head = blockIdx.x;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y, head = blockIdx.x;
     const uint32_t pairs = a.c.kv_heads * a.row_tiles;
     // units before the sequence, its own, and all
     uint32_t before = 0, units = 0, total = 0;
@@ -644,37 +651,47 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     const uint32_t first = cut.owner(u0), last = cut.owner(u0 + units - 1);
     if (first == last) return;
     const uint32_t n = last - first + 1;
-    auto slot = [&](uint32_t j) { return (uint64_t)(first + j) * 2 + (j == 0 && cut.begin(first) != u0); };
-    float top = -INFINITY;
-    for (uint32_t j = tid; j < n; j += kJoinThreads) {
-        const float m = a.share_ml[(slot(j) * a.rows + row) * 2];
-        s_w[j] = m;
-        top = fmaxf(top, m);
-    }
-    top = block_reduce<true>(top, s_part);
-    float sum = 0.f;
-    for (uint32_t j = tid; j < n; j += kJoinThreads) {
-        const float l = a.share_ml[(slot(j) * a.rows + row) * 2 + 1];
-        const float w = s_w[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_w[j] - top);
-        s_w[j] = w;
-        sum += s_w[j] == 0.f && l == l ? 0.f : l * w;
-    }
-    sum = block_reduce<false>(sum, s_part);
-    const uint32_t pieces = a.c.dim / 4;                // 4-column pieces of a row
-    const uint32_t ways = kJoinThreads / pieces;        // shares summed side by side
-    f32x4 y{0.f, 0.f, 0.f, 0.f};
+    // the first share is its run's second one where the run begins before u0
+    const uint32_t late = cut.begin(first) != u0;
+    auto share = [&](uint32_t j) { return (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row; };
+    const uint32_t pieces = a.c.dim / 4;             // 4-column pieces of a row
+    const uint32_t ways = kJoinThreads / pieces;     // shares summed side by side
     const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
-    if (way < ways) {
-#pragma unroll 8
-        for (uint32_t j = way; j < n; j += ways)
-            y += *(const f32x4 *)(a.share_o + (slot(j) * a.rows + row) * a.c.dim + d) * s_w[j];
+    f32x4 y[kJoinAhead];
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+        const uint32_t j = way + i * ways;
+        y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (way < ways && j < n) y[i] = *(const f32x4 *)(a.share_o + share(j) * a.c.dim + d);
     }
-    s_o[tid] = y;
+    float top = -INFINITY, sum = 0.f;
+    for (uint32_t j = lane; j < n; j += 64) top = fmaxf(top, a.share_ml[share(j) * 2]);
+    top = wave_reduce<true>(top);
+    for (uint32_t j = lane; j < n; j += 64) {
+        const float m = a.share_ml[share(j) * 2], l = a.share_ml[share(j) * 2 + 1];
+        // a share with m = -inf saw no finite logit: l is 0, or NaN, which stays
+        const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+        s_w[wave][j] = w;
+        sum += l * w;
+    }
+    sum = wave_reduce<false>(sum);
+    __builtin_amdgcn_wave_barrier();
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    if (way < ways) {
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const uint32_t j = way + i * ways;
+            if (j < n) o += y[i] * s_w[wave][j];
+        }
+        for (uint32_t j = way + kJoinAhead * ways; j < n; j += ways)
+            o += *(const f32x4 *)(a.share_o + share(j) * a.c.dim + d) * s_w[wave][j];
+    }
+    s_o[tid] = o;
     __syncthreads();
     if (tid < pieces) {
-        for (uint32_t w = 1; w < ways; ++w) y += s_o[w * pieces + tid];
+        for (uint32_t w = 1; w < ways; ++w) o += s_o[w * pieces + tid];
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
+        u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
         *(u32x2 *)(a.out + b * a.os[0] + head * a.os[1] + d) = z;
         if (tid == 0) {
             const float e = sum == 0.f ? -INFINITY : top + log2f(sum);
@@ -1027,7 +1044,7 @@ struct AttendPlan {
     size_t ml_at, lse2_at, logits_at, bytes;
 };
 
-constexpr uint32_t kRuns = 768;      // three workgroups on each of 256 compute units
+constexpr uint32_t kRuns = 512;      // two workgroups on each of 256 compute units
 static_assert(kRuns <= kMaxRuns, "the join holds one weight per run");
 
 inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }

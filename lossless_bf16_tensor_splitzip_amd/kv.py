@@ -15,21 +15,15 @@ Nothing here computes gradients: a cache is what a serving step keeps.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 
 import torch
 
 from . import _abi
-from .codec import _device_or_pinned, _same_gpu, _status_ptr, _stream
+from .codec import _device_or_pinned, _same_gpu, _status_ptr
 
 _DTYPES = {torch.bfloat16: _abi.KV_BF16, torch.float16: _abi.KV_FP16}
-
-
-def _on(device):
-    """The call's device as the current one (kernels go to the current one)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_raw_stream = torch._C._cuda_getCurrentRawStream     # an int, without making a Stream object
 
 
 def _strides(t: torch.Tensor, what: str, multiple: int = 8):
@@ -47,6 +41,18 @@ def _strides(t: torch.Tensor, what: str, multiple: int = 8):
                 raise ValueError("the strides of the %s must be multiples of %d elements, got %s"
                                  % (what, multiple, tuple(stride)))
     return out
+
+
+def _place(t: torch.Tensor, what: str, written: bool):
+    """Address and strides of a 16-bit tensor of three dimensions, checked as
+    ``_strides`` and, where it is written, ``_no_overlap`` do; those two run
+    only where the quick look is not content."""
+    p, (s0, s1, s2) = t.data_ptr(), t.stride()
+    if s2 != 1 or (s0 | s1 | p >> 1) & 7:
+        s0, s1 = _strides(t, what)
+    if written and not (s1 >= t.shape[2] and s0 >= s1 * t.shape[1]):
+        _no_overlap(t, what)
+    return p, s0, s1
 
 
 def _no_overlap(t: torch.Tensor, what: str) -> None:
@@ -116,32 +122,48 @@ class KVCache:
                                      max(_strides(table, "page table", 1)[0], self.max_pages), lens.data_ptr(),
                                      pages, page_size, kv_heads, dim, self.batch, self.max_pages,
                                      _DTYPES[self.dtype], 0)
+        self._ref = ctypes.byref(self.args)
+        self._index = self.device.index
 
     def _call(self, fn: str, stream, *args):
-        with _on(self.device):
-            _abi._check(fn, getattr(_abi, fn)(self.args, *args, _stream(stream, self.device)))
+        call = getattr(_abi.kv_lib(), fn)
+        if torch.cuda.current_device() == self._index:
+            code = call(self._ref, *args, _raw_stream(self._index) if stream is None else stream.cuda_stream)
+        else:               # kernels go to the current device
+            with torch.cuda.device(self._index):
+                code = call(self._ref, *args, _raw_stream(self._index) if stream is None else stream.cuda_stream)
+        if code:
+            raise _abi.SplitZipError(fn, code)
+
+    def _here(self, t: torch.Tensor, what: str) -> None:
+        if t.device != self.device:
+            raise ValueError("the %s must be on %s, got %s" % (what, self.device, t.device))
 
     def _rows(self, k, v, cu, start, written: bool):
+        grad = torch.is_grad_enabled()
         for t, what in ((k, "K rows"), (v, "V rows")):
-            _device_or_pinned(t, what)
-            if t.dtype is not self.dtype or t.dim() != 3 or tuple(t.shape[1:]) != (self.kv_heads, self.head_dim):
+            if t.is_cuda:
+                self._here(t, what)
+            else:
+                _device_or_pinned(t, what)
+            if t.dtype is not self.dtype or t.dim() != 3 or t.shape[1] != self.kv_heads or t.shape[2] != self.head_dim:
                 raise ValueError("the %s must be %s [rows, %d, %d], got %s %s"
                                  % (what, self.dtype, self.kv_heads, self.head_dim, t.dtype, tuple(t.shape)))
-            _no_grad(t, what)
-            if written:
-                _no_overlap(t, what)
+            if grad:
+                _no_grad(t, what)
         if k.shape[0] != v.shape[0]:
             raise ValueError("K and V must have the same number of rows")
-        _plain(cu, torch.int32, 1, "row ranges")
-        if cu.shape[0] != self.batch + 1 or not cu.is_contiguous():
-            raise ValueError("the row ranges need %d contiguous entries" % (self.batch + 1))
-        if start is not None:
-            _plain(start, torch.int32, 1, "first positions")
-            if start.shape[0] != self.batch or not start.is_contiguous():
-                raise ValueError("one contiguous first position per sequence")
-        _same_gpu(self.device, k, v, cu, start)
-        return _abi.KVRows(k.data_ptr(), v.data_ptr(), *_strides(k, "K rows"), *_strides(v, "V rows"), k.shape[0], 0,
-                           cu.data_ptr(), start.data_ptr() if start is not None else None)
+        for t, n, what in ((cu, self.batch + 1, "row ranges"), (start, self.batch, "first positions")):
+            if t is None and what == "first positions":
+                continue
+            _plain(t, torch.int32, 1, what)
+            self._here(t, what)
+            if t.shape[0] != n or not t.is_contiguous():
+                raise ValueError("the %s need %d contiguous entries" % (what, n))
+        kp, k0, k1 = _place(k, "K rows", written)
+        vp, v0, v1 = _place(v, "V rows", written)
+        return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, k.shape[0], 0, cu.data_ptr(),
+                                        None if start is None else start.data_ptr()))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor | None = None,
                status: torch.Tensor | None = None, stream=None) -> None:
@@ -161,12 +183,14 @@ class KVCache:
         self._call("splitzip_kv_gather", stream, rows, self._status(status))
 
     def _status(self, status):
+        if status is None:
+            return None
         _same_gpu(self.device, status)
         return _status_ptr(status)
 
     def _mass(self, mass, what: str, written: bool):
         _plain(mass, torch.float32, 3, what)
-        _same_gpu(self.device, mass)
+        self._here(mass, what)
         if mass.shape[0] != self.batch or mass.shape[1] != self.kv_heads:
             raise ValueError("the %s must be [%d, %d, tokens], got %s"
                              % (what, self.batch, self.kv_heads, tuple(mass.shape)))
@@ -208,12 +232,14 @@ class KVCache:
         weight every token received, summed over its KV head's query heads, is
         added to it: in place, or into ``mass_out``, whose entries up to the
         length are all written (with ``mass_out`` alone, starting from 0)."""
-        if not q.is_cuda:
-            raise ValueError("the queries must be on the GPU")
         if q.dtype is not self.dtype or q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != self.head_dim:
             raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
                              % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(q.shape)))
-        _no_grad(q, "queries")
+        self._here(q, "queries")
+        self._here(ws.buf, "workspace")
+        grad = torch.is_grad_enabled()
+        if grad:
+            _no_grad(q, "queries")
         heads = q.shape[1]
         if heads < 1 or heads % self.kv_heads:
             raise ValueError("%d query heads do not divide over %d KV heads" % (heads, self.kv_heads))
@@ -223,26 +249,30 @@ class KVCache:
             raise ValueError("the window must be in 0..2^31-1, got %d" % window)
         if not 0 <= sinks < 1 << 31:
             raise ValueError("the sinks must be in 0..2^31-1, got %d" % sinks)
-        if out is None:
-            pass
-        elif not out.is_cuda or out.dtype is not q.dtype or out.shape != q.shape:
-            raise ValueError("the output must be on the GPU and shaped like the queries")
-        else:
-            _no_overlap(out, "output")
-            _no_grad(out, "output")
+        if out is not None:
+            if out.dtype is not self.dtype or out.shape != q.shape:
+                raise ValueError("the output must be shaped like the queries")
+            self._here(out, "output")
+            if grad:
+                _no_grad(out, "output")
         if lse is not None:
             _plain(lse, torch.float32, 2, "lse")
             if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
                 raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))
-        mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
-        _same_gpu(self.device, q, out, lse, ws.buf)
+            self._here(lse, "lse")
+        mass_in = mass_to = None
+        ms = mos = (0, 0)
+        mass_len = 0
+        if mass is not None or mass_out is not None:
+            mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
+        qp, q0, q1 = _place(q, "queries", False)
         if out is None:
             with torch.cuda.stream(stream):
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        query = _abi.KVQuery(q.data_ptr(), *_strides(q, "queries"), out.data_ptr(), *_strides(out, "output"),
-                             lse.data_ptr() if lse is not None else None, mass_in, mass_to, *ms, *mos, heads, window,
-                             sinks, self.head_dim ** -0.5 if scale is None else scale, mass_len, 0)
-        self._call("splitzip_kv_attend", stream, query, ws.buf.data_ptr(), ws.nbytes, self._status(status))
+        op, o0, o1 = _place(out, "output", True)
+        query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), mass_in, mass_to, *ms, *mos,
+                             heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale, mass_len, 0)
+        self._call("splitzip_kv_attend", stream, ctypes.byref(query), ws.buf.data_ptr(), ws.nbytes, self._status(status))
         return out
 
     def evict(self, mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, to: "KVCache | None" = None,
@@ -273,13 +303,13 @@ class KVCache:
             _plain(kept, torch.int32, 3, "kept positions")
             if tuple(kept.shape) != shape or not kept.is_contiguous():
                 raise ValueError("the kept positions must be contiguous %s" % (shape,))
+            self._here(kept, "kept positions")
         mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
-        _same_gpu(self.device, kept)
         if kept is None:
             with torch.cuda.stream(stream):
                 kept = torch.empty(shape, dtype=torch.int32, device=self.device)
         args = _abi.KVBudget(mass_in, mass_to, *ms, *mos, kept.data_ptr(), budget, sinks, recent, mass_len)
-        self._call("splitzip_kv_evict", stream, to.args, args, self._status(status))
+        self._call("splitzip_kv_evict", stream, to._ref, ctypes.byref(args), self._status(status))
         return kept
 
 

@@ -1,8 +1,6 @@
 """The refusals of the key-value cache's tensor-level calls without a GPU: host
 tensors that say they are on one, and the real library, in which a call that
 is accepted gets as far as the launch (no device: a HIP error) and no further."""
-import contextlib
-
 import pytest
 import torch
 
@@ -23,8 +21,8 @@ class SaysGpu(torch.Tensor):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would launch on host memory")
 @pytest.mark.parametrize("part", ["caches", "rows", "queries", "budgets"])
 def test_refusals(part, monkeypatch):
-    monkeypatch.setattr(kv, "_stream", lambda stream, device: 0)
-    monkeypatch.setattr(kv, "_on", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(kv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(S.KVWorkspace, "_buffer", lambda self, nbytes, device: put(torch.empty(nbytes, dtype=torch.uint8)))
 
     def put(t):
