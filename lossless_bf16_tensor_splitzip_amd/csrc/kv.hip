@@ -746,24 +746,42 @@ struct EvictArgs {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
-constexpr int kSelCopies = 16;
 
-// The masses as unsigned integers of the same order: -0 as 0, NaN above all.
+// The masses as unsigned integers of the same order: -0 as 0, NaN above all
+// numbers; above NaN the tokens that stay whatever their mass, and below all
+// keys (-inf has 0x007fffff) what is no token.
+constexpr uint32_t kKeyAlways = 0xffffffffu, kKeyNan = 0xfffffffeu, kKeyNone = 0;
+
 __device__ inline uint32_t mass_key(float m) {
-    if (m != m) return 0xffffffffu;
     const uint32_t u = __float_as_uint(m + 0.f);   // -0 + 0 = 0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t key = u ^ (0x80000000u | (uint32_t)((int32_t)u >> 31));
+    return m != m ? kKeyNan : key;
 }
 
-// One workgroup per sequence and KV head: the threshold key by four
-// passes over its bytes from the top (a histogram in LDS of the keys that
-// agree so far), then every wave places what it keeps of a run of tokens of
-// its own, in order.
+// Set lanes of the mask below this one.
+__device__ inline uint32_t lanes_below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// The threshold is found by its bits from the top, kSelDigits[i] of them a
+// pass: a histogram in LDS of the keys that agree so far, and its suffix sums.
+// The first digit of 11 bits is sign, exponent and two bits below, so that
+// masses, which crowd into a few powers of two, spread over more than a few
+// counters (LDS adds to one address take turns).
+constexpr int kSelBits = 11, kSelBins = 1 << kSelBits, kSelPasses = 3;
+constexpr int kSelCopies = 4;      // of the first pass's histogram, by lane
+constexpr int kSelHeld = 32;       // masses a thread can hold
+
+// One workgroup per sequence and KV head.  Wave w has the run of tokens from
+// w * span; lane l its tokens l, l + 64, ..., HELD of them in registers (all
+// of them where span is at most 64 HELD, and then the masses are read once);
+// HELD 0: read again by every pass.
+template <int HELD>
 __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
-    __shared__ uint32_t hist[256 * kSelCopies];
-    __shared__ uint32_t above_w[kSelWaves], equal_w[kSelWaves];
+    __shared__ __align__(16) uint32_t hist[kSelBins * kSelCopies];
+    __shared__ uint32_t part[kSelWaves], part2[kSelWaves];
     __shared__ uint32_t s_prefix, s_need;
-    const uint32_t b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int32_t *status = tid == 0 && h == 0 ? a.status : nullptr;
     uint32_t n = seq_len(a.c, b, status);
     if (n > a.mass_len) {
@@ -775,100 +793,127 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
     int32_t *kept = a.kept + ((uint64_t)b * a.c.kv_heads + h) * a.budget;
     if (n <= a.budget) {
         for (uint32_t t = tid; t < a.budget; t += kSelThreads) kept[t] = t < n ? (int32_t)t : -1;
-        if (out)
+        if (out && out != mass)
             for (uint32_t t = tid; t < n; t += kSelThreads) out[t] = mass[t];
         return;
     }
-    const uint32_t lo = a.sinks, hi = n - a.recent, take = a.budget - a.sinks - a.recent;
-    uint32_t prefix = 0, need = take;
-    if (take) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (uint32_t k = tid; k < 256 * kSelCopies; k += kSelThreads) hist[k] = 0;
-            __syncthreads();
-            const uint32_t seen = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (uint32_t t = lo + tid; t < hi; t += kSelThreads) {
-                const uint32_t key = mass_key(mass[t]);
-                if ((key & seen) == prefix)
-                    atomicAdd(&hist[((key >> shift) & 255u) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
-            }
-            __syncthreads();
-            if (wave == 0) {
-                // lane l holds bins 4l .. 4l+3; suffix sums over the lanes
-                uint32_t bin[4], sum = 0;
-                for (int k = 0; k < 4; ++k) {
-                    bin[k] = 0;
-                    for (int j = 0; j < kSelCopies; ++j) bin[k] += hist[(lane * 4 + k) * kSelCopies + j];
-                    sum += bin[k];
-                }
-                uint32_t suf = sum;
-                for (int d = 1; d < 64; d <<= 1) {
-                    const uint32_t y = __shfl_down(suf, d);
-                    if (lane + d < 64) suf += y;
-                }
-                uint32_t above = suf - sum;      // keys in higher lanes' bins
-                for (int k = 3; k >= 0; --k) {
-                    if (above < need && above + bin[k] >= need) {
-                        s_prefix = prefix | ((lane * 4 + k) << shift);
-                        s_need = need - above;
-                    }
-                    above += bin[k];
-                }
-            }
-            __syncthreads();
-            prefix = s_prefix;
-            need = s_need;
+    const uint32_t span = ((n + kSelThreads - 1) / kSelThreads) * 64;
+    const uint32_t w0 = min(n, wave * span), w1 = min(n, w0 + span);
+    auto key_of = [&](uint32_t t, float m) {
+        return t >= w1 ? kKeyNone : t < a.sinks || t >= n - a.recent ? kKeyAlways : mass_key(m);
+    };
+    float held[HELD ? HELD : 1];
+    uint32_t keys[HELD ? HELD : 1];
+    if (HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const uint32_t t = w0 + i * 64 + lane;
+            held[i] = t < w1 ? mass[t] : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) keys[i] = key_of(w0 + i * 64 + lane, held[i]);
     }
-    // Of [lo, hi): keys above prefix stay, and the first `need` equal to it.
-    const uint32_t span = (hi - lo + kSelWaves - 1) / kSelWaves;
-    const uint32_t w0 = min(hi, lo + wave * span), w1 = min(hi, w0 + span);
-    uint32_t above = 0, equal = 0;
-    if (take)
-        for (uint32_t t0 = w0; t0 < w1; t0 += 64) {
-            const uint32_t t = t0 + lane;
-            const uint32_t key = t < w1 ? mass_key(mass[t]) : 0u;
-            above += __popcll(__ballot(t < w1 && key > prefix));
-            equal += __popcll(__ballot(t < w1 && key == prefix));
+    // f(token, mass, key) over the wave's run, in order
+    auto each = [&](auto f) {
+        if (HELD) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (w0 + i * 64 < w1) f(w0 + i * 64 + lane, held[i], keys[i]);
+        } else {
+            for (uint32_t t = w0 + lane; t - lane < w1; t += 64) {
+                const float m = t < w1 ? mass[t] : 0.f;
+                f(t, m, key_of(t, m));
+            }
         }
+    };
+    uint32_t prefix = 0, need = a.budget;
+    for (int pass = 0, left = 32; pass < kSelPasses; ++pass) {
+        // the last digit repeats a bit of the one before, which is agreed on
+        const int shift = left > kSelBits ? left - kSelBits : 0;
+        const uint32_t agreed = pass ? 0xffffffffu << left : 0u;
+        for (uint32_t k = tid; k < (uint32_t)(kSelBins * kSelCopies / 4); k += kSelThreads) ((u32x4 *)hist)[k] = u32x4{0, 0, 0, 0};
+        __syncthreads();
+        each([&](uint32_t, float, uint32_t key) {
+            if ((key & agreed) == prefix)
+                atomicAdd(&hist[(key >> shift & (kSelBins - 1)) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
+        });
+        __syncthreads();
+        // thread i has bins 2i and 2i + 1, counted from the top bin down
+        const uint32_t top = kSelBins - 1 - 2 * tid;
+        uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+        for (int j = 0; j < kSelCopies; ++j) {
+            c0 += hist[top * kSelCopies + j];
+            c1 += hist[(top - 1) * kSelCopies + j];
+        }
+        const uint32_t upto = wave_scan(c0 + c1);
+        if (lane == 63) part[wave] = upto;
+        __syncthreads();
+        uint32_t above = upto - c0 - c1;
+        for (uint32_t w = 0; w < wave; ++w) above += part[w];
+        if (above < need && above + c0 >= need) {
+            s_prefix = prefix | top << shift;
+            s_need = need - above;
+        }
+        above += c0;
+        if (above < need && above + c1 >= need) {
+            s_prefix = prefix | (top - 1) << shift;
+            s_need = need - above;
+        }
+        __syncthreads();
+        prefix = s_prefix;
+        need = s_need;
+        left = shift;
+    }
+    // Kept: the keys above the threshold, and the first `need` of those equal to
+    // it.  A wave counts its own, then places them from where the waves before
+    // it end.
+    uint32_t mine = 0, ties = 0;
+    each([&](uint32_t, float, uint32_t key) {
+        mine += __popcll(__ballot(key > prefix));
+        ties += __popcll(__ballot(key == prefix));
+    });
     if (lane == 0) {
-        above_w[wave] = above;
-        equal_w[wave] = equal;
+        part[wave] = mine;
+        part2[wave] = ties;
     }
     __syncthreads();
-    uint32_t at = a.sinks, eq = 0;
+    uint32_t at = 0, eq = 0;
     for (uint32_t w = 0; w < wave; ++w) {
-        at += above_w[w];
-        eq += equal_w[w];
+        at += part[w];
+        eq += part2[w];
     }
     at += min(eq, need);
-    // In place, a kept mass moves to a position that is not above its own, which
-    // an earlier wave may not have read yet: the tokens are placed first,
-    // then their masses copied in order.
-    for (uint32_t t = tid; t < lo; t += kSelThreads) kept[t] = (int32_t)t;
-    for (uint32_t t = tid; t < a.recent; t += kSelThreads) kept[a.budget - a.recent + t] = (int32_t)(hi + t);
-    if (take)
-        for (uint32_t t0 = w0; t0 < w1; t0 += 64) {
-            const uint32_t t = t0 + lane;
-            const uint32_t key = t < w1 ? mass_key(mass[t]) : 0u;
-            const uint64_t below = (1ull << lane) - 1;
-            const uint64_t gt = __ballot(t < w1 && key > prefix), same = __ballot(t < w1 && key == prefix);
-            const uint32_t rank = eq + __popcll(same & below);
-            const bool tie = (same >> lane & 1) && rank < need;
-            const uint64_t keep = gt | __ballot(tie);
-            if (keep >> lane & 1) kept[at + __popcll(keep & below)] = (int32_t)t;
-            at += __popcll(keep);
+    // In place a mass moves to a position at or below its own; with all of
+    // them in registers that is free of order, else see below.
+    each([&](uint32_t t, float m, uint32_t key) {
+        const uint64_t same = __ballot(key == prefix);
+        uint64_t all = __ballot(key > prefix);
+        if (same) {
+            const uint32_t rank = eq + lanes_below(same);
+            all |= __ballot(key == prefix && rank < need);
             eq += __popcll(same);
         }
+        if (all >> lane & 1) {
+            const uint32_t to = at + lanes_below(all);
+            kept[to] = (int32_t)t;
+            if (HELD && out) out[to] = m;
+        }
+        at += __popcll(all);
+    });
     if (!out) return;
     __syncthreads();
-    for (uint32_t t0 = 0; t0 < a.budget; t0 += kSelThreads) {
-        const uint32_t t = t0 + tid;
-        float m = 0.f;
-        if (t < a.budget) m = mass[kept[t]];
+    if (!HELD) {
+        // step by step upwards, a step's masses read before any of it is written
+        for (uint32_t t0 = 0; t0 < a.budget; t0 += kSelThreads) {
+            const uint32_t t = t0 + tid;
+            float m = 0.f;
+            if (t < a.budget) m = mass[kept[t]];
+            __syncthreads();
+            if (t < a.budget) out[t] = m;
+        }
         __syncthreads();
-        if (t < a.budget) out[t] = m;
     }
-    __syncthreads();
     for (uint32_t t = a.budget + tid; t < n; t += kSelThreads) out[t] = 0.f;
 }
 
@@ -1238,7 +1283,11 @@ int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *t
     a.chunk = pieces < 8 ? pieces : 8;
     a.chunks = (pieces + a.chunk - 1) / a.chunk;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    k_select<<<dim3(cache->batch, cache->kv_heads), kSelThreads, 0, s>>>(a);
+    const dim3 heads(cache->kv_heads, cache->batch);
+    const uint64_t longest = all < B.mass_len ? all : B.mass_len;
+    if (longest <= 4 * kSelThreads) k_select<4><<<heads, kSelThreads, 0, s>>>(a);
+    else if (longest <= kSelHeld * kSelThreads) k_select<kSelHeld><<<heads, kSelThreads, 0, s>>>(a);
+    else k_select<0><<<heads, kSelThreads, 0, s>>>(a);
     const int rc = launched();
     if (rc) return rc;
     const uint32_t most = (uint32_t)(all < B.budget ? all : B.budget);
