@@ -68,6 +68,10 @@ __device__ inline bool locate(const Cache &c, uint32_t b, uint32_t t, uint32_t &
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// 16 bytes that nothing reads again soon.
+__device__ inline u32x4 load_once(const uint16_t *p) { return __builtin_nontemporal_load((const u32x4 *)p); }
+__device__ inline void store_away(uint16_t *p, u32x4 x) { __builtin_nontemporal_store(x, (u32x4 *)p); }
+
 // ---------------------------------------------------------------------------
 // append / gather
 // ---------------------------------------------------------------------------
@@ -84,6 +88,7 @@ struct RowArgs {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowMax = 64;      // rows a workgroup
+constexpr int kRowAhead = 4;
 
 // A workgroup copies per_wg rows: one thread per row finds its place, then
 // all threads copy 16-byte pieces, neighbouring threads neighbouring pieces.
@@ -123,19 +128,34 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
         }
         __syncthreads();
         const uint32_t total = count * a.items.d;
-#pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < total; i += kRowThreads) {
-            const uint32_t r = div(i, a.items), j = i - r * a.items.d;
-            const uint32_t h = div(j, a.chunks), d = (j - h * a.chunks.d) * 8;
-            if (at_k[r] == kNone) continue;
-            uint16_t *pk = a.c.k + at_k[r] + h * a.c.ks[1] + d;
-            uint16_t *pv = a.c.v + at_v[r] + h * a.c.vs[1] + d;
-            uint16_t *rk = a.k + (uint64_t)(r0 + r) * a.ks[0] + h * a.ks[1] + d;
-            uint16_t *rv = a.v + (uint64_t)(r0 + r) * a.vs[0] + h * a.vs[1] + d;
-            const u32x4 xk = *(const u32x4 *)(GATHER ? pk : rk);
-            const u32x4 xv = *(const u32x4 *)(GATHER ? pv : rv);
-            *(u32x4 *)(GATHER ? rk : pk) = xk;
-            *(u32x4 *)(GATHER ? rv : pv) = xv;
+        // kRowAhead pieces of each pool a time, so that as many loads are under way
+        for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kRowThreads * kRowAhead) {
+            u32x4 xk[kRowAhead], xv[kRowAhead];
+            uint16_t *tk[kRowAhead], *tv[kRowAhead];
+#pragma unroll
+            for (int u = 0; u < kRowAhead; ++u) {
+                const uint32_t i = i0 + u * kRowThreads;
+                tk[u] = nullptr;
+                if (i >= total) continue;
+                const uint32_t r = div(i, a.items), j = i - r * a.items.d;
+                const uint32_t h = div(j, a.chunks), d = (j - h * a.chunks.d) * 8;
+                if (at_k[r] == kNone) continue;
+                uint16_t *pk = a.c.k + at_k[r] + h * a.c.ks[1] + d;
+                uint16_t *pv = a.c.v + at_v[r] + h * a.c.vs[1] + d;
+                uint16_t *rk = a.k + (uint64_t)(r0 + r) * a.ks[0] + h * a.ks[1] + d;
+                uint16_t *rv = a.v + (uint64_t)(r0 + r) * a.vs[0] + h * a.vs[1] + d;
+                // pages are read for this once, new rows may still be in a cache
+                xk[u] = GATHER ? load_once(pk) : *(const u32x4 *)rk;
+                xv[u] = GATHER ? load_once(pv) : *(const u32x4 *)rv;
+                tk[u] = GATHER ? rk : pk;
+                tv[u] = GATHER ? rv : pv;
+            }
+#pragma unroll
+            for (int u = 0; u < kRowAhead; ++u)
+                if (tk[u]) {
+                    store_away(tk[u], xk[u]);
+                    store_away(tv[u], xv[u]);
+                }
         }
         __syncthreads();
     }
@@ -265,6 +285,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 template <bool BF16>
 __device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -313,6 +334,10 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     constexpr int VW = 4 * P16 + 2 * P8;    // words of them
     constexpr int VC = 2 * VW;              // columns
     constexpr int LD = DP + 4;
+    // The query rows stay in registers, or in LDS where those would spill.
+    constexpr bool QLDS = NT * KS >= 12;
+    constexpr int LQ = DP + 8;
+    __shared__ __align__(16) uint16_t s_q[QLDS ? NT * 16 * LQ : 8];
     // fp16 weights are held times 2^15: their smallest normal step then lies 2^-29
     // below the largest weight instead of 2^-14.
     constexpr float kLift = BF16 ? 0.f : 15.f;
@@ -357,16 +382,31 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
         const uint32_t v_end = min(seen.count, (unit0 + count) * kUnit);
         const int32_t *table = a.c.table + b * a.c.table_stride;
 
-        u32x4 q[NT][KS];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                q[t][j] = u32x4{0, 0, 0, 0};
-                const uint32_t d = j * 32 + g * 8;
-                if (t * 16 + c16 < rows && (EXACT || d < D))
-                    q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + t * 16 + c16) * a.qs[1] + d);
+        u32x4 q[QLDS ? 1 : NT][QLDS ? 1 : KS];
+        if constexpr (QLDS) {
+            __syncthreads();
+            for (uint32_t i = tid; i < NT * 16 * (DP / 8); i += kAttendThreads) {
+                const uint32_t row = i / (DP / 8), d = i % (DP / 8) * 8;
+                u32x4 x{0, 0, 0, 0};
+                if (row < rows && (EXACT || d < D)) x = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + row) * a.qs[1] + d);
+                *(u32x4 *)&s_q[row * LQ + d] = x;
             }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    q[t][j] = u32x4{0, 0, 0, 0};
+                    const uint32_t d = j * 32 + g * 8;
+                    if (t * 16 + c16 < rows && (EXACT || d < D))
+                        q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + t * 16 + c16) * a.qs[1] + d);
+                }
+        }
+        auto query = [&](int t, int j) {
+            if constexpr (QLDS) return *(const u32x4 *)&s_q[(t * 16 + c16) * LQ + j * 32 + g * 8];
+            else return q[t][j];
+        };
         f32x4 o[NT][VC];
         float m[NT], l[NT];
 #pragma unroll
@@ -421,7 +461,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                 const uint64_t off = off_k[wave][buf][s * 16 + c16];
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
-                    kr[s][j] = *(const u32x4 *)(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
+                    kr[s][j] = load_once(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
             }
         };
         auto load_v = [&](int buf) {
@@ -429,8 +469,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (int i = 0; i < 8; ++i) {
                 const uint64_t off = off_v[wave][buf][(i >> 2) * 16 + g * 4 + (i & 3)];
 #pragma unroll
-                for (int p = 0; p < P16; ++p) v16[i][p] = *(const u32x4 *)(v_lane[p] + off);
-                if (P8) v8[i] = *(const u32x2 *)(v_lane[P16] + off);
+                for (int p = 0; p < P16; ++p) v16[i][p] = load_once(v_lane[p] + off);
+                if constexpr (P8 > 0) v8[i] = __builtin_nontemporal_load((const u32x2 *)(v_lane[P16] + off));
             }
         };
 
@@ -457,13 +497,15 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             }
             f32x4 x[NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                x[t][0] = x[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    x[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) x[t][s] = mfma<BF16>(kr[s][j], q[t][j], x[t][s]);
+                for (int j = 0; j < KS; ++j) {
+                    const u32x4 y = query(t, j);
+                    x[t][0] = mfma<BF16>(kr[0][j], y, x[t][0]);
+                    x[t][1] = mfma<BF16>(kr[1][j], y, x[t][1]);
                 }
+            }
             if (more) load_k(buf ^ 1);
 
             u32x4 hi[NT], lo[NT];
@@ -513,7 +555,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                     if (!(mine >> i & 1)) {
 #pragma unroll
                         for (int p = 0; p < P16; ++p) v16[i][p] = u32x4{0, 0, 0, 0};
-                        if (P8) v8[i] = u32x2{0, 0};
+                        if constexpr (P8 > 0) v8[i] = u32x2{0, 0};
                     }
             }
 #pragma unroll
@@ -623,37 +665,160 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 12;      // shares a thread loads before their weights are known
 constexpr uint32_t kMaxRuns = 1024;
 
+// Which runs have shares of a sequence's query head.
+struct Shares {
+    Cut cut;
+    uint32_t before, units, pairs;     // units before the sequence, of one of its pairs; pairs of a sequence
+    uint32_t first, n, row, late;      // of the head looked up: runs first .. first + n - 1; its row in their shares;
+                                       // whether the first has it as its second share
+
+    __device__ void sequence(const AttendArgs &a, uint32_t b) {
+        uint32_t total = 0;
+        before = units = 0;
+        for (uint32_t f = 0; f < a.c.batch; f += 64) {
+            Block64 k;
+            load_block(a, f, total, k, nullptr);
+            if (b >= f && b < f + 64) {
+                before = __builtin_amdgcn_readlane(k.before, b - f);
+                units = __builtin_amdgcn_readlane(k.upto, b - f) - before;
+            }
+            total = k.total;
+        }
+        pairs = a.c.kv_heads * a.row_tiles;
+        cut = cut_of(total * pairs, a.runs);
+    }
+    __device__ void head(const AttendArgs &a, uint32_t h, uint32_t in_group) {
+        const uint32_t tile = in_group / a.rows;
+        row = in_group - tile * a.rows;
+        const uint32_t u0 = before * pairs + (h * a.row_tiles + tile) * units;
+        first = cut.owner(u0);
+        n = cut.owner(u0 + units - 1) - first + 1;
+        late = cut.begin(first) != u0;
+    }
+    __device__ uint64_t at(const AttendArgs &a, uint32_t j) const {
+        return (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row;
+    }
+};
+
+// Largest share's maximum and the joined sum of the head looked up, over the
+// lanes of a wave; keep(j, weight) for every share.
+template <typename F>
+__device__ inline void weigh(const AttendArgs &a, const Shares &sh, float &top, float &sum, F keep) {
+    const uint32_t lane = threadIdx.x & 63;
+    // a share with m = -inf saw no finite logit: its sum is 0, or NaN, which stays
+    auto weight = [&](float m) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
+    f32x2 ml{-INFINITY, 0.f};
+    if (lane < sh.n) ml = *(const f32x2 *)(a.share_ml + sh.at(a, lane) * 2);
+    top = ml[0];
+    for (uint32_t j = lane + 64; j < sh.n; j += 64) top = fmaxf(top, a.share_ml[sh.at(a, j) * 2]);
+    top = wave_reduce<true>(top);
+    const float w = weight(ml[0]);
+    if (lane < sh.n) keep(lane, w);
+    sum = ml[1] * w;
+    for (uint32_t j = lane + 64; j < sh.n; j += 64) {
+        const f32x2 more = *(const f32x2 *)(a.share_ml + sh.at(a, j) * 2);
+        const float v = weight(more[0]);
+        keep(j, v);
+        sum += more[1] * v;
+    }
+    sum = wave_reduce<false>(sum);
+}
+
+constexpr int kMassAhead = 4;                                   // tokens a thread, and query rows loaded ahead
+constexpr uint32_t kMassTokens = kMassAhead * kJoinThreads;     // a workgroup
+constexpr uint32_t kMassRows = 64;                              // query rows it takes at a time
+
+// mass_out = mass + the group's weights, for one KV head's tokens from `part`
+// on.  Each workgroup works the rows' lse out for itself from their shares (or
+// takes them where one run had all).
+__device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uint32_t part) {
+    __shared__ float s_lse[kMassRows];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t n = seq_len(a.c, b);
+    const Seen seen = seen_of(n, a.window, a.sinks);
+    if (n > a.mass_len) {
+        if (part == 0 && h == 0 && tid == 0) report(a.status, SPLITZIP_KV_BAD_LEN);
+        n = a.mass_len;
+    }
+    const uint32_t t0 = part * kMassTokens + tid;
+    if (part * kMassTokens >= n) return;
+    Shares sh;
+    sh.sequence(a, b);
+    const float *x = a.logits + (b * (uint64_t)a.heads + h * a.group) * a.logit_stride;
+    const float *in = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
+    float *out = a.mass_out + b * a.mos[0] + h * a.mos[1];
+    // the masses and the first rows' logits are under way while the lse are found
+    float w[kMassAhead], old[kMassAhead], ahead[kMassAhead][kMassAhead];
+    uint32_t v[kMassAhead];
+#pragma unroll
+    for (int k = 0; k < kMassAhead; ++k) {
+        const uint32_t t = t0 + k * kJoinThreads;
+        const bool hidden = t >= n || (t >= seen.sinks && t - seen.sinks < seen.shift);
+        v[k] = hidden ? 0xffffffffu : t < seen.sinks ? t : t - seen.shift;
+        w[k] = 0.f;
+        old[k] = in && t < n ? in[t] : 0.f;
+#pragma unroll
+        for (int r = 0; r < kMassAhead; ++r)
+            ahead[k][r] = hidden || r >= (int)a.group ? -INFINITY : x[r * a.logit_stride + v[k]];
+    }
+    for (uint32_t r0 = 0; r0 < a.group; r0 += kMassRows) {
+        const uint32_t rows = min(kMassRows, a.group - r0);
+        __syncthreads();
+        for (uint32_t r = wave; r < rows; r += kJoinThreads / 64) {
+            sh.head(a, h, r0 + r);
+            float e;
+            if (sh.n == 1) {
+                e = a.lse2[b * (uint64_t)a.heads + h * a.group + r0 + r];
+            } else {
+                float top, sum;
+                weigh(a, sh, top, sum, [](uint32_t, float) {});
+                e = sum == 0.f ? -INFINITY : top + log2f(sum);
+            }
+            // where nothing weighs, no logit does
+            if (lane == 0) s_lse[r] = e == -INFINITY ? INFINITY : e;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kMassAhead; ++k) {
+            if (v[k] == 0xffffffffu) continue;
+            uint32_t r = 0;
+            if (r0 == 0) {
+#pragma unroll
+                for (int i = 0; i < kMassAhead; ++i)
+                    if (i < (int)rows) w[k] += __builtin_amdgcn_exp2f(ahead[k][i] - s_lse[i]);
+                r = kMassAhead;
+            }
+#pragma unroll 4
+            for (; r < rows; ++r) w[k] += __builtin_amdgcn_exp2f(x[(r0 + r) * a.logit_stride + v[k]] - s_lse[r]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kMassAhead; ++k)
+        if (t0 + k * kJoinThreads < n) out[t0 + k * kJoinThreads] = old[k] + w[k];
+}
+
 // One workgroup per query head of a sequence: nothing to do where one run
 // held all of its tokens; else the runs' shares, rescaled to their common
 // maximum.  It is a chain of three loads (lengths; maxima and sums; outputs),
 // so the outputs are asked for together with the maxima, and every wave works
-// the weights out for itself instead of waiting for another.
+// the weights out for itself instead of waiting for another.  The workgroups
+// behind them add the mass.
 template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     __shared__ float s_w[kJoinThreads / 64][kMaxRuns];
     __shared__ f32x4 s_o[kJoinThreads];
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y, head = blockIdx.x;
-    const uint32_t pairs = a.c.kv_heads * a.row_tiles;
-    // units before the sequence, its own, and all
-    uint32_t before = 0, units = 0, total = 0;
-    for (uint32_t f = 0; f < a.c.batch; f += 64) {
-        Block64 k;
-        load_block(a, f, total, k, nullptr);
-        if (b >= f && b < f + 64) {
-            before = __builtin_amdgcn_readlane(k.before, b - f);
-            units = __builtin_amdgcn_readlane(k.upto, b - f) - before;
-        }
-        total = k.total;
+    const uint32_t tid = threadIdx.x, wave = tid >> 6, b = blockIdx.y, head = blockIdx.x;
+    if (head >= a.heads) {
+        const uint32_t i = head - a.heads, part = i / a.c.kv_heads;
+        add_mass(a, b, i - part * a.c.kv_heads, part);
+        return;
     }
-    const Cut cut = cut_of(total * pairs, a.runs);
-    const uint32_t h = head / a.group, in_group = head - h * a.group, tile = in_group / a.rows, row = in_group - tile * a.rows;
-    const uint32_t u0 = before * pairs + (h * a.row_tiles + tile) * units;
-    const uint32_t first = cut.owner(u0), last = cut.owner(u0 + units - 1);
-    if (first == last) return;
-    const uint32_t n = last - first + 1;
-    // the first share is its run's second one where the run begins before u0
-    const uint32_t late = cut.begin(first) != u0;
-    auto share = [&](uint32_t j) { return (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row; };
+    Shares sh;
+    sh.sequence(a, b);
+    const uint32_t h = head / a.group;
+    sh.head(a, h, head - h * a.group);
+    const uint32_t n = sh.n;
+    if (n == 1) return;
     const uint32_t pieces = a.c.dim / 4;             // 4-column pieces of a row
     const uint32_t ways = kJoinThreads / pieces;     // shares summed side by side
     const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
@@ -662,19 +827,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     for (int i = 0; i < kJoinAhead; ++i) {
         const uint32_t j = way + i * ways;
         y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (way < ways && j < n) y[i] = *(const f32x4 *)(a.share_o + share(j) * a.c.dim + d);
+        if (way < ways && j < n) y[i] = *(const f32x4 *)(a.share_o + sh.at(a, j) * a.c.dim + d);
     }
-    float top = -INFINITY, sum = 0.f;
-    for (uint32_t j = lane; j < n; j += 64) top = fmaxf(top, a.share_ml[share(j) * 2]);
-    top = wave_reduce<true>(top);
-    for (uint32_t j = lane; j < n; j += 64) {
-        const float m = a.share_ml[share(j) * 2], l = a.share_ml[share(j) * 2 + 1];
-        // a share with m = -inf saw no finite logit: l is 0, or NaN, which stays
-        const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        s_w[wave][j] = w;
-        sum += l * w;
-    }
-    sum = wave_reduce<false>(sum);
+    float top, sum;
+    weigh(a, sh, top, sum, [&](uint32_t j, float w) { s_w[wave][j] = w; });
     __builtin_amdgcn_wave_barrier();
     f32x4 o{0.f, 0.f, 0.f, 0.f};
     if (way < ways) {
@@ -684,7 +840,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
             if (j < n) o += y[i] * s_w[wave][j];
         }
         for (uint32_t j = way + kJoinAhead * ways; j < n; j += ways)
-            o += *(const f32x4 *)(a.share_o + share(j) * a.c.dim + d) * s_w[wave][j];
+            o += *(const f32x4 *)(a.share_o + sh.at(a, j) * a.c.dim + d) * s_w[wave][j];
     }
     s_o[tid] = o;
     __syncthreads();
@@ -696,36 +852,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
         if (tid == 0) {
             const float e = sum == 0.f ? -INFINITY : top + log2f(sum);
             if (a.lse) a.lse[b * (uint64_t)a.heads + head] = e * kLn2;
-            if (a.lse2) a.lse2[b * (uint64_t)a.heads + head] = e;
         }
-    }
-}
-
-constexpr int kMassThreads = 256;
-
-// mass_out = mass + the group's weights, four tokens a thread.
-__global__ __launch_bounds__(kMassThreads) void k_mass(AttendArgs a) {
-    const uint32_t h = blockIdx.y, b = blockIdx.z;
-    uint32_t n = seq_len(a.c, b);
-    const Seen seen = seen_of(n, a.window, a.sinks);
-    if (n > a.mass_len) {
-        if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) report(a.status, SPLITZIP_KV_BAD_LEN);
-        n = a.mass_len;
-    }
-    const float *in = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
-    float *out = a.mass_out + b * a.mos[0] + h * a.mos[1];
-    const float *x = a.logits + (b * (uint64_t)a.heads + h * a.group) * a.logit_stride;
-    const float *lse2 = a.lse2 + b * (uint64_t)a.heads + h * a.group;
-    for (uint64_t t = blockIdx.x * kMassThreads + threadIdx.x; t < n; t += (uint64_t)gridDim.x * kMassThreads) {
-        float w = 0.f;
-        if (t < seen.sinks || t >= (uint64_t)seen.sinks + seen.shift) {
-            const uint64_t v = t < seen.sinks ? t : t - seen.shift;
-            for (uint32_t i = 0; i < a.group; ++i) {
-                const float e = lse2[i];
-                w += e == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x[i * a.logit_stride + v] - e);
-            }
-        }
-        out[t] = (in ? in[t] : 0.f) + w;
     }
 }
 
@@ -968,13 +1095,13 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
         for (int u = 0; u < kMoveUnroll; ++u) {
             const uint32_t j = u * lane_rows + row;
             ok[u] = row < lane_rows && piece < width && from[j] != kNone;
-            if (ok[u]) x[u] = *(const u32x4 *)(src + from[j] + piece * 8);
+            if (ok[u]) x[u] = load_once(src + from[j] + piece * 8);
         }
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
-            if (ok[u]) *(u32x4 *)(dst + dest[u * lane_rows + row] + piece * 8) = x[u];
+            if (ok[u]) store_away(dst + dest[u * lane_rows + row] + piece * 8, x[u]);
         __syncthreads();
     }
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.to.lens[b] = (int32_t)n;
@@ -1068,8 +1195,8 @@ int copy_rows(const splitzip_kv_cache *cache, const splitzip_kv_rows *r, int32_t
     a.status = d_status;
     a.chunks = make_div(cache->head_dim / 8);
     a.items = make_div(cache->kv_heads * (cache->head_dim / 8));
-    // about 2048 pieces a workgroup, while that leaves 1024 workgroups
-    uint32_t per = 2048 / a.items.d;
+    // kRowAhead pieces a thread, while that leaves 1024 workgroups
+    uint32_t per = kRowThreads * kRowAhead / a.items.d;
     if (per > r->rows / 1024) per = r->rows / 1024;
     if (per < 1) per = 1;
     if (per > (uint32_t)kRowMax) per = kRowMax;
@@ -1108,6 +1235,7 @@ bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, 
     if (mass_len > all) mass_len = all;      // no sequence is longer
     p.logit_stride = ((uint64_t)mass_len + 3) & ~3ull;
     if ((double)p.logit_stride * c->batch * heads > 1e15) return false;
+    if ((p.logit_stride / kMassTokens + 1) * c->kv_heads + heads >= 1ull << 24) return false;      // k_join's grid
     p.ml_at = up16((size_t)p.runs * 2 * p.rows * c->head_dim * 4);
     p.lse2_at = up16(p.ml_at + (size_t)p.runs * 2 * p.rows * 8);
     p.logits_at = up16(p.lse2_at + (p.logit_stride ? (size_t)c->batch * heads * 4 : 0));
@@ -1227,16 +1355,12 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     else launch_attend<false>(a, P.blocks, s);
     int rc = launched();
     if (rc) return rc;
-    if (units > 1) {      // else every KV head is one run's
-        const dim3 grid(Q.heads, cache->batch);
+    // with one unit every KV head is one run's, and there is nothing to join
+    const uint32_t parts = a.logits ? (uint32_t)((P.logit_stride - 1) / kMassTokens + 1) : 0;
+    if (units > 1 || parts) {
+        const dim3 grid(Q.heads + parts * cache->kv_heads, cache->batch);
         if (bf16) k_join<true><<<grid, kJoinThreads, 0, s>>>(a);
         else k_join<false><<<grid, kJoinThreads, 0, s>>>(a);
-        rc = launched();
-        if (rc) return rc;
-    }
-    if (a.logits) {
-        const uint32_t parts = (uint32_t)((P.logit_stride - 1) / kMassThreads + 1);
-        k_mass<<<dim3(parts < 65536 ? parts : 65536, cache->kv_heads, cache->batch), kMassThreads, 0, s>>>(a);
         rc = launched();
     }
     return rc;
