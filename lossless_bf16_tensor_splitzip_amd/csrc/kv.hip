@@ -201,7 +201,7 @@ struct AttendArgs {
     uint32_t heads, group, window, sinks;
     uint32_t row_tiles, rows;     // row tiles a group is cut into, query rows a tile
     float scale2;                 // scale * log2(e): logits in base 2
-    uint32_t runs;                // workgroups of k_attend
+    uint32_t runs;                // workgroups of k_attend; 0: one for every row tile of every KV head, nothing split
     float *share_o, *share_ml;    // [runs][2] shares of [rows][dim] and [rows][2]
     float *logits;                // [batch][heads][logit_stride], by visible number (mass only)
     float *lse2;                  // [batch][heads] (mass only)
@@ -350,31 +350,46 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     const uint32_t pairs = a.c.kv_heads * a.row_tiles;     // of a sequence
 
     // this workgroup's run of units
-    Block64 blk;
-    int32_t *status0 = blockIdx.x == 0 && wave == 0 ? a.status : nullptr;
-    load_block(a, 0, 0, blk, status0);
-    uint32_t total = blk.total;
-    for (uint32_t f = 64; f < a.c.batch; f += 64) {
-        Block64 k;
-        load_block(a, f, total, k, status0);
-        total = k.total;
+    Block64 blk{};
+    Cut cut{};
+    uint32_t at = 0, u_begin = 0, u_end = 1;
+    if (a.runs) {
+        int32_t *status0 = blockIdx.x == 0 && wave == 0 ? a.status : nullptr;
+        load_block(a, 0, 0, blk, status0);
+        uint32_t total = blk.total;
+        for (uint32_t f = 64; f < a.c.batch; f += 64) {
+            Block64 k;
+            load_block(a, f, total, k, status0);
+            total = k.total;
+        }
+        cut = cut_of(total * pairs, a.runs);
+        if (blockIdx.x >= cut.runs) return;
+        u_begin = cut.begin(blockIdx.x);
+        u_end = cut.begin(blockIdx.x + 1);
+        while (blk.total * pairs <= u_begin) load_block(a, blk.first + 64, blk.total, blk, nullptr);
+        at = (uint32_t)__builtin_ctzll(__ballot(blk.upto * pairs > u_begin));    // the sequence's lane
     }
-    const Cut cut = cut_of(total * pairs, a.runs);
-    if (blockIdx.x >= cut.runs) return;
-    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = cut.begin(blockIdx.x + 1);
-    while (blk.total * pairs <= u_begin) load_block(a, blk.first + 64, blk.total, blk, nullptr);
-    uint32_t at = (uint32_t)__builtin_ctzll(__ballot(blk.upto * pairs > u_begin));    // the sequence's lane
 
     for (uint32_t u = u_begin; u < u_end;) {
-        while (at >= 64) {
-            load_block(a, blk.first + 64, blk.total, blk, nullptr);
-            at -= 64;
+        uint32_t b, n, units, pair, unit0 = 0, count;
+        if (a.runs) {
+            while (at >= 64) {
+                load_block(a, blk.first + 64, blk.total, blk, nullptr);
+                at -= 64;
+            }
+            b = blk.first + at;
+            n = __builtin_amdgcn_readlane(blk.len, at);
+            const uint32_t before = __builtin_amdgcn_readlane(blk.before, at), rel = u - before * pairs;
+            units = __builtin_amdgcn_readlane(blk.upto, at) - before;
+            pair = rel / units;
+            unit0 = rel - pair * units;
+            count = min(units - unit0, u_end - u);
+        } else {
+            b = blockIdx.x / pairs;
+            pair = blockIdx.x - b * pairs;
+            n = __builtin_amdgcn_readfirstlane(seq_len(a.c, b, pair == 0 && wave == 0 ? a.status : nullptr));
+            count = units = units_of(n, a.window, a.sinks);
         }
-        const uint32_t b = blk.first + at;
-        const uint32_t n = __builtin_amdgcn_readlane(blk.len, at), before = __builtin_amdgcn_readlane(blk.before, at);
-        const uint32_t units = __builtin_amdgcn_readlane(blk.upto, at) - before;
-        const uint32_t rel = u - before * pairs, pair = rel / units, unit0 = rel - pair * units;
-        const uint32_t count = min(units - unit0, u_end - u);
         const bool whole = count == units;
         const uint32_t h = pair / a.row_tiles, row0 = (pair - h * a.row_tiles) * a.rows;     // rows of the group
         const uint32_t rows = min(a.rows, a.group - row0), head0 = h * a.group + row0;
@@ -645,7 +660,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             }
             __syncthreads();
         }
-        u += count;
+        u += a.runs ? count : 1;
         if (pair == pairs - 1 && unit0 + count == units) ++at;
     }
 }
@@ -743,7 +758,7 @@ __device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uin
     const uint32_t t0 = part * kMassTokens + tid;
     if (part * kMassTokens >= n) return;
     Shares sh;
-    sh.sequence(a, b);
+    if (a.runs) sh.sequence(a, b);
     const float *x = a.logits + (b * (uint64_t)a.heads + h * a.group) * a.logit_stride;
     const float *in = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
     float *out = a.mass_out + b * a.mos[0] + h * a.mos[1];
@@ -765,9 +780,9 @@ __device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uin
         const uint32_t rows = min(kMassRows, a.group - r0);
         __syncthreads();
         for (uint32_t r = wave; r < rows; r += kJoinThreads / 64) {
-            sh.head(a, h, r0 + r);
+            if (a.runs) sh.head(a, h, r0 + r);
             float e;
-            if (sh.n == 1) {
+            if (!a.runs || sh.n == 1) {
                 e = a.lse2[b * (uint64_t)a.heads + h * a.group + r0 + r];
             } else {
                 float top, sum;
@@ -808,8 +823,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     __shared__ float s_w[kJoinThreads / 64][kMaxRuns];
     __shared__ f32x4 s_o[kJoinThreads];
     const uint32_t tid = threadIdx.x, wave = tid >> 6, b = blockIdx.y, head = blockIdx.x;
-    if (head >= a.heads) {
-        const uint32_t i = head - a.heads, part = i / a.c.kv_heads;
+    const uint32_t joins = a.runs ? a.heads : 0;
+    if (head >= joins) {
+        const uint32_t i = head - joins, part = i / a.c.kv_heads;
         add_mass(a, b, i - part * a.c.kv_heads, part);
         return;
     }
@@ -1245,24 +1261,24 @@ bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, 
 }
 
 template <bool BF16, int DP, int NT>
-void launch_attend(const AttendArgs &a, hipStream_t s) {
-    if (a.c.dim == DP) k_attend<BF16, DP, NT, true><<<a.runs, kAttendThreads, 0, s>>>(a);
-    else k_attend<BF16, DP, NT, false><<<a.runs, kAttendThreads, 0, s>>>(a);
+void launch_attend(const AttendArgs &a, uint32_t grid, hipStream_t s) {
+    if (a.c.dim == DP) k_attend<BF16, DP, NT, true><<<grid, kAttendThreads, 0, s>>>(a);
+    else k_attend<BF16, DP, NT, false><<<grid, kAttendThreads, 0, s>>>(a);
 }
 
 template <bool BF16>
-void launch_attend(const AttendArgs &a, uint32_t blocks, hipStream_t s) {
+void launch_attend(const AttendArgs &a, uint32_t blocks, uint32_t grid, hipStream_t s) {
     const uint32_t d = (a.c.dim + 63) / 64;
     if (blocks == 1) {
-        if (d == 1) launch_attend<BF16, 64, 1>(a, s);
-        else if (d == 2) launch_attend<BF16, 128, 1>(a, s);
-        else if (d == 3) launch_attend<BF16, 192, 1>(a, s);
-        else launch_attend<BF16, 256, 1>(a, s);
+        if (d == 1) launch_attend<BF16, 64, 1>(a, grid, s);
+        else if (d == 2) launch_attend<BF16, 128, 1>(a, grid, s);
+        else if (d == 3) launch_attend<BF16, 192, 1>(a, grid, s);
+        else launch_attend<BF16, 256, 1>(a, grid, s);
     } else {
-        if (d == 1) launch_attend<BF16, 64, 2>(a, s);
-        else if (d == 2) launch_attend<BF16, 128, 2>(a, s);
-        else if (d == 3) launch_attend<BF16, 192, 2>(a, s);
-        else launch_attend<BF16, 256, 2>(a, s);
+        if (d == 1) launch_attend<BF16, 64, 2>(a, grid, s);
+        else if (d == 2) launch_attend<BF16, 128, 2>(a, grid, s);
+        else if (d == 3) launch_attend<BF16, 192, 2>(a, grid, s);
+        else launch_attend<BF16, 256, 2>(a, grid, s);
     }
 }
 
@@ -1347,18 +1363,24 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     const uint64_t window = (uint64_t)Q.window + Q.sinks;
     const uint64_t seen = Q.window == SPLITZIP_KV_ALL || window > a.c.max_len ? a.c.max_len : window;
     const uint32_t units = seen ? (uint32_t)((seen - 1) / kUnit + 1) : 1;
-    const uint64_t most = (uint64_t)units * cache->batch * cache->kv_heads * P.row_tiles;
-    a.runs = most < P.runs ? (uint32_t)most : P.runs;
+    // Whole, with few units a KV head: no join (5 us), no search for the run's
+    // place.  Split/whole in us, KV heads by units (dim 128, batches of equal and
+    // of ragged lengths): 64 x 2 11.1/9.6 and 10.8/9.0, 64 x 4 11.7/14.5 and
+    // 11.1/13.5, 256 x 4 22.0/16.8 and 14.3/14.0, 256 x 8 33.4/28.5 and 17.0/23.7,
+    // 2048 x 4 107/98 and 50/38, 2048 x 32 666/727 and 132/161.
+    const uint64_t tiles = (uint64_t)cache->batch * cache->kv_heads * P.row_tiles;
+    const bool whole = units <= 2 || (units <= 4 && tiles >= 256);
+    a.runs = whole ? 0 : tiles * units < P.runs ? (uint32_t)(tiles * units) : P.runs;
+    const uint32_t grid_x = a.runs ? a.runs : (uint32_t)tiles;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = cache->dtype == SPLITZIP_KV_BF16;
-    if (bf16) launch_attend<true>(a, P.blocks, s);
-    else launch_attend<false>(a, P.blocks, s);
+    if (bf16) launch_attend<true>(a, P.blocks, grid_x, s);
+    else launch_attend<false>(a, P.blocks, grid_x, s);
     int rc = launched();
     if (rc) return rc;
-    // with one unit every KV head is one run's, and there is nothing to join
     const uint32_t parts = a.logits ? (uint32_t)((P.logit_stride - 1) / kMassTokens + 1) : 0;
-    if (units > 1 || parts) {
-        const dim3 grid(Q.heads + parts * cache->kv_heads, cache->batch);
+    if (a.runs || parts) {
+        const dim3 grid((a.runs ? Q.heads : 0) + parts * cache->kv_heads, cache->batch);
         if (bf16) k_join<true><<<grid, kJoinThreads, 0, s>>>(a);
         else k_join<false><<<grid, kJoinThreads, 0, s>>>(a);
         rc = launched();
@@ -1404,7 +1426,9 @@ int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *t
     a.mass_len = B.mass_len;
     a.status = d_status;
     const uint32_t pieces = cache->head_dim / 8;
-    a.chunk = pieces < 8 ? pieces : 8;
+    // columns of 256 bytes; in place, where a column is one workgroup's, of 128
+    const uint32_t wide = share ? 8 : 16;
+    a.chunk = pieces < wide ? pieces : wide;
     a.chunks = (pieces + a.chunk - 1) / a.chunk;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const dim3 heads(cache->kv_heads, cache->batch);
