@@ -68,6 +68,11 @@ __device__ inline bool locate(const Cache &c, uint32_t b, uint32_t t, uint32_t &
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// Until every vector memory operation this wave issued has completed.
+// (The builtin, which the compiler counts; after an asm it would wait again
+// before every load into a register that a store has read.)
+__device__ inline void wait_vector_memory() { __builtin_amdgcn_s_waitcnt(0); }
+
 // 16 bytes that nothing reads again soon.
 __device__ inline u32x4 load_once(const uint16_t *p) { return __builtin_nontemporal_load((const u32x4 *)p); }
 __device__ inline void store_away(uint16_t *p, u32x4 x) { __builtin_nontemporal_store(x, (u32x4 *)p); }
@@ -88,10 +93,11 @@ struct RowArgs {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowMax = 64;      // rows a workgroup
-constexpr int kRowAhead = 4;
 
 // A workgroup copies per_wg rows: one thread per row finds its place, then
 // all threads copy 16-byte pieces, neighbouring threads neighbouring pieces.
+// Memory bounds it: 268 MB move in 48 us (5.6 TB/s), with loads and stores that
+// leave the caches alone where nothing reads the bytes again soon.
 template <bool GATHER>
 __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
     __shared__ uint64_t at_k[kRowMax], at_v[kRowMax];
@@ -128,34 +134,19 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
         }
         __syncthreads();
         const uint32_t total = count * a.items.d;
-        // kRowAhead pieces of each pool a time, so that as many loads are under way
-        for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kRowThreads * kRowAhead) {
-            u32x4 xk[kRowAhead], xv[kRowAhead];
-            uint16_t *tk[kRowAhead], *tv[kRowAhead];
-#pragma unroll
-            for (int u = 0; u < kRowAhead; ++u) {
-                const uint32_t i = i0 + u * kRowThreads;
-                tk[u] = nullptr;
-                if (i >= total) continue;
-                const uint32_t r = div(i, a.items), j = i - r * a.items.d;
-                const uint32_t h = div(j, a.chunks), d = (j - h * a.chunks.d) * 8;
-                if (at_k[r] == kNone) continue;
-                uint16_t *pk = a.c.k + at_k[r] + h * a.c.ks[1] + d;
-                uint16_t *pv = a.c.v + at_v[r] + h * a.c.vs[1] + d;
-                uint16_t *rk = a.k + (uint64_t)(r0 + r) * a.ks[0] + h * a.ks[1] + d;
-                uint16_t *rv = a.v + (uint64_t)(r0 + r) * a.vs[0] + h * a.vs[1] + d;
-                // pages are read for this once, new rows may still be in a cache
-                xk[u] = GATHER ? load_once(pk) : *(const u32x4 *)rk;
-                xv[u] = GATHER ? load_once(pv) : *(const u32x4 *)rv;
-                tk[u] = GATHER ? rk : pk;
-                tv[u] = GATHER ? rv : pv;
-            }
-#pragma unroll
-            for (int u = 0; u < kRowAhead; ++u)
-                if (tk[u]) {
-                    store_away(tk[u], xk[u]);
-                    store_away(tv[u], xv[u]);
-                }
+        for (uint32_t i = threadIdx.x; i < total; i += kRowThreads) {
+            const uint32_t r = div(i, a.items), j = i - r * a.items.d;
+            const uint32_t h = div(j, a.chunks), d = (j - h * a.chunks.d) * 8;
+            if (at_k[r] == kNone) continue;
+            uint16_t *pk = a.c.k + at_k[r] + h * a.c.ks[1] + d;
+            uint16_t *pv = a.c.v + at_v[r] + h * a.c.vs[1] + d;
+            uint16_t *rk = a.k + (uint64_t)(r0 + r) * a.ks[0] + h * a.ks[1] + d;
+            uint16_t *rv = a.v + (uint64_t)(r0 + r) * a.vs[0] + h * a.vs[1] + d;
+            // pages are read for this once, new rows may still be in a cache
+            const u32x4 xk = GATHER ? load_once(pk) : *(const u32x4 *)rk;
+            const u32x4 xv = GATHER ? load_once(pv) : *(const u32x4 *)rv;
+            store_away(GATHER ? rk : pk, xk);
+            store_away(GATHER ? rv : pv, xv);
         }
         __syncthreads();
     }
@@ -466,6 +457,13 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             __builtin_amdgcn_wave_barrier();      // the wave's own LDS: in order without a wait
             return (uint32_t)__ballot(ok);
         };
+        // Rows of whole cache lines pass the caches by (32 sequences of 32768 tokens
+        // 644 us, through them 718); others share lines with their neighbours and
+        // go through them (dim 80, 16 x 8192 tokens: 85 us, past them 113).
+        auto load_kv = [](const uint16_t *p) { return EXACT ? load_once(p) : *(const u32x4 *)p; };
+        auto load_kv8 = [](const uint16_t *p) {
+            return EXACT ? __builtin_nontemporal_load((const u32x2 *)p) : *(const u32x2 *)p;
+        };
         u32x4 kr[2][KS];
         u32x4 v16[8][P16 ? P16 : 1];
         u32x2 v8[8];
@@ -476,7 +474,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                 const uint64_t off = off_k[wave][buf][s * 16 + c16];
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
-                    kr[s][j] = load_once(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
+                    kr[s][j] = load_kv(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
             }
         };
         auto load_v = [&](int buf) {
@@ -484,8 +482,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (int i = 0; i < 8; ++i) {
                 const uint64_t off = off_v[wave][buf][(i >> 2) * 16 + g * 4 + (i & 3)];
 #pragma unroll
-                for (int p = 0; p < P16; ++p) v16[i][p] = load_once(v_lane[p] + off);
-                if constexpr (P8 > 0) v8[i] = __builtin_nontemporal_load((const u32x2 *)(v_lane[P16] + off));
+                for (int p = 0; p < P16; ++p) v16[i][p] = load_kv(v_lane[p] + off);
+                if constexpr (P8 > 0) v8[i] = load_kv8(v_lane[P16] + off);
             }
         };
 
@@ -1061,16 +1059,26 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
 }
 
 constexpr int kMoveThreads = 512;
-constexpr int kMoveUnroll = 4;
-constexpr uint32_t kMaxMoveParts = 65536;
+// Rows a thread moves at a time: apart from the source, where workgroups are
+// many, and in place, where one has a whole column (32000 of 32768 tokens kept,
+// 8 KV heads: 218 us with 2, 145 with 4, 111 with 8).
+constexpr int kMoveApart = 4, kMoveInPlace = 8;
+constexpr uint32_t kMoveParts = 65536;
+constexpr uint32_t kMoveRows = 64;      // most rows side by side in a workgroup
+__host__ __device__ inline uint32_t move_rows(uint32_t chunk) { return kMoveThreads / chunk < kMoveRows ? kMoveThreads / chunk : kMoveRows; }
 
 // A workgroup moves a column of one pool: `chunk` 16-byte pieces of the rows
-// of a sequence's KV head. Row i comes from row kept[i] >= i, so within a
+// of a sequence's KV head.  Row i comes from row kept[i] >= i, so within a
 // column, step by step upwards, a step's writes can only meet sources of the
 // step itself: they wait until all its loads have arrived (the barrier), and
-// steps need no other order. Columns share nothing.
+// steps need no other order.  Columns share nothing.  Memory bounds it where
+// there are workgroups enough: 16 x 4096 tokens of 8 heads of 128 to half,
+// 268 MB, in 50 us.  In place with few columns a step's three loads in turn do
+// (one sequence of 32768 tokens of 8 heads to 8192 in 62 us, selection included);
+// looking the next step's places up ahead gained nothing.
+template <bool LINES, int U>
 __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
-    __shared__ uint64_t from[kMoveThreads * kMoveUnroll], dest[kMoveThreads * kMoveUnroll];
+    __shared__ uint64_t from[kMoveRows * U], dest[kMoveRows * U];
     const uint32_t b = blockIdx.z, tid = threadIdx.x;
     const uint32_t h = blockIdx.y / (2 * a.chunks), col = blockIdx.y % (2 * a.chunks);
     const bool is_v = col >= a.chunks;
@@ -1080,44 +1088,50 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
     const uint16_t *src = (is_v ? a.c.v : a.c.k) + h * (is_v ? a.c.vs[1] : a.c.ks[1]) + piece0 * 8;
     uint16_t *dst = (is_v ? a.to.v : a.to.k) + h * (is_v ? a.to.vs[1] : a.to.ks[1]) + piece0 * 8;
     const int32_t *kept = a.kept + ((uint64_t)b * a.c.kv_heads + h) * a.budget;
-    const uint32_t lane_rows = kMoveThreads / a.chunk, step = lane_rows * kMoveUnroll;
+    const uint32_t lane_rows = move_rows(a.chunk), step = lane_rows * U;
     const uint32_t row = tid / a.chunk, piece = tid % a.chunk;
-    const uint64_t begin = (uint64_t)blockIdx.x * a.per_wg;
-    const uint32_t end = (uint32_t)min((uint64_t)n, begin + a.per_wg);
-    const bool same = a.to.k == a.c.k;
+    const uint64_t begin = (uint64_t)blockIdx.x * a.per_wg, end = min((uint64_t)n, begin + a.per_wg);
+    const bool same = a.to.k == a.c.k, mine = row < lane_rows && piece < width;
     constexpr uint64_t kNone = ~0ull;
+    static_assert(kMoveRows * U <= kMoveThreads, "a thread per row of a step");
     for (uint64_t i0 = begin; i0 < end; i0 += step) {
-        for (uint32_t j = tid; j < step; j += kMoveThreads) {
+        if (tid < step) {
             uint64_t f = kNone, d = kNone;
-            if (i0 + j < end) {
-                const uint32_t i = (uint32_t)(i0 + j), t = (uint32_t)kept[i];
+            if (i0 + tid < end) {
+                const uint32_t i = (uint32_t)(i0 + tid), t = (uint32_t)kept[i];
                 uint32_t p0, s0, p1, s1;
-                if (locate(a.c, b, t, p0, s0) && locate(a.to, b, i, p1, s1)) {
-                    if (!(same && t == i)) {
-                        f = p0 * (is_v ? a.c.vs[0] : a.c.ks[0]) + s0 * (is_v ? a.c.vs[2] : a.c.ks[2]);
-                        d = p1 * (is_v ? a.to.vs[0] : a.to.ks[0]) + s1 * (is_v ? a.to.vs[2] : a.to.ks[2]);
-                    }
-                } else {
+                const bool here = locate(a.c, b, t, p0, s0), there = locate(a.to, b, i, p1, s1);
+                if (!here || !there) {
                     report(a.status, SPLITZIP_KV_BAD_PAGE);
+                } else if (!(same && t == i)) {
+                    f = p0 * (is_v ? a.c.vs[0] : a.c.ks[0]) + s0 * (is_v ? a.c.vs[2] : a.c.ks[2]);
+                    d = p1 * (is_v ? a.to.vs[0] : a.to.ks[0]) + s1 * (is_v ? a.to.vs[2] : a.to.ks[2]);
                 }
             }
-            from[j] = f;
-            dest[j] = d;
+            from[tid] = f;
+            dest[tid] = d;
         }
         __syncthreads();
-        u32x4 x[kMoveUnroll];
-        bool ok[kMoveUnroll];
+        u32x4 x[U];
+        bool ok[U];
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const uint32_t j = u * lane_rows + row;
-            ok[u] = row < lane_rows && piece < width && from[j] != kNone;
-            if (ok[u]) x[u] = load_once(src + from[j] + piece * 8);
+            ok[u] = mine && from[j] != kNone;
+            if (ok[u]) {
+                const uint16_t *p = src + from[j] + piece * 8;
+                x[u] = LINES ? load_once(p) : *(const u32x4 *)p;
+            }
         }
-        __builtin_amdgcn_s_waitcnt(0);
+        wait_vector_memory();
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u)
-            if (ok[u]) store_away(dst + dest[u * lane_rows + row] + piece * 8, x[u]);
+        for (int u = 0; u < U; ++u)
+            if (ok[u]) {
+                uint16_t *p = dst + dest[u * lane_rows + row] + piece * 8;
+                if (LINES) store_away(p, x[u]);
+                else *(u32x4 *)p = x[u];
+            }
         __syncthreads();
     }
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.to.lens[b] = (int32_t)n;
@@ -1162,7 +1176,7 @@ bool cache_ok(const splitzip_kv_cache *c) {
     }
     if (ke + c->head_dim > kMaxOffset || ve + c->head_dim > kMaxOffset) return false;
     return c->batch == 0 || (c->lens && aligned(c->lens, 4) && aligned(c->table, 4) && (c->table || c->max_pages == 0) &&
-                             (c->batch == 1 || c->table_stride >= c->max_pages) && c->table_stride <= kMaxOffset / 65536);
+                             (c->batch == 1 || c->table_stride >= c->max_pages) && c->table_stride <= kMaxOffset);
 }
 
 Cache view(const splitzip_kv_cache *c) {
@@ -1211,9 +1225,9 @@ int copy_rows(const splitzip_kv_cache *cache, const splitzip_kv_rows *r, int32_t
     a.status = d_status;
     a.chunks = make_div(cache->head_dim / 8);
     a.items = make_div(cache->kv_heads * (cache->head_dim / 8));
-    // kRowAhead pieces a thread, while that leaves 1024 workgroups
-    uint32_t per = kRowThreads * kRowAhead / a.items.d;
-    if (per > r->rows / 1024) per = r->rows / 1024;
+    // One piece of each pool a thread: 32768 rows of 8 x 128 gathered in 48 us
+    // with one, 53 with two, 57 with four.
+    uint32_t per = kRowThreads / a.items.d;
     if (per < 1) per = 1;
     if (per > (uint32_t)kRowMax) per = kRowMax;
     a.per_wg = per;
@@ -1232,8 +1246,11 @@ struct AttendPlan {
     size_t ml_at, lse2_at, logits_at, bytes;
 };
 
-constexpr uint32_t kRuns = 512;      // two workgroups on each of 256 compute units
-static_assert(kRuns <= kMaxRuns, "the join holds one weight per run");
+// As many runs as workgroups are resident on 256 compute units: registers allow
+// three to dim 64, two above (from dim 129 on only one fits, and the second
+// follows).  Batch 16, 8192 tokens: dim 64 122 us with 512 runs, 113 with 768,
+// 124 with 1024; dim 128 103, 108, 102; dim 256 97, 104, 105.
+inline uint32_t runs_for(uint32_t dim) { return dim <= 64 ? 768 : 512; }
 
 inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
@@ -1247,7 +1264,7 @@ bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, 
     const uint32_t all = c->max_pages * c->page_size;
     const uint64_t units = (uint64_t)(all ? (all - 1) / kUnit + 1 : 1) * c->batch * c->kv_heads * p.row_tiles;
     if (units >> 31) return false;
-    p.runs = units < kRuns ? (uint32_t)units : kRuns;
+    p.runs = units < runs_for(c->head_dim) ? (uint32_t)units : runs_for(c->head_dim);
     if (mass_len > all) mass_len = all;      // no sequence is longer
     p.logit_stride = ((uint64_t)mass_len + 3) & ~3ull;
     if ((double)p.logit_stride * c->batch * heads > 1e15) return false;
@@ -1282,7 +1299,7 @@ void launch_attend(const AttendArgs &a, uint32_t blocks, uint32_t grid, hipStrea
     }
 }
 
-bool mass_strides_ok(const uint64_t s[2]) { return s[0] <= kMaxOffset / 65536 && s[1] <= kMaxOffset / 65536; }
+bool mass_strides_ok(const uint64_t s[2]) { return s[0] <= kMaxOffset && s[1] <= kMaxOffset; }
 
 }  // namespace
 
@@ -1316,10 +1333,10 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     if (!cache_ok(cache) || !query || (d_status && !aligned(d_status, 4))) return SPLITZIP_ERR_INVALID;
     const splitzip_kv_query &Q = *query;
     AttendPlan P;
-    if (!attend_plan(cache, Q.heads, Q.mass_out ? Q.mass_len : 0, P) || !(Q.scale - Q.scale == 0.f))
-        return SPLITZIP_ERR_INVALID;      // also a scale that is not finite
+    if (!attend_plan(cache, Q.heads, Q.mass_out ? Q.mass_len : 0, P) || !(Q.scale * kLog2e - Q.scale * kLog2e == 0.f))
+        return SPLITZIP_ERR_INVALID;      // also a scale that is not finite in base 2
     for (int i = 0; i < 2; ++i)
-        if (Q.q_stride[i] % 8 || Q.out_stride[i] % 8 || Q.q_stride[i] > kMaxOffset / 65536 || Q.out_stride[i] > kMaxOffset / 65536)
+        if (Q.q_stride[i] % 8 || Q.out_stride[i] % 8 || Q.q_stride[i] > kMaxOffset || Q.out_stride[i] > kMaxOffset)
             return SPLITZIP_ERR_INVALID;
     if (!mass_strides_ok(Q.mass_stride) || !mass_strides_ok(Q.mass_out_stride) || (Q.mass && !Q.mass_out) ||
         !aligned(Q.mass, 4) || !aligned(Q.mass_out, 4) || !aligned(Q.lse, 4))
@@ -1369,7 +1386,7 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     // 11.1/13.5, 256 x 4 22.0/16.8 and 14.3/14.0, 256 x 8 33.4/28.5 and 17.0/23.7,
     // 2048 x 4 107/98 and 50/38, 2048 x 32 666/727 and 132/161.
     const uint64_t tiles = (uint64_t)cache->batch * cache->kv_heads * P.row_tiles;
-    const bool whole = units <= 2 || (units <= 4 && tiles >= 256);
+    const bool whole = tiles < 1u << 24 && (units <= 2 || (units <= 4 && tiles >= 256));      // a grid's limit
     a.runs = whole ? 0 : tiles * units < P.runs ? (uint32_t)(tiles * units) : P.runs;
     const uint32_t grid_x = a.runs ? a.runs : (uint32_t)tiles;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -1442,13 +1459,19 @@ int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *t
     uint32_t parts = 1;
     a.per_wg = most ? most : 1;
     if (!share) {
-        const uint32_t step = kMoveThreads / a.chunk * kMoveUnroll;
+        const uint32_t step = move_rows(a.chunk) * kMoveApart;
         const uint32_t steps = most ? (most - 1) / step + 1 : 1;
-        a.per_wg = (steps - 1) / kMaxMoveParts + 1;
+        a.per_wg = (steps - 1) / kMoveParts + 1;
         parts = (steps - 1) / a.per_wg + 1;
         a.per_wg *= step;
     }
-    k_move<<<dim3(parts, cache->kv_heads * 2 * a.chunks, cache->batch), kMoveThreads, 0, s>>>(a);
+    const dim3 grid(parts, cache->kv_heads * 2 * a.chunks, cache->batch);
+    // Apart, rows of whole cache lines pass the caches by, as in k_attend; what is
+    // moved in place stays in them (through them 75 us, past them 87: 64 x 4096 to
+    // 4000 tokens of 8 heads).
+    if (share) k_move<false, kMoveInPlace><<<grid, kMoveThreads, 0, s>>>(a);
+    else if (cache->head_dim % 64 == 0) k_move<true, kMoveApart><<<grid, kMoveThreads, 0, s>>>(a);
+    else k_move<false, kMoveApart><<<grid, kMoveThreads, 0, s>>>(a);
     return launched();
 }
 

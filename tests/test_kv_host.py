@@ -86,9 +86,10 @@ def test_bad_rows_are_refused(over):
 
 
 @pytest.mark.parametrize("over", [dict(q=0), dict(q=0x10008), dict(out=0), dict(out=0x20004), dict(q_stride0=4),
-                                  dict(out_stride1=1 << 30), dict(heads=0), dict(heads=12), dict(heads=65536),
+                                  dict(out_stride1=1 << 41), dict(heads=0), dict(heads=12), dict(heads=65536),
                                   dict(lse=0x7001), dict(mass=0x7000), dict(mass_out=0x7002),
-                                  dict(scale=float("nan")), dict(scale=float("inf"))], ids=str)
+                                  dict(scale=float("nan")), dict(scale=float("inf")),
+                                  dict(scale=3e38)], ids=str)
 def test_bad_queries_are_refused(over):
     assert _abi.splitzip_kv_attend(cache(), query(**over), 0x8000, 1 << 40, 0, 0) == _abi.ERR_INVALID
 
@@ -113,7 +114,7 @@ def test_workspace_and_status_are_checked():
 
 @pytest.mark.parametrize("over", [dict(mass=0), dict(mass=0x10002), dict(mass_out=0x10001), dict(kept=0),
                                   dict(kept=0x9002), dict(budget=0), dict(budget=1 << 31), dict(sinks=33),
-                                  dict(sinks=20, recent=13), dict(recent=0xFFFFFFFF), dict(mass_stride0=1 << 30)],
+                                  dict(sinks=20, recent=13), dict(recent=0xFFFFFFFF), dict(mass_stride0=1 << 41)],
                          ids=str)
 def test_bad_budgets_are_refused(over):
     assert _abi.splitzip_kv_evict(cache(), cache(), budget(**over), 0, 0) == _abi.ERR_INVALID
