@@ -1246,25 +1246,35 @@ struct AttendPlan {
     size_t ml_at, lse2_at, logits_at, bytes;
 };
 
-// As many runs as workgroups are resident on 256 compute units: registers allow
-// three to dim 64, two above (from dim 129 on only one fits, and the second
-// follows).  Batch 16, 8192 tokens: dim 64 122 us with 512 runs, 113 with 768,
-// 124 with 1024; dim 128 103, 108, 102; dim 256 97, 104, 105.
-inline uint32_t runs_for(uint32_t dim) { return dim <= 64 ? 768 : 512; }
+// As many runs as workgroups are resident on 256 compute units, which the
+// registers of k_attend decide.  16 sequences of 8192 tokens, us: dim 64 122
+// with 512 runs, 113 with 768, 124 with 1024; dim 128 103, 108, 102; dim 256
+// 97 with 256, 100 with 512, 104 with 768; 2 sequences, dim 256 21 and 27.
+inline uint32_t runs_for(uint32_t dim, uint32_t blocks) {
+    return dim <= 64 ? (blocks == 1 ? 768 : blocks == 2 ? 512 : 256) : dim <= 128 && blocks == 1 ? 512 : 256;
+}
 
 inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, AttendPlan &p) {
     if (heads == 0 || heads > SPLITZIP_KV_MAX_HEADS || heads % c->kv_heads) return false;
     p.group = heads / c->kv_heads;
-    p.row_tiles = (p.group - 1) / 32 + 1;
+    const uint32_t all = c->max_pages * c->page_size;
+    const uint64_t kv_units = (uint64_t)(all ? (all - 1) / kUnit + 1 : 1) * c->batch * c->kv_heads;
+    // K and V are read once for every row tile: of 64 rows, or 32 where the
+    // accumulators of 64 would not fit the registers, or where there is so little
+    // to read that more and shorter workgroups win (64 rows against 32, dim 128,
+    // 64 rows a KV head, us: 256 units 20 and 16, 512 25 and 23, 768 35.2 and
+    // 34.2, 8192 133 and 201).
+    const uint32_t most = c->head_dim <= 128 && kv_units >= 1024 ? 64 : 32;
+    p.row_tiles = (p.group - 1) / most + 1;
     p.rows = (p.group - 1) / p.row_tiles + 1;
     p.row_tiles = (p.group - 1) / p.rows + 1;
-    p.blocks = p.rows > 16 ? 2 : 1;
-    const uint32_t all = c->max_pages * c->page_size;
-    const uint64_t units = (uint64_t)(all ? (all - 1) / kUnit + 1 : 1) * c->batch * c->kv_heads * p.row_tiles;
+    p.blocks = p.rows > 32 ? 4 : p.rows > 16 ? 2 : 1;
+    const uint64_t units = kv_units * p.row_tiles;
     if (units >> 31) return false;
-    p.runs = units < runs_for(c->head_dim) ? (uint32_t)units : runs_for(c->head_dim);
+    const uint32_t runs = runs_for(c->head_dim, p.blocks);
+    p.runs = units < runs ? (uint32_t)units : runs;
     if (mass_len > all) mass_len = all;      // no sequence is longer
     p.logit_stride = ((uint64_t)mass_len + 3) & ~3ull;
     if ((double)p.logit_stride * c->batch * heads > 1e15) return false;
@@ -1291,6 +1301,9 @@ void launch_attend(const AttendArgs &a, uint32_t blocks, uint32_t grid, hipStrea
         else if (d == 2) launch_attend<BF16, 128, 1>(a, grid, s);
         else if (d == 3) launch_attend<BF16, 192, 1>(a, grid, s);
         else launch_attend<BF16, 256, 1>(a, grid, s);
+    } else if (blocks == 4) {
+        if (d == 1) launch_attend<BF16, 64, 4>(a, grid, s);
+        else launch_attend<BF16, 128, 4>(a, grid, s);
     } else {
         if (d == 1) launch_attend<BF16, 64, 2>(a, grid, s);
         else if (d == 2) launch_attend<BF16, 128, 2>(a, grid, s);

@@ -85,6 +85,19 @@ def test_pages(page, layout):
     check(R.to_gpu(m, S))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,group", [(8, 3), (64, 1), (64, 20), (64, 50), (80, 4), (80, 64), (128, 1), (128, 16),
+                                       (128, 31), (128, 33), (128, 64), (128, 70), (192, 2), (192, 32), (256, 1),
+                                       (256, 17), (256, 40)])
+def test_tables_far_wider_than_the_sequences(dim, group, dtype):
+    """A serving loop's table: what it could hold decides how the work is cut,
+    what it holds is short, ragged or nothing."""
+    _say("attend wide table dim=%d group=%d %s" % (dim, group, dtype))
+    m = R.make([0, 1, 300, 31, 0, 700, 129, 2], 2, dim, 16, dtype, layout="nhd", heads=2 * group, seed=group, width=600)
+    check(R.to_gpu(m, S))
+    check(m, window=200, sinks=5, want_mass=False)
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (0, 4), (1, 0), (1, 1), (16, 4), (100, 0), (100, 33), (128, 64),
                                           (511, 1), (512, 4), (2 ** 31 - 1, 5), (7, 2 ** 31 - 1), (None, 9)])
 def test_windows(window, sinks):
