@@ -84,6 +84,17 @@ def _no_grad(t: torch.Tensor, what: str) -> None:
         raise ValueError("the %s requires a gradient, and the cache computes none" % what)
 
 
+def _fixed(name: str):
+    def get(self):
+        return self._tensors[name]
+
+    def put(self, value):
+        if value is not self._tensors[name]:
+            raise ValueError("the cache's %s stays the tensor it was made with: copy into it" % name)
+
+    return property(get, put)
+
+
 class KVCache:
     """A paged cache: K and V pools [pages, kv_heads, page_size, head_dim]
     (bfloat16 or float16, last dimension contiguous, other strides multiples
@@ -113,7 +124,7 @@ class KVCache:
             _no_overlap(t, what)
             _no_grad(t, what)
         _same_gpu(k_pages.device, v_pages, table, lens)
-        self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
+        self._tensors = {"k_pages": k_pages, "v_pages": v_pages, "table": table, "lens": lens}
         self.device, self.dtype = k_pages.device, k_pages.dtype
         self.batch, self.max_pages = table.shape
         self.kv_heads, self.page_size, self.head_dim = kv_heads, page_size, dim
@@ -124,6 +135,11 @@ class KVCache:
                                      _DTYPES[self.dtype], 0)
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
+        self._row, self._cu = (kv_heads, dim), (self.batch + 1,)
+
+    # The kernels are given these tensors' memory once: in-place changes reach
+    # them (cache.lens += 1, cache.table.copy_(...)), other tensors do not.
+    k_pages, v_pages, table, lens = (_fixed(name) for name in ("k_pages", "v_pages", "table", "lens"))
 
     def _call(self, fn: str, stream, *args):
         call = getattr(_abi.kv_lib(), fn)
@@ -140,17 +156,27 @@ class KVCache:
             raise ValueError("the %s must be on %s, got %s" % (what, self.device, t.device))
 
     def _rows(self, k, v, cu, start, written: bool):
-        grad = torch.is_grad_enabled()
+        size = k.shape
+        if not (k.dtype is v.dtype is self.dtype and size == v.shape and len(size) == 3 and size[1:] == self._row and
+                k.device == v.device == cu.device == self.device and cu.dtype is torch.int32 and cu.shape == self._cu and
+                start is None and cu.is_contiguous() and not (k.requires_grad or v.requires_grad)):
+            self._check_rows(k, v, cu, start)
+        kp, k0, k1 = _place(k, "K rows", written)
+        vp, v0, v1 = _place(v, "V rows", written)
+        return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, size[0], 0, cu.data_ptr(),
+                                        None if start is None else start.data_ptr()))
+
+    def _check_rows(self, k, v, cu, start):
+        """The same one by one, for what the quick look is not content with."""
         for t, what in ((k, "K rows"), (v, "V rows")):
             if t.is_cuda:
                 self._here(t, what)
             else:
                 _device_or_pinned(t, what)
-            if t.dtype is not self.dtype or t.dim() != 3 or t.shape[1] != self.kv_heads or t.shape[2] != self.head_dim:
+            if t.dtype is not self.dtype or t.dim() != 3 or tuple(t.shape[1:]) != self._row:
                 raise ValueError("the %s must be %s [rows, %d, %d], got %s %s"
-                                 % (what, self.dtype, self.kv_heads, self.head_dim, t.dtype, tuple(t.shape)))
-            if grad:
-                _no_grad(t, what)
+                                 % ((what, self.dtype) + self._row + (t.dtype, tuple(t.shape))))
+            _no_grad(t, what)
         if k.shape[0] != v.shape[0]:
             raise ValueError("K and V must have the same number of rows")
         for t, n, what in ((cu, self.batch + 1, "row ranges"), (start, self.batch, "first positions")):
@@ -160,10 +186,6 @@ class KVCache:
             self._here(t, what)
             if t.shape[0] != n or not t.is_contiguous():
                 raise ValueError("the %s need %d contiguous entries" % (what, n))
-        kp, k0, k1 = _place(k, "K rows", written)
-        vp, v0, v1 = _place(v, "V rows", written)
-        return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, k.shape[0], 0, cu.data_ptr(),
-                                        None if start is None else start.data_ptr()))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, start: torch.Tensor | None = None,
                status: torch.Tensor | None = None, stream=None) -> None:
@@ -232,15 +254,16 @@ class KVCache:
         weight every token received, summed over its KV head's query heads, is
         added to it: in place, or into ``mass_out``, whose entries up to the
         length are all written (with ``mass_out`` alone, starting from 0)."""
-        if q.dtype is not self.dtype or q.dim() != 3 or q.shape[0] != self.batch or q.shape[2] != self.head_dim:
+        size, dev = q.shape, self.device
+        if q.dtype is not self.dtype or len(size) != 3 or size[0] != self.batch or size[2] != self.head_dim:
             raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
-                             % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(q.shape)))
-        self._here(q, "queries")
-        self._here(ws.buf, "workspace")
-        grad = torch.is_grad_enabled()
-        if grad:
+                             % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(size)))
+        if not q.device == ws.buf.device == dev:
+            self._here(q, "queries")
+            self._here(ws.buf, "workspace")
+        if q.requires_grad:
             _no_grad(q, "queries")
-        heads = q.shape[1]
+        heads = size[1]
         if heads < 1 or heads % self.kv_heads:
             raise ValueError("%d query heads do not divide over %d KV heads" % (heads, self.kv_heads))
         if window is None:
@@ -250,10 +273,11 @@ class KVCache:
         if not 0 <= sinks < 1 << 31:
             raise ValueError("the sinks must be in 0..2^31-1, got %d" % sinks)
         if out is not None:
-            if out.dtype is not self.dtype or out.shape != q.shape:
+            if out.dtype is not self.dtype or out.shape != size:
                 raise ValueError("the output must be shaped like the queries")
-            self._here(out, "output")
-            if grad:
+            if out.device != dev:
+                self._here(out, "output")
+            if out.requires_grad:
                 _no_grad(out, "output")
         if lse is not None:
             _plain(lse, torch.float32, 2, "lse")
@@ -268,7 +292,7 @@ class KVCache:
         qp, q0, q1 = _place(q, "queries", False)
         if out is None:
             with torch.cuda.stream(stream):
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+                out = torch.empty(size, dtype=q.dtype, device=dev)
         op, o0, o1 = _place(out, "output", True)
         query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), mass_in, mass_to, *ms, *mos,
                              heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale, mass_len, 0)

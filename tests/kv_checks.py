@@ -41,6 +41,13 @@ def caches(new, to_gpu, runs):
     k.requires_grad_(False)
 
 
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, seed=1))
+    m.cache.lens += 1                                                     # in place: the same tensor
+    assert m.cache.lens is m.glens and m.glens.tolist() == [21, 4]
+    for name in ("lens", "table", "k_pages", "v_pages"):
+        refused(setattr, m.cache, name, getattr(m.cache, name).clone())
+
+
 def rows(new, to_gpu, runs):
     m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
     k = new(torch.zeros, 4, 2, 64, dtype=torch.bfloat16)
