@@ -24,6 +24,7 @@ from .codec import _device_or_pinned, _same_gpu, _status_ptr
 
 _DTYPES = {torch.bfloat16: _abi.KV_BF16, torch.float16: _abi.KV_FP16}
 _raw_stream = torch._C._cuda_getCurrentRawStream     # an int, without making a Stream object
+_NO_MASS = (None, None, 0, 0, 0, 0, 0)
 
 
 def _strides(t: torch.Tensor, what: str, multiple: int = 8):
@@ -135,7 +136,8 @@ class KVCache:
                                      _DTYPES[self.dtype], 0)
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
-        self._row, self._cu = (kv_heads, dim), (self.batch + 1,)
+        self._row, self._cu, self._heads = (kv_heads, dim), (self.batch + 1,), (self.batch, kv_heads)
+        self._shape = (self.batch, kv_heads, dim, self.dtype, self.device)
 
     # The kernels are given these tensors' memory once: in-place changes reach
     # them (cache.lens += 1, cache.table.copy_(...)), other tensors do not.
@@ -222,22 +224,37 @@ class KVCache:
         return _strides(mass, what, 1)
 
     def _mass_pair(self, mass, mass_out):
-        """Pointers, strides and entries of a mass that is read and one that
-        is written (the same one, or one apart from it)."""
+        """Addresses, strides and entries of a mass that is read (or None) and
+        one that is written (the same one, or one apart from it)."""
         if mass_out is None:
             mass_out = mass
-        if mass_out is None:
-            return None, None, (0, 0), (0, 0), 0
+        size, f32 = mass_out.shape, torch.float32
+        if len(size) == 3 and size[:2] == self._heads and mass_out.dtype is f32 and mass_out.device == self.device:
+            p, (s0, s1, s2) = mass_out.data_ptr(), mass_out.stride()
+            if s2 == 1 and s1 >= size[2] and s0 >= s1 * size[1] and not mass_out.requires_grad:
+                if mass is mass_out:
+                    return p, p, s0, s1, s0, s1, size[2]
+                if mass is None:
+                    return None, p, 0, 0, s0, s1, size[2]
+                if (mass.shape == size and mass.dtype is f32 and mass.device == self.device and not mass.requires_grad and
+                        mass.stride() == (s0, s1, 1)):
+                    q, reach = mass.data_ptr(), 4 * s0 * size[0]
+                    if q + reach <= p or p + reach <= q:
+                        return q, p, s0, s1, s0, s1, size[2]
+        return self._check_masses(mass, mass_out)
+
+    def _check_masses(self, mass, mass_out):
+        """The same one by one, for what the quick look is not content with."""
         out_strides = self._mass(mass_out, "mass output", True)
         if mass is None:
-            return None, mass_out.data_ptr(), (0, 0), out_strides, mass_out.shape[2]
+            return (None, mass_out.data_ptr(), 0, 0, *out_strides, mass_out.shape[2])
         strides = out_strides if mass is mass_out else self._mass(mass, "mass", False)
         if mass.shape[2] != mass_out.shape[2]:
             raise ValueError("the masses differ in length: %d and %d" % (mass.shape[2], mass_out.shape[2]))
         (a0, a1), (b0, b1) = _span(mass), _span(mass_out)
         if a0 < b1 and b0 < a1 and (a0, strides) != (b0, out_strides):
             raise ValueError("the mass and its output overlap without being the same")
-        return mass.data_ptr(), mass_out.data_ptr(), strides, out_strides, mass.shape[2]
+        return (mass.data_ptr(), mass_out.data_ptr(), *strides, *out_strides, mass.shape[2])
 
     def attend(self, q: torch.Tensor, ws: "KVWorkspace", out: torch.Tensor | None = None, scale: float | None = None,
                window: int | None = None, sinks: int = 0, lse: torch.Tensor | None = None,
@@ -284,18 +301,14 @@ class KVCache:
             if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
                 raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))
             self._here(lse, "lse")
-        mass_in = mass_to = None
-        ms = mos = (0, 0)
-        mass_len = 0
-        if mass is not None or mass_out is not None:
-            mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
+        masses = _NO_MASS if mass is None and mass_out is None else self._mass_pair(mass, mass_out)
         qp, q0, q1 = _place(q, "queries", False)
         if out is None:
             with torch.cuda.stream(stream):
                 out = torch.empty(size, dtype=q.dtype, device=dev)
         op, o0, o1 = _place(out, "output", True)
-        query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), mass_in, mass_to, *ms, *mos,
-                             heads, window, sinks, self.head_dim ** -0.5 if scale is None else scale, mass_len, 0)
+        query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), *masses[:6], heads, window,
+                             sinks, self.head_dim ** -0.5 if scale is None else scale, masses[6], 0)
         self._call("splitzip_kv_attend", stream, ctypes.byref(query), ws.buf.data_ptr(), ws.nbytes, self._status(status))
         return out
 
@@ -315,24 +328,24 @@ class KVCache:
                              % (budget, sinks, recent))
         if to is None:
             to = self
-        elif (to.batch, to.kv_heads, to.head_dim, to.dtype, to.device) != \
-                (self.batch, self.kv_heads, self.head_dim, self.dtype, self.device):
+        elif to._shape != self._shape:
             raise ValueError("the destination cache differs in batch, heads, dtype or device")
         if to.max_pages * to.page_size < min(budget, self.max_pages * self.page_size):
             raise ValueError("the destination's table cannot hold %d tokens" % budget)
         shape = (self.batch, self.kv_heads, budget)
         if mass is None:
             raise ValueError("an eviction needs the mass")
-        if kept is not None:
+        if kept is not None and not (kept.shape == shape and kept.dtype is torch.int32 and kept.device == self.device and
+                                     kept.is_contiguous()):
             _plain(kept, torch.int32, 3, "kept positions")
             if tuple(kept.shape) != shape or not kept.is_contiguous():
                 raise ValueError("the kept positions must be contiguous %s" % (shape,))
             self._here(kept, "kept positions")
-        mass_in, mass_to, ms, mos, mass_len = self._mass_pair(mass, mass_out)
+        masses = self._mass_pair(mass, mass_out)
         if kept is None:
             with torch.cuda.stream(stream):
                 kept = torch.empty(shape, dtype=torch.int32, device=self.device)
-        args = _abi.KVBudget(mass_in, mass_to, *ms, *mos, kept.data_ptr(), budget, sinks, recent, mass_len)
+        args = _abi.KVBudget(*masses[:6], kept.data_ptr(), budget, sinks, recent, masses[6])
         self._call("splitzip_kv_evict", stream, to._ref, ctypes.byref(args), self._status(status))
         return kept
 
