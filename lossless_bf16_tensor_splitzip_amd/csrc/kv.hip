@@ -904,6 +904,18 @@ __device__ inline uint32_t lanes_below(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
+// Sum of part[0 .. wave - 1], of up to 16 waves: one look at LDS, a scan over
+// 16 lanes.
+__device__ inline uint32_t sum_before(const uint32_t *part, uint32_t wave) {
+    uint32_t x = part[threadIdx.x & (kSelWaves - 1)];
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, false);    // row_shr:1
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, false);    // row_shr:2
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, false);    // row_shr:4
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, false);    // row_shr:8
+    return wave ? __builtin_amdgcn_readlane(x, wave - 1) : 0u;
+}
+static_assert(kSelWaves == 16, "a DPP row holds a count of every wave");
+
 // The threshold is found by its bits from the top, kSelDigits[i] of them a
 // pass: a histogram in LDS of the keys that agree so far, and its suffix sums.
 // The first digit of 11 bits is sign, exponent and two bits below, so that
@@ -922,7 +934,8 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
     __shared__ __align__(16) uint32_t hist[kSelBins * kSelCopies];
     __shared__ uint32_t part[kSelWaves], part2[kSelWaves];
     __shared__ uint32_t s_prefix, s_need;
-    const uint32_t b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int32_t *status = tid == 0 && h == 0 ? a.status : nullptr;
     uint32_t n = seq_len(a.c, b, status);
     if (n > a.mass_len) {
@@ -968,9 +981,9 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         }
     };
     uint32_t prefix = 0, need = a.budget;
-    for (int pass = 0, left = 32; pass < kSelPasses; ++pass) {
+    for (int pass = 0; pass < kSelPasses; ++pass) {
         // the last digit repeats a bit of the one before, which is agreed on
-        const int shift = left > kSelBits ? left - kSelBits : 0;
+        const int left = 32 - pass * kSelBits, shift = left > kSelBits ? left - kSelBits : 0;
         const uint32_t agreed = pass ? 0xffffffffu << left : 0u;
         for (uint32_t k = tid; k < (uint32_t)(kSelBins * kSelCopies / 4); k += kSelThreads) ((u32x4 *)hist)[k] = u32x4{0, 0, 0, 0};
         __syncthreads();
@@ -981,17 +994,13 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         __syncthreads();
         // thread i has bins 2i and 2i + 1, counted from the top bin down
         const uint32_t top = kSelBins - 1 - 2 * tid;
-        uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-        for (int j = 0; j < kSelCopies; ++j) {
-            c0 += hist[top * kSelCopies + j];
-            c1 += hist[(top - 1) * kSelCopies + j];
-        }
+        static_assert(kSelCopies == 4, "a bin's copies are 16 bytes");
+        const u32x4 h0 = *(const u32x4 *)&hist[top * kSelCopies], h1 = *(const u32x4 *)&hist[(top - 1) * kSelCopies];
+        const uint32_t c0 = h0[0] + h0[1] + h0[2] + h0[3], c1 = h1[0] + h1[1] + h1[2] + h1[3];
         const uint32_t upto = wave_scan(c0 + c1);
         if (lane == 63) part[wave] = upto;
         __syncthreads();
-        uint32_t above = upto - c0 - c1;
-        for (uint32_t w = 0; w < wave; ++w) above += part[w];
+        uint32_t above = upto - c0 - c1 + sum_before(part, wave);
         if (above < need && above + c0 >= need) {
             s_prefix = prefix | top << shift;
             s_need = need - above;
@@ -1004,7 +1013,6 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         __syncthreads();
         prefix = s_prefix;
         need = s_need;
-        left = shift;
     }
     // Kept: the keys above the threshold, and the first `need` of those equal to
     // it.  A wave counts its own, then places them from where the waves before
@@ -1019,11 +1027,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         part2[wave] = ties;
     }
     __syncthreads();
-    uint32_t at = 0, eq = 0;
-    for (uint32_t w = 0; w < wave; ++w) {
-        at += part[w];
-        eq += part2[w];
-    }
+    uint32_t at = sum_before(part, wave), eq = sum_before(part2, wave);
     at += min(eq, need);
     // In place a mass moves to a position at or below its own; with all of
     // them in registers that is free of order, else see below.
