@@ -52,6 +52,9 @@ def parse():
     ap.add_argument("--sizes", action="store_true",
                     help="instead of the benchmark, time single-tensor calls of N(0, 0.02) values "
                          "at 2^16, 2^18, ..., 2^30 elements and print them as one JSON line")
+    ap.add_argument("--kv", metavar="CASE", nargs="?", const="all",
+                    help="instead of the benchmark, time the key-value cache operators on the cases "
+                         "of perf/operators.py (or the one named) and print them as one JSON line")
     ap.add_argument("--probes", action="store_true",
                     help="instead of the benchmark, run the probes of the part's costs that the "
                          "design rests on (reference-stream library) and print them as one JSON line")
@@ -378,6 +381,54 @@ def single_call_sizes(S, W, dev, stream):
         out["2^%d" % k] = {ph: {"us": round(v, 1), "raw_GBps": round(2 * n / v / 1e3, 1)}
                           for ph, v in us.items()}
         del x, payload, dst
+    return out
+
+
+def kv_operators(only=None):
+    """The key-value cache operators on the cases of perf/operators.py: us a
+    pass of the kernels and of the plain forms (elementary torch operations),
+    GB/s by the bytes an operator cannot do without, and that floor's time at
+    the rate of a 2 GiB device-to-device copy of the same run.  Passes take
+    turns over three states of different inputs; median of five rounds."""
+    import statistics
+
+    import torch
+
+    from perf import operators as P
+
+    def timed(fn, passes):
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for k in range(passes):
+            fn(k)
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) * 1e3 / passes
+
+    src = torch.ones(1 << 31, dtype=torch.uint8, device="cuda")
+    dst = torch.empty_like(src)
+    copy = lambda k: dst.copy_(src)       # noqa: E731
+    timed(copy, 3)
+    rate = 2 * src.numel() / statistics.median(timed(copy, 5) for _ in range(5)) / 1e3
+    del src, dst
+    out = {"copy_GBps": round(rate, 0)}
+    for case in P.listed():
+        if only and case["name"] != only:
+            continue
+        P.own = True
+        states = [P.prepare(case, seed) for seed in range(3)]
+        us = {}
+        for side in ("kernel", "plain"):
+            P.own = side == "kernel"
+            passes = 60 if P.own else 6
+            run = lambda k: P.run(states[k % 3])      # noqa: E731
+            timed(run, 6)
+            us[side] = statistics.median(timed(run, passes) for _ in range(5 if P.own else 3))
+        nbytes = P.work(case)["bytes"]
+        out[case["name"]] = {"us": round(us["kernel"], 2), "plain_us": round(us["plain"], 1),
+                             "floor_us": round(nbytes / rate / 1e3, 2),
+                             "GBps": round(nbytes / us["kernel"] / 1e3, 0)}
+        del states
     return out
 
 
@@ -719,6 +770,10 @@ def main():
         return
     if args.sizes:
         print(json.dumps({"single_call_sizes": single_call_sizes(S, W, dev, stream)}))
+        return
+    if args.kv:
+        print(json.dumps({"kv_operators": kv_operators(None if args.kv == "all" else args.kv),
+                          "device": torch.cuda.get_device_name(dev)}))
         return
     if args.small_only:
         only = None if args.small_only == "all" else args.small_only

@@ -176,6 +176,19 @@ def test_lowest_and_infinite_values():
         assert bool(torch.isnan(m.cache.attend(m.gq, ws)).all())
 
 
+@pytest.mark.parametrize("dtype,size,scale", [(BF16, 1e-39, 1e34), (BF16, 3e-38, 1e34), (FP16, 1e-6, 125.0),
+                                              (FP16, 6e-8, 2000.0)])
+def test_subnormal_values(dtype, size, scale):
+    """Subnormal K and V count for what they are."""
+    m = R.make([200, 3], 1, 64, 16, dtype, heads=4, seed=1, fill=0.0)
+    m.v = (torch.randn(m.v.shape, generator=torch.Generator().manual_seed(2)) * size).to(dtype)
+    check(R.to_gpu(m, S))
+    m = R.make([200, 3], 1, 64, 16, dtype, heads=4, seed=1, fill=0.0)
+    m.k = (m.k.float() * size).to(dtype)
+    m.q = (m.q.float() * 1000).to(dtype)
+    check(R.to_gpu(m, S), scale=scale)
+
+
 def test_every_logit_minus_infinity_gives_zeros():
     m = R.make([40, 5], 1, 64, 16, BF16, heads=2, seed=4)
     m.q[:] = 1.0
