@@ -100,7 +100,8 @@ typedef struct splitzip_kv_query {
                                     q_stride[0] + i * q_stride[1] + d; query head
                                     i reads KV head i / (heads / kv_heads)       */
     uint64_t q_stride[2];        /* multiples of 8                               */
-    uint16_t *out;               /* laid out like q, with strides of its own     */
+    uint16_t *out;               /* laid out like q, with strides of its own; may
+                                    be q itself                                  */
     uint64_t out_stride[2];
     float *lse;                  /* NULL, or [batch][heads]: log of the sum of
                                     exp(logit); -inf where nothing is visible    */

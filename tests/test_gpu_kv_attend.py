@@ -114,6 +114,25 @@ def test_batches(lens, want_mass):
     check(R.to_gpu(m, S), want_mass=want_mass)
 
 
+@pytest.mark.parametrize("batch", [64, 65, 150, 400])
+def test_many_sequences_cut_into_runs(batch):
+    """More sequences than a wave has lanes, none of them whole in a run."""
+    _say("attend %d sequences in a wide table" % batch)
+    lens = [(37 * b) % 301 if b % 7 else 0 for b in range(batch)]
+    lens[-1] = 700
+    m = R.make(lens, 1, 64, 16, BF16, heads=3, seed=batch, width=64)
+    check(R.to_gpu(m, S))
+    check(m, window=64, sinks=4, want_mass=False)
+
+
+def test_output_in_place_of_the_queries():
+    m = R.to_gpu(R.make([2000, 0, 33], 2, 128, 16, BF16, heads=8, seed=6), S)
+    ws = S.KVWorkspace(m.cache, 8)
+    want = m.cache.attend(m.gq, ws)
+    assert m.cache.attend(m.gq, ws, out=m.gq) is m.gq
+    assert torch.equal(m.gq.view(torch.int16), want.view(torch.int16))
+
+
 def test_peaked_and_far_logits():
     """Logits in the hundreds: one token takes all, whatever tile it is in; and
     a maximum that grows from tile to tile."""
