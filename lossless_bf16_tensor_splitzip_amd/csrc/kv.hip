@@ -215,6 +215,7 @@ struct AttendArgs {
     float scale2;                 // scale * log2(e): logits in base 2
     uint32_t runs;                // workgroups of k_attend; 0: one for every row tile of every KV head, nothing split
     float *share_o, *share_ml;    // [runs][2] shares of [rows][dim] and [rows][2]
+    uint32_t *splits;             // [batch][kv_heads][row_tiles][2]: see Shares
     float *logits;                // [batch][heads][logit_stride], by visible number (mass only)
     float *lse2;                  // [batch][heads] (mass only)
     uint64_t logit_stride;
@@ -270,6 +271,8 @@ __device__ inline void load_block(const AttendArgs &a, uint32_t first, uint32_t 
     k.upto = carry + sum;
     k.total = __builtin_amdgcn_readlane(k.upto, 63);
 }
+
+constexpr uint32_t kMaxBlocks = (SPLITZIP_KV_MAX_BATCH + 63) / 64;
 
 // Units of a launch, and how they are cut into runs: the first `extra` runs
 // have size + 1 of them, the others size.
@@ -357,6 +360,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
     __shared__ float s_o[kWaves][16][LD];
     __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16];
+    __shared__ uint32_t s_block[kMaxBlocks];
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim;
@@ -367,19 +371,44 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     Cut cut{};
     uint32_t at = 0, u_begin = 0, u_end = 1;
     if (a.runs) {
-        int32_t *status0 = blockIdx.x == 0 && wave == 0 ? a.status : nullptr;
-        load_block(a, 0, 0, blk, status0);
-        uint32_t total = blk.total;
-        for (uint32_t f = 64; f < a.c.batch; f += 64) {
-            Block64 k;
-            load_block(a, f, total, k, status0);
-            total = k.total;
+        int32_t *status0 = blockIdx.x == 0 ? a.status : nullptr;
+        const uint32_t blocks = (a.c.batch + 63) / 64;
+        uint32_t total = 0;
+        if (blocks == 1) {
+            load_block(a, 0, 0, blk, status0);
+            total = blk.total;
+        } else {
+            // Every wave sums some blocks, then all of them look at the sums
+            // (1024 sequences of 64 tokens in a table for 8192: 92 us, and 214
+            // where every wave and every join read all of the lengths).
+            for (uint32_t i = wave; i < blocks; i += kWaves) {
+                const uint32_t b = i * 64 + lane;
+                const uint32_t sum = wave_scan(b < a.c.batch ? units_of(seq_len(a.c, b, status0), a.window, a.sinks) : 0);
+                if (lane == 63) s_block[i] = sum;
+            }
+            __syncthreads();
+            for (uint32_t f = 0; f < blocks; f += 64)
+                total += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
         }
         cut = cut_of(total * pairs, a.runs);
         if (blockIdx.x >= cut.runs) return;
         u_begin = cut.begin(blockIdx.x);
         u_end = cut.begin(blockIdx.x + 1);
-        while (blk.total * pairs <= u_begin) load_block(a, blk.first + 64, blk.total, blk, nullptr);
+        if (blocks > 1) {
+            uint32_t first = 0, carry = 0;
+            for (uint32_t f = 0;; f += 64) {
+                const uint32_t sum = f + lane < blocks ? s_block[f + lane] : 0, upto = carry + wave_scan(sum);
+                const uint64_t past = __ballot(upto * pairs > u_begin);
+                if (past) {       // before the last block's end: u_begin < total * pairs
+                    const uint32_t i = (uint32_t)__builtin_ctzll(past);
+                    first = (f + i) * 64;
+                    carry = __builtin_amdgcn_readlane(upto - sum, i);
+                    break;
+                }
+                carry = __builtin_amdgcn_readlane(upto, 63);
+            }
+            load_block(a, first, carry, blk, nullptr);
+        }
         at = (uint32_t)__builtin_ctzll(__ballot(blk.upto * pairs > u_begin));    // the sequence's lane
     }
 
@@ -681,6 +710,10 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             }
             __syncthreads();
         }
+        if (a.runs && unit0 == 0 && tid == 0) {
+            const uint32_t shares = cut.owner(u + units - 1) - blockIdx.x + 1;
+            ((u32x2 *)a.splits)[(uint64_t)b * pairs + pair] = u32x2{blockIdx.x, shares * 2 + (u != u_begin)};
+        }
         u += a.runs ? count : 1;
         if (pair == pairs - 1 && unit0 + count == units) ++at;
     }
@@ -701,35 +734,16 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 12;      // shares a thread loads before their weights are known
 constexpr uint32_t kMaxRuns = 1024;
 
-// Which runs have shares of a sequence's query head.
+// A query head's shares: runs first .. first + n - 1 have them, at its row in
+// the row tile, the first as its second share if it is late.  The run that
+// began the row tile left first and n * 2 + late in splits.
 struct Shares {
-    Cut cut;
-    uint32_t before, units, pairs;     // units before the sequence, of one of its pairs; pairs of a sequence
-    uint32_t first, n, row, late;      // of the head looked up: runs first .. first + n - 1; its row in their shares;
-                                       // whether the first has it as its second share
+    uint32_t first, n, row, late;
 
-    __device__ void sequence(const AttendArgs &a, uint32_t b) {
-        uint32_t total = 0;
-        before = units = 0;
-        for (uint32_t f = 0; f < a.c.batch; f += 64) {
-            Block64 k;
-            load_block(a, f, total, k, nullptr);
-            if (b >= f && b < f + 64) {
-                before = __builtin_amdgcn_readlane(k.before, b - f);
-                units = __builtin_amdgcn_readlane(k.upto, b - f) - before;
-            }
-            total = k.total;
-        }
-        pairs = a.c.kv_heads * a.row_tiles;
-        cut = cut_of(total * pairs, a.runs);
-    }
-    __device__ void head(const AttendArgs &a, uint32_t h, uint32_t in_group) {
+    __device__ Shares(const AttendArgs &a, uint32_t b, uint32_t h, uint32_t in_group) {
         const uint32_t tile = in_group / a.rows;
-        row = in_group - tile * a.rows;
-        const uint32_t u0 = before * pairs + (h * a.row_tiles + tile) * units;
-        first = cut.owner(u0);
-        n = cut.owner(u0 + units - 1) - first + 1;
-        late = cut.begin(first) != u0;
+        const u32x2 x = ((const u32x2 *)a.splits)[((uint64_t)b * a.c.kv_heads + h) * a.row_tiles + tile];
+        first = x[0], n = x[1] >> 1, late = x[1] & 1, row = in_group - tile * a.rows;
     }
     __device__ uint64_t at(const AttendArgs &a, uint32_t j) const {
         return (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row;
@@ -778,8 +792,6 @@ __device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uin
     }
     const uint32_t t0 = part * kMassTokens + tid;
     if (part * kMassTokens >= n) return;
-    Shares sh;
-    if (a.runs) sh.sequence(a, b);
     const float *x = a.logits + (b * (uint64_t)a.heads + h * a.group) * a.logit_stride;
     const float *in = a.mass ? a.mass + b * a.ms[0] + h * a.ms[1] : nullptr;
     float *out = a.mass_out + b * a.mos[0] + h * a.mos[1];
@@ -801,10 +813,12 @@ __device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uin
         const uint32_t rows = min(kMassRows, a.group - r0);
         __syncthreads();
         for (uint32_t r = wave; r < rows; r += kJoinThreads / 64) {
-            if (a.runs) sh.head(a, h, r0 + r);
+            const uint32_t head = h * a.group + r0 + r;
             float e;
-            if (!a.runs || sh.n == 1) {
-                e = a.lse2[b * (uint64_t)a.heads + h * a.group + r0 + r];
+            if (!a.runs) {
+                e = a.lse2[b * (uint64_t)a.heads + head];
+            } else if (const Shares sh(a, b, h, r0 + r); sh.n == 1) {
+                e = a.lse2[b * (uint64_t)a.heads + head];
             } else {
                 float top, sum;
                 weigh(a, sh, top, sum, [](uint32_t, float) {});
@@ -835,10 +849,9 @@ __device__ inline void add_mass(const AttendArgs &a, uint32_t b, uint32_t h, uin
 
 // One workgroup per query head of a sequence: nothing to do where one run
 // held all of its tokens; else the runs' shares, rescaled to their common
-// maximum.  It is a chain of three loads (lengths; maxima and sums; outputs),
-// so the outputs are asked for together with the maxima, and every wave works
-// the weights out for itself instead of waiting for another.  The workgroups
-// behind them add the mass.
+// maximum.  It is a chain of two loads (which shares; their maxima, sums and
+// outputs together), and every wave works the weights out for itself instead
+// of waiting for another.  The workgroups behind them add the mass.
 template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     __shared__ float s_w[kJoinThreads / 64][kMaxRuns];
@@ -850,10 +863,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
         add_mass(a, b, i - part * a.c.kv_heads, part);
         return;
     }
-    Shares sh;
-    sh.sequence(a, b);
     const uint32_t h = head / a.group;
-    sh.head(a, h, head - h * a.group);
+    const Shares sh(a, b, h, head - h * a.group);
     const uint32_t n = sh.n;
     if (n == 1) return;
     const uint32_t pieces = a.c.dim / 4;             // 4-column pieces of a row
@@ -1272,7 +1283,7 @@ int copy_rows(const splitzip_kv_cache *cache, const splitzip_kv_rows *r, int32_t
 struct AttendPlan {
     uint32_t group, row_tiles, rows, blocks, runs;
     uint64_t logit_stride;
-    size_t ml_at, lse2_at, logits_at, bytes;
+    size_t o_at, ml_at, lse2_at, logits_at, bytes;
 };
 
 // As many runs as workgroups are resident on 256 compute units, which the
@@ -1308,7 +1319,8 @@ bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, 
     p.logit_stride = ((uint64_t)mass_len + 3) & ~3ull;
     if ((double)p.logit_stride * c->batch * heads > 1e15) return false;
     if ((p.logit_stride / kMassTokens + 1) * c->kv_heads + heads >= 1ull << 24) return false;      // k_join's grid
-    p.ml_at = up16((size_t)p.runs * 2 * p.rows * c->head_dim * 4);
+    p.o_at = up16((size_t)c->batch * c->kv_heads * p.row_tiles * 8);
+    p.ml_at = up16(p.o_at + (size_t)p.runs * 2 * p.rows * c->head_dim * 4);
     p.lse2_at = up16(p.ml_at + (size_t)p.runs * 2 * p.rows * 8);
     p.logits_at = up16(p.lse2_at + (p.logit_stride ? (size_t)c->batch * heads * 4 : 0));
     p.bytes = p.logits_at + 4 * p.logit_stride * c->batch * heads;
@@ -1410,7 +1422,8 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     a.mass_len = Q.mass_len;
     a.status = d_status;
     uint8_t *ws = reinterpret_cast<uint8_t *>(d_ws);
-    a.share_o = reinterpret_cast<float *>(ws);
+    a.splits = reinterpret_cast<uint32_t *>(ws);
+    a.share_o = reinterpret_cast<float *>(ws + P.o_at);
     a.share_ml = reinterpret_cast<float *>(ws + P.ml_at);
     if (Q.mass_out && P.logit_stride) {
         a.lse2 = reinterpret_cast<float *>(ws + P.lse2_at);

@@ -125,6 +125,14 @@ def test_many_sequences_cut_into_runs(batch):
     check(m, window=64, sinks=4, want_mass=False)
 
 
+def test_sequences_beyond_a_wave_of_blocks():
+    """More than 64 times 64 of them: their blocks' sums take a second look."""
+    lens = [(13 * b) % 40 if b % 5 else 0 for b in range(4200)]
+    lens[0], lens[4101], lens[-1] = 900, 500, 300
+    _say("attend %d sequences" % len(lens))
+    check(R.to_gpu(R.make(lens, 1, 64, 16, BF16, heads=2, seed=3, width=64), S))
+
+
 def test_output_in_place_of_the_queries():
     m = R.to_gpu(R.make([2000, 0, 33], 2, 128, 16, BF16, heads=8, seed=6), S)
     ws = S.KVWorkspace(m.cache, 8)
