@@ -328,6 +328,20 @@ __device__ inline void unpack2(uint32_t w, float &x, float &y) {
     }
 }
 
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Two values with infinities and NaN replaced by the largest finite number of
+// their sign, as integers: positive ones compare as signed, negative ones are
+// the upper half of the unsigned.
+template <bool BF16>
+__device__ inline uint32_t finite2(uint32_t w) {
+    constexpr uint16_t top = BF16 ? 0x7f7f : 0x7bff;
+    const i16x2 x = __builtin_elementwise_min(__builtin_bit_cast(i16x2, w), i16x2{(int16_t)top, (int16_t)top});
+    constexpr uint16_t low = 0x8000 | top;
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, x), u16x2{low, low}));
+}
+
 // Over the four lanes that hold a query row's tokens (16 apart).
 template <bool MAX>
 __device__ inline float row_reduce(float x) {
@@ -627,14 +641,18 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (int w = 0; w < VW; ++w)
 #pragma unroll
                 for (int odd = 0; odd < 2; ++odd) {
-                    u32x4 col;
+                    // An infinity in V counts once: times a low part that is 0 or
+                    // negative it would make a NaN.
+                    u32x4 col, fin;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i) {
                         col[i] = __builtin_amdgcn_perm(word(2 * i + 1, w), word(2 * i, w), odd ? 0x07060302u : 0x05040100u);
+                        fin[i] = finite2<BF16>(col[i]);
+                    }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         o[t][2 * w + odd] = mfma<BF16>(col, hi[t], o[t][2 * w + odd]);
-                        o[t][2 * w + odd] = mfma<BF16>(col, lo[t], o[t][2 * w + odd]);
+                        o[t][2 * w + odd] = mfma<BF16>(fin, lo[t], o[t][2 * w + odd]);
                     }
                 }
             if (more) load_v(buf ^ 1);

@@ -203,6 +203,35 @@ def test_lowest_and_infinite_values():
         assert bool(torch.isnan(m.cache.attend(m.gq, ws)).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,heads", [(64, 1), (128, 20), (72, 3), (256, 2)])
+def test_infinite_v_whatever_its_weight(dim, heads, dtype):
+    """Infinities in V under tokens of every weight, the largest (exactly 1
+    before the division) among them: infinite in their columns and of their
+    sign, all others as without them."""
+    n = 160
+    m = R.make([n], 1, dim, 16, dtype, heads=heads, seed=12)
+    R.to_gpu(m, S)
+    ws = S.KVWorkspace(m.cache, heads)
+    want = R.attend(m)[0]
+    top = int((m.k[m.table[0].long()].float().permute(0, 2, 1, 3).reshape(-1, dim)[:n] @ m.q[0, 0].float()).argmax())
+    for step, tokens in enumerate([[top]] + [range(i, n, 40) for i in range(40)]):
+        v = m.v.clone()
+        cols = torch.zeros(dim, dtype=torch.float64)
+        for i, t in enumerate(tokens):
+            col = (5 * step + 13 * i) % dim
+            x = math.inf if i % 2 == 0 else -math.inf
+            if cols[col]:
+                continue
+            v[m.table[0, t // 16].long(), 0, t % 16, col] = x
+            cols[col] = x
+        m.gv.copy_(v)
+        out = m.cache.attend(m.gq, ws)[0].double().cpu()
+        hit = cols != 0
+        assert torch.equal(out[:, hit], cols[hit].expand(heads, -1)), step
+        assert bool(((out - want[0]).abs() <= want[1])[:, ~hit].all()), step
+
+
 @pytest.mark.parametrize("dtype,size,scale", [(BF16, 1e-39, 1e34), (BF16, 3e-38, 1e34), (FP16, 1e-6, 125.0),
                                               (FP16, 6e-8, 2000.0)])
 def test_subnormal_values(dtype, size, scale):
