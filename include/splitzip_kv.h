@@ -61,8 +61,8 @@ extern "C" {
 /* Limits: head_dim a multiple of 8 in 8..256; all strides multiples of 8 (16
  * bytes) and pools 16-byte aligned; 1..65536 slots a page; max_pages *
  * page_size below 2^31; num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV
- * heads; the pools' largest offset below 2^40 elements.  Pages that two
- * sequences share may be read, not written. */
+ * heads; the pools' largest offset below 2^40 elements.  A page that the table
+ * names twice (for two sequences or in one) may be read, not written. */
 typedef struct splitzip_kv_cache {
     uint16_t *k, *v;             /* pools (bf16 or fp16 bit patterns)            */
     uint64_t k_stride[3];        /* elements between pages, heads, slots         */
@@ -156,8 +156,9 @@ int splitzip_kv_gather(const splitzip_kv_cache *cache, const splitzip_kv_rows *r
 /* Bytes of workspace that splitzip_kv_attend needs for caches of this shape
  * (batch, kv_heads, head_dim; no pointer is read), `heads` query heads and,
  * where mass is asked for, up to mass_len entries (0: none); 0 for invalid
- * shapes.  A larger workspace serves too.  Its content between calls does not matter; one workspace must
- * not be used by two calls that can run at the same time. */
+ * shapes.  A larger workspace serves too.  Its content between calls does not
+ * matter; one workspace must not be used by two calls that can run at the same
+ * time. */
 size_t splitzip_kv_attend_workspace_size(const splitzip_kv_cache *cache, uint32_t heads,
                                          uint32_t mass_len);
 
