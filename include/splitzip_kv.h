@@ -166,7 +166,9 @@ size_t splitzip_kv_attend_workspace_size(const splitzip_kv_cache *cache, uint32_
  * V appended before).  Of a sequence of length n, token t is visible when
  * t >= n - window or t < sinks.  With x[t] = scale * (q . k[t]) over the
  * visible tokens, out = sum_t exp(x[t] - lse) v[t], lse = log sum_t exp(x[t]).
- * A sequence with no visible token gives zeros and lse = -inf.  With mass_out,
+ * A sequence with no visible token gives zeros and lse = -inf.  Logits and the
+ * sum before its division are held in 32 bits: where they pass 3.4e38 (bf16
+ * values near the type's largest) the result is not finite.  With mass_out,
  * mass_out[t] = mass[t] + the sum of exp(x[t] - lse) over the query heads of
  * the KV head for visible tokens, mass[t] for the others, up to the sequence's
  * length (mass NULL: 0); entries behind it are left alone.

@@ -374,7 +374,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
     __shared__ float s_o[kWaves][16][LD];
     __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16];
-    __shared__ uint32_t s_block[kMaxBlocks];
+    uint32_t *s_block = (uint32_t *)s_o;      // while the run is looked up, before any output
+    static_assert(sizeof s_o >= 4 * kMaxBlocks, "sums of all blocks");
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim;
