@@ -214,6 +214,7 @@ struct AttendArgs {
     uint32_t row_tiles, rows;     // row tiles a group is cut into, query rows a tile
     float scale2;                 // scale * log2(e): logits in base 2
     uint32_t runs;                // workgroups of k_attend; 0: one for every row tile of every KV head, nothing split
+    Div by_runs, by_row_tiles, by_pairs;    // divisors: runs, row_tiles, kv_heads * row_tiles
     float *share_o, *share_ml;    // [runs][2] shares of [rows][dim] and [rows][2]
     uint32_t *splits;             // [batch][kv_heads][row_tiles][2]: see Shares
     float *logits;                // [batch][heads][logit_stride], by visible number (mass only)
@@ -285,13 +286,10 @@ struct Cut {
     }
 };
 
-__device__ inline Cut cut_of(uint32_t units, uint32_t runs) {
-    Cut c;
-    c.units = units;
-    c.runs = min(units, runs);
-    c.size = units / c.runs;
-    c.extra = units - c.size * c.runs;
-    return c;
+__device__ inline Cut cut_of(uint32_t units, Div runs) {
+    if (units < runs.d) return Cut{units, units, 1, 0};
+    const uint32_t size = div(units, runs);
+    return Cut{units, runs.d, size, units - size * runs.d};
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -373,7 +371,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     constexpr float kLift = BF16 ? 0.f : 15.f;
     __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
     __shared__ float s_o[kWaves][16][LD];
-    __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16];
+    __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16], s_top[16], s_sum[16];
     uint32_t *s_block = (uint32_t *)s_o;      // while the run is looked up, before any output
     static_assert(sizeof s_o >= 4 * kMaxBlocks, "sums of all blocks");
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
@@ -405,7 +403,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (uint32_t f = 0; f < blocks; f += 64)
                 total += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
         }
-        cut = cut_of(total * pairs, a.runs);
+        cut = cut_of(total * pairs, a.by_runs);
         if (blockIdx.x >= cut.runs) return;
         u_begin = cut.begin(blockIdx.x);
         u_end = cut.begin(blockIdx.x + 1);
@@ -442,28 +440,28 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             unit0 = rel - pair * units;
             count = min(units - unit0, u_end - u);
         } else {
-            b = blockIdx.x / pairs;
+            b = div(blockIdx.x, a.by_pairs);
             pair = blockIdx.x - b * pairs;
             n = __builtin_amdgcn_readfirstlane(seq_len(a.c, b, pair == 0 && wave == 0 ? a.status : nullptr));
             count = units = units_of(n, a.window, a.sinks);
         }
         const bool whole = count == units;
-        const uint32_t h = pair / a.row_tiles, row0 = (pair - h * a.row_tiles) * a.rows;     // rows of the group
+        const uint32_t h = div(pair, a.by_row_tiles), row0 = (pair - h * a.row_tiles) * a.rows;     // rows of the group
         const uint32_t rows = min(a.rows, a.group - row0), head0 = h * a.group + row0;
         const Seen seen = seen_of(n, a.window, a.sinks);
         const uint32_t v_end = min(seen.count, (unit0 + count) * kUnit);
         const int32_t *table = a.c.table + b * a.c.table_stride;
 
         u32x4 q[QLDS ? 1 : NT][QLDS ? 1 : KS];
+        constexpr int kStage = QLDS ? NT * 16 * (DP / 8) / kAttendThreads : 1;
+        u32x4 stage[kStage];
         if constexpr (QLDS) {
-            __syncthreads();
-            for (uint32_t i = tid; i < NT * 16 * (DP / 8); i += kAttendThreads) {
-                const uint32_t row = i / (DP / 8), d = i % (DP / 8) * 8;
-                u32x4 x{0, 0, 0, 0};
-                if (row < rows && (EXACT || d < D)) x = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + row) * a.qs[1] + d);
-                *(u32x4 *)&s_q[row * LQ + d] = x;
+#pragma unroll
+            for (int k = 0; k < kStage; ++k) {
+                const uint32_t i = tid + k * kAttendThreads, row = i / (DP / 8), d = i % (DP / 8) * 8;
+                stage[k] = u32x4{0, 0, 0, 0};
+                if (row < rows && (EXACT || d < D)) stage[k] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + row) * a.qs[1] + d);
             }
-            __syncthreads();
         } else {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -562,6 +560,18 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             load_k(0);
             load_v(0);
             page = page_of(v0 + kUnit);
+        }
+        if constexpr (QLDS) {      // K and V are on their way; the row tile before has been read (its last barriers)
+#pragma unroll
+            for (int k = 0; k < kStage; ++k) {
+                const uint32_t i = tid + k * kAttendThreads;
+                *(u32x4 *)&s_q[i / (DP / 8) * LQ + i % (DP / 8) * 8] = stage[k];
+            }
+            __syncthreads();
+        }
+        if (a.runs && unit0 == 0 && tid == 0) {      // here its divisions are waited for by nothing
+            const uint32_t shares = whole ? 1 : cut.owner(u + units - 1) - blockIdx.x + 1;
+            ((u32x2 *)a.splits)[(uint64_t)b * pairs + pair] = u32x2{blockIdx.x, shares * 2 + (u != u_begin)};
         }
         for (; v0 < v_end; v0 += kUnit) {
             const bool more = v0 + kUnit < v_end;
@@ -674,15 +684,25 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
         __syncthreads();
         const uint32_t slot = blockIdx.x * 2 + (u != u_begin);
         for (int t = 0; t < NT && t * 16 < (int)rows; ++t) {
-            float top = s_m[0][t * 16 + c16];
+            // a lane's row c16: the waves' maximum and sum
+            float M = -INFINITY, L = 0.f, mw[kWaves], lw[kWaves];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, s_m[w][t * 16 + c16]);
+            for (int w = 0; w < kWaves; ++w) {
+                mw[w] = s_m[w][t * 16 + c16];
+                lw[w] = s_l[w][t * 16 + c16];
+                M = fmaxf(M, mw[w]);
+            }
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) L += mw[w] == -INFINITY ? lw[w] : lw[w] * __builtin_amdgcn_exp2f(mw[w] - M);
+            if (tid < 16) {
+                s_top[tid] = M;
+                s_sum[tid] = L;
+            }
             // o[t] is indexed by a constant: one of the NT blocks is taken
-            float r = 0.f;
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt)
                 if (tt == t) {
-                    r = m[tt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[tt] - top);
+                    const float r = m[tt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[tt] - M);
 #pragma unroll
                     for (int p = 0; p < P16 + P8; ++p) {
                         const int wide = p < P16 ? 8 : 4;      // columns of the piece
@@ -699,39 +719,38 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                     }
                 }
             __syncthreads();
-            for (uint32_t item = tid; item < 16 * (DP / 4); item += kAttendThreads) {
-                const uint32_t row = item / (DP / 4), d = item % (DP / 4) * 4, gr = t * 16 + row;
+            constexpr int kItems = 16 * (DP / 4) / kAttendThreads;
+            f32x4 y[kItems];
+            float top[kItems], sum[kItems];
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
+                top[k] = s_top[row];
+                sum[k] = s_sum[row];
+                y[k] = *(const f32x4 *)&s_o[0][row][d];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) y[k] += *(const f32x4 *)&s_o[w][row][d];
+            }
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
+                const uint32_t gr = t * 16 + row;
                 if (gr >= rows || d >= D) continue;
-                float M = -INFINITY, L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) M = fmaxf(M, s_m[w][gr]);
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) L += s_m[w][gr] == -INFINITY ? s_l[w][gr] : s_l[w][gr] * __builtin_amdgcn_exp2f(s_m[w][gr] - M);
-                f32x4 y = *(const f32x4 *)&s_o[0][row][d];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w) y += *(const f32x4 *)&s_o[w][row][d];
                 if (whole) {
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
-                    u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
+                    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
+                    u32x2 z{pack2<BF16>(y[k][0] * inv, y[k][1] * inv), pack2<BF16>(y[k][2] * inv, y[k][3] * inv)};
                     *(u32x2 *)(a.out + b * a.os[0] + (head0 + gr) * a.os[1] + d) = z;
                     if (d == 0) {
-                        const float e = L == 0.f ? -INFINITY : M + log2f(L);
+                        const float e = sum[k] == 0.f ? -INFINITY : top[k] + log2f(sum[k]);
                         if (a.lse) a.lse[b * (uint64_t)a.heads + head0 + gr] = e * kLn2;
                         if (a.lse2) a.lse2[b * (uint64_t)a.heads + head0 + gr] = e;
                     }
                 } else {
-                    *(f32x4 *)(a.share_o + ((uint64_t)slot * a.rows + gr) * D + d) = y;
-                    if (d == 0) {
-                        a.share_ml[((uint64_t)slot * a.rows + gr) * 2] = M;
-                        a.share_ml[((uint64_t)slot * a.rows + gr) * 2 + 1] = L;
-                    }
+                    *(f32x4 *)(a.share_o + ((uint64_t)slot * a.rows + gr) * D + d) = y[k];
+                    if (d == 0) *(f32x2 *)(a.share_ml + ((uint64_t)slot * a.rows + gr) * 2) = f32x2{top[k], sum[k]};
                 }
             }
             __syncthreads();
-        }
-        if (a.runs && unit0 == 0 && tid == 0) {
-            const uint32_t shares = cut.owner(u + units - 1) - blockIdx.x + 1;
-            ((u32x2 *)a.splits)[(uint64_t)b * pairs + pair] = u32x2{blockIdx.x, shares * 2 + (u != u_begin)};
         }
         u += a.runs ? count : 1;
         if (pair == pairs - 1 && unit0 + count == units) ++at;
@@ -1463,6 +1482,9 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     const bool whole = tiles < 1u << 24 && (units <= 2 || (units <= 4 && tiles >= 256));      // a grid's limit
     a.runs = whole ? 0 : tiles * units < P.runs ? (uint32_t)(tiles * units) : P.runs;
     const uint32_t grid_x = a.runs ? a.runs : (uint32_t)tiles;
+    a.by_runs = make_div(a.runs ? a.runs : 1);
+    a.by_row_tiles = make_div(P.row_tiles);
+    a.by_pairs = make_div(cache->kv_heads * P.row_tiles);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = cache->dtype == SPLITZIP_KV_BF16;
     if (bf16) launch_attend<true>(a, P.blocks, grid_x, s);
