@@ -196,7 +196,8 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
 //
 // 32 sequences of 32768 tokens, 8 KV heads of 128, 8 query heads each: 4.30 GB
 // in 643 us, 6.7 TB/s, the rate of a bare read stream.  One sequence: 30 us, 25
-// of them here and 5 in the join's launch.  48 sequences of 0 to 8192: 44 us.
+// of them here and 5 in the join's launch.  48 sequences of 0 to 8192: 43 us.  A run without any
+// token takes 4 (dim 64) to 6.5 us (24 rows of dim 256).
 
 constexpr int kWaves = 4;
 constexpr int kAttendThreads = 64 * kWaves;
