@@ -195,9 +195,9 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
 // 32768 tokens of one sequence 37 us against 30.)
 //
 // 32 sequences of 32768 tokens, 8 KV heads of 128, 8 query heads each: 4.30 GB
-// in 643 us, 6.7 TB/s, the rate of a bare read stream.  One sequence: 30 us, 25
-// of them here and 5 in the join's launch.  48 sequences of 0 to 8192: 43 us.  A run without any
-// token takes 4 (dim 64) to 6.5 us (24 rows of dim 256).
+// in 643 us, 6.7 TB/s, the rate of a bare read stream.  One sequence: 30 us, 26
+// of them here and 4.5 in the join's launch.  48 sequences of 0 to 8192: 43 us.
+// A run without any token takes 4 (dim 64) to 6.5 us (24 rows of dim 256).
 
 constexpr int kWaves = 4;
 constexpr int kAttendThreads = 64 * kWaves;
@@ -995,12 +995,15 @@ static_assert(kSelWaves == 16, "a DPP row holds a count of every wave");
 // masses, which crowd into a few powers of two, spread over more than a few
 // counters (LDS adds to one address take turns).
 constexpr int kSelBits = 11, kSelBins = 1 << kSelBits, kSelPasses = 3;
-constexpr int kSelCopies = 4;      // of the first pass's histogram, by lane
+// Copies of the first pass's histogram, by lane (32768 masses counted in 2.6 us
+// with 8, 4.0 with 4, and more of them to clear and sum); later digits are
+// spread enough for one.
+constexpr int kSelCopies = 8;
 constexpr int kSelHeld = 32;       // masses a thread can hold
 
-// One workgroup per sequence and KV head: 8 us for 4096 tokens, 22 us for 32768
-// (three passes of 2 to 5 us, 4 us to place what stays; the instructions of one
-// compute unit bound it).  Wave w has the run of tokens from
+// One workgroup per sequence and KV head: 8 us for 4096 tokens, 19 us for 32768
+// (3 until the masses are there, 4.5, 2 and 2 for the passes, 5.5 to count and
+// place what stays; the instructions of one compute unit bound it).  Wave w has the run of tokens from
 // w * span; lane l its tokens l, l + 64, ..., HELD of them in registers (all
 // of them where span is at most 64 HELD, and then the masses are read once);
 // HELD 0: read again by every pass.
@@ -1060,18 +1063,32 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         // the last digit repeats a bit of the one before, which is agreed on
         const int left = 32 - pass * kSelBits, shift = left > kSelBits ? left - kSelBits : 0;
         const uint32_t agreed = pass ? 0xffffffffu << left : 0u;
-        for (uint32_t k = tid; k < (uint32_t)(kSelBins * kSelCopies / 4); k += kSelThreads) ((u32x4 *)hist)[k] = u32x4{0, 0, 0, 0};
+        const uint32_t copies = pass ? 1 : kSelCopies, copy = lane & (copies - 1);
+        for (uint32_t k = tid; k < kSelBins / 4 * copies; k += kSelThreads) ((u32x4 *)hist)[k] = u32x4{0, 0, 0, 0};
         __syncthreads();
         each([&](uint32_t, float, uint32_t key) {
             if ((key & agreed) == prefix)
-                atomicAdd(&hist[(key >> shift & (kSelBins - 1)) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
+                atomicAdd(&hist[(key >> shift & (kSelBins - 1)) * copies + copy], 1u);
         });
         __syncthreads();
+        // every mass is in registers now
+        if (HELD && pass == 0 && out)
+            for (uint32_t t = a.budget + tid; t < n; t += kSelThreads) out[t] = 0.f;
         // thread i has bins 2i and 2i + 1, counted from the top bin down
         const uint32_t top = kSelBins - 1 - 2 * tid;
-        static_assert(kSelCopies == 4, "a bin's copies are 16 bytes");
-        const u32x4 h0 = *(const u32x4 *)&hist[top * kSelCopies], h1 = *(const u32x4 *)&hist[(top - 1) * kSelCopies];
-        const uint32_t c0 = h0[0] + h0[1] + h0[2] + h0[3], c1 = h1[0] + h1[1] + h1[2] + h1[3];
+        uint32_t c0, c1;
+        if (pass) {
+            const u32x2 both = *(const u32x2 *)&hist[top - 1];
+            c0 = both[1], c1 = both[0];
+        } else {
+            u32x4 h0{0, 0, 0, 0}, h1 = h0;
+#pragma unroll
+            for (int k = 0; k < kSelCopies; k += 4) {
+                h0 += *(const u32x4 *)&hist[top * kSelCopies + k];
+                h1 += *(const u32x4 *)&hist[(top - 1) * kSelCopies + k];
+            }
+            c0 = h0[0] + h0[1] + h0[2] + h0[3], c1 = h1[0] + h1[1] + h1[2] + h1[3];
+        }
         const uint32_t upto = wave_scan(c0 + c1);
         if (lane == 63) part[wave] = upto;
         __syncthreads();
@@ -1104,12 +1121,14 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
     __syncthreads();
     uint32_t at = sum_before(part, wave), eq = sum_before(part2, wave);
     at += min(eq, need);
+    // mostly all of the equal ones stay, and one comparison tells
+    const bool some = sum_before(part2, kSelWaves) > need;
+    const uint32_t least = some ? prefix + 1 : prefix;
     // In place a mass moves to a position at or below its own; with all of
     // them in registers that is free of order, else see below.
     each([&](uint32_t t, float m, uint32_t key) {
-        const uint64_t same = __ballot(key == prefix);
-        uint64_t all = __ballot(key > prefix);
-        if (same) {
+        uint64_t all = __ballot(key >= least);
+        if (const uint64_t same = some ? __ballot(key == prefix) : 0) {
             const uint32_t rank = eq + lanes_below(same);
             all |= __ballot(key == prefix && rank < need);
             eq += __popcll(same);
@@ -1121,19 +1140,17 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
         }
         at += __popcll(all);
     });
-    if (!out) return;
+    if (HELD || !out) return;
+    // step by step upwards, a step's masses read before any of it is written
     __syncthreads();
-    if (!HELD) {
-        // step by step upwards, a step's masses read before any of it is written
-        for (uint32_t t0 = 0; t0 < a.budget; t0 += kSelThreads) {
-            const uint32_t t = t0 + tid;
-            float m = 0.f;
-            if (t < a.budget) m = mass[kept[t]];
-            __syncthreads();
-            if (t < a.budget) out[t] = m;
-        }
+    for (uint32_t t0 = 0; t0 < a.budget; t0 += kSelThreads) {
+        const uint32_t t = t0 + tid;
+        float m = 0.f;
+        if (t < a.budget) m = mass[kept[t]];
         __syncthreads();
+        if (t < a.budget) out[t] = m;
     }
+    __syncthreads();
     for (uint32_t t = a.budget + tid; t < n; t += kSelThreads) out[t] = 0.f;
 }
 
@@ -1153,7 +1170,7 @@ __host__ __device__ inline uint32_t move_rows(uint32_t chunk) { return kMoveThre
 // steps need no other order.  Columns share nothing.  Memory bounds it where
 // there are workgroups enough: 16 x 4096 tokens of 8 heads of 128 to half,
 // 268 MB, in 50 us.  In place with few columns a step's three loads in turn do
-// (one sequence of 32768 tokens of 8 heads to 8192 in 62 us, selection included);
+// (one sequence of 32768 tokens of 8 heads to 8192 in 59 us, selection included);
 // looking the next step's places up ahead gained nothing.
 template <bool LINES, int U>
 __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
