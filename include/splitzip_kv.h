@@ -25,6 +25,7 @@
  * outside the rows given.  Such a token is left out (neither read nor
  * written), such a length is taken as the nearest one allowed, and where
  * d_status is given the bits below are ORed into it.
+ * Table, lengths and row ranges must not change while a call runs.
  */
 #ifndef SPLITZIP_KV_H
 #define SPLITZIP_KV_H

@@ -423,7 +423,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             }
             load_block(a, first, carry, blk, nullptr);
         }
-        at = (uint32_t)__builtin_ctzll(__ballot(blk.upto * pairs > u_begin));    // the sequence's lane
+        const uint64_t past = __ballot(blk.upto * pairs > u_begin);
+        at = past ? (uint32_t)__builtin_ctzll(past) : 64;      // the sequence's lane
     }
 
     for (uint32_t u = u_begin; u < u_end;) {
@@ -438,6 +439,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             const uint32_t before = __builtin_amdgcn_readlane(blk.before, at), rel = u - before * pairs;
             units = __builtin_amdgcn_readlane(blk.upto, at) - before;
             pair = rel / units;
+            if (b >= a.c.batch || pair >= pairs) break;      // lengths that another stream changes meanwhile
             unit0 = rel - pair * units;
             count = min(units - unit0, u_end - u);
         } else {
@@ -782,7 +784,8 @@ struct Shares {
     __device__ Shares(const AttendArgs &a, uint32_t b, uint32_t h, uint32_t in_group) {
         const uint32_t tile = in_group / a.rows;
         const u32x2 x = ((const u32x2 *)a.splits)[((uint64_t)b * a.c.kv_heads + h) * a.row_tiles + tile];
-        first = x[0], n = x[1] >> 1, late = x[1] & 1, row = in_group - tile * a.rows;
+        // within the workspace also where lengths that changed meanwhile left it unwritten
+        first = min(x[0], a.runs - 1), n = min(x[1] >> 1, a.runs - first), late = x[1] & 1, row = in_group - tile * a.rows;
     }
     __device__ uint64_t at(const AttendArgs &a, uint32_t j) const {
         return (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row;
@@ -905,7 +908,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
     const uint32_t h = head / a.group;
     const Shares sh(a, b, h, head - h * a.group);
     const uint32_t n = sh.n;
-    if (n == 1) return;
+    if (n <= 1) return;
     const uint32_t pieces = a.c.dim / 4;             // 4-column pieces of a row
     const uint32_t ways = kJoinThreads / pieces;     // shares summed side by side
     const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
