@@ -76,6 +76,17 @@ def test_groups(group, dim):
     check(R.to_gpu(m, S))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim,group", [(40, 20), (24, 64), (72, 24), (104, 64), (168, 20), (176, 48), (208, 24), (248, 32)])
+def test_odd_dims_of_many_rows(dim, group, dtype):
+    """Head sizes between the kernels' own with several blocks of query rows,
+    whole and cut into runs."""
+    _say("attend dim=%d group=%d %s" % (dim, group, dtype))
+    for width in (None, 500):
+        m = R.make([40, 0, 333, 129, 1], 2, dim, 16, dtype, heads=2 * group, seed=dim, width=width)
+        check(R.to_gpu(m, S))
+
+
 @pytest.mark.parametrize("page", [1, 2, 7, 8, 16, 24, 33, 64, 128, 1000])
 @pytest.mark.parametrize("layout", ["hnd", "nhd"])
 def test_pages(page, layout):
