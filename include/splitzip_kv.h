@@ -61,8 +61,8 @@ extern "C" {
 
 /* Limits: head_dim a multiple of 8 in 8..256; all strides multiples of 8 (16
  * bytes) and pools 16-byte aligned; 1..65536 slots a page; max_pages *
- * page_size below 2^31; num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV
- * heads; the pools' largest offset below 2^40 elements.  A page that the table
+ * page_size below 2^31; rows of the table at least max_pages apart;
+ * num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV heads; the pools' largest offset below 2^40 elements.  A page that the table
  * names twice (for two sequences or in one) may be read, not written. */
 typedef struct splitzip_kv_cache {
     uint16_t *k, *v;             /* pools (bf16 or fp16 bit patterns)            */

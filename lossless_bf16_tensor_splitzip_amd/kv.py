@@ -99,9 +99,9 @@ def _fixed(name: str):
 class KVCache:
     """A paged cache: K and V pools [pages, kv_heads, page_size, head_dim]
     (bfloat16 or float16, last dimension contiguous, other strides multiples
-    of 8), ``table`` int32 [batch, max_pages] and ``lens`` int32 [batch].  It
-    holds the caller's tensors and allocates nothing; table and lens may be
-    changed between calls.
+    of 8), ``table`` int32 [batch, max_pages] (rows of their own, not one
+    expanded) and ``lens`` int32 [batch].  It holds the caller's tensors and
+    allocates nothing; table and lens may be changed between calls.
 
     Every call takes ``status``, an int32 tensor that the caller has set to 0:
     bits _abi.KV_BAD_PAGE (a page number outside the pools: its tokens are left
@@ -126,6 +126,9 @@ class KVCache:
             raise ValueError("head_dim must be a multiple of 8 in 8..256, got %d" % dim)
         if table.shape[1] * page_size >= 1 << 31:
             raise ValueError("a sequence's table reaches 2^31 tokens")
+        row = _strides(table, "page table", 1)[0]
+        if table.shape[0] > 1 and row < table.shape[1]:
+            raise ValueError("rows of the page table overlap in memory: %d pages, %d apart" % (table.shape[1], row))
         for t, what in ((k_pages, "K pool"), (v_pages, "V pool")):
             _no_overlap(t, what)
             _no_grad(t, what)
@@ -136,9 +139,8 @@ class KVCache:
         self.kv_heads, self.page_size, self.head_dim = kv_heads, page_size, dim
         ks, vs = _strides(k_pages, "K pool"), _strides(v_pages, "V pool")
         self.args = _abi.KVCacheArgs(k_pages.data_ptr(), v_pages.data_ptr(), *ks, *vs, table.data_ptr(),
-                                     max(_strides(table, "page table", 1)[0], self.max_pages), lens.data_ptr(),
-                                     pages, page_size, kv_heads, dim, self.batch, self.max_pages,
-                                     _DTYPES[self.dtype], 0)
+                                     row, lens.data_ptr(), pages, page_size, kv_heads, dim, self.batch,
+                                     self.max_pages, _DTYPES[self.dtype], 0)
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
         self._row, self._cu, self._heads = (kv_heads, dim), (self.batch + 1,), (self.batch, kv_heads)
