@@ -1199,7 +1199,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
             if (i0 + tid < end) {
                 const uint32_t i = (uint32_t)(i0 + tid), t = (uint32_t)kept[i];
                 uint32_t p0, s0, p1, s1;
-                const bool here = locate(a.c, b, t, p0, s0), there = locate(a.to, b, i, p1, s1);
+                // kept is as the selection left it: -1 where a length has grown since
+                const bool here = t < a.c.max_len && locate(a.c, b, t, p0, s0), there = locate(a.to, b, i, p1, s1);
                 if (!here || !there) {
                     report(a.status, SPLITZIP_KV_BAD_PAGE);
                 } else if (!(same && t == i)) {

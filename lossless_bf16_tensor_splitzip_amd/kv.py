@@ -71,6 +71,40 @@ def _span(t: torch.Tensor):
     return first, first + t.element_size() * (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())))
 
 
+def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether some element of one tensor shares memory with one of the other
+    (interleaved ones need not).  Their distance is a sum of strides, each
+    taken c times; of the largest stride only the c that the others can bring
+    back to 0 are looked at, and so on down."""
+    (p, p_end), (q, q_end) = _span(x), _span(y)
+    if not x.numel() or not y.numel() or p_end <= q or q_end <= p:
+        return False
+    ex, ey = x.element_size(), y.element_size()
+    steps = {}
+    for t, side in ((x, 1), (y, 0)):
+        for n, st in zip(t.shape, t.stride()):
+            if n > 1 and st:
+                steps.setdefault(st * t.element_size(), [0, 0])[side] += n - 1
+    steps = sorted(steps.items(), reverse=True)
+    below = [(0, 0)]
+    for st, (less, more) in reversed(steps):
+        below.append((below[-1][0] - st * less, below[-1][1] + st * more))
+    below.reverse()
+    looks = 0
+
+    def found(d, i):
+        nonlocal looks
+        looks += 1
+        if i == len(steps) or looks > 100000:       # strides of no order: taken as meeting
+            return i < len(steps) or -ex < d < ey
+        st, (less, more) = steps[i]
+        low, high = below[i + 1]
+        first, last = max(-less, -((d + high + ex - 1) // st)), min(more, (ey - 1 - low - d) // st)
+        return any(found(d + st * c, i + 1) for c in range(first, last + 1))
+
+    return found(p - q, 0)
+
+
 def _plain(t: torch.Tensor, dtype, dims: int, what: str) -> None:
     if not t.is_cuda:
         raise ValueError("the %s must be on the GPU" % what)
@@ -339,6 +373,8 @@ class KVCache:
             raise ValueError("the destination cache differs in batch, heads, dtype or device")
         if to.max_pages * to.page_size < min(budget, self.max_pages * self.page_size):
             raise ValueError("the destination's table cannot hold %d tokens" % budget)
+        if to is not self:
+            self._apart(to)
         shape = (self.batch, self.kv_heads, budget)
         if mass is None:
             raise ValueError("an eviction needs the mass")
@@ -355,6 +391,19 @@ class KVCache:
         args = _abi.KVBudget(*masses[:6], kept.data_ptr(), budget, sinks, recent, masses[6])
         self._call("splitzip_kv_evict", stream, to._ref, ctypes.byref(args), self._status(status))
         return kept
+
+
+    def _apart(self, to: "KVCache") -> None:
+        """Refuses a destination that would overwrite what is still to be read
+        (one with a start in common is the library's to judge: the cache itself
+        in all fields, or refused)."""
+        if any(getattr(self.args, f) == getattr(to.args, f) for f in ("k", "v", "table", "lens")):
+            return
+        mine, its = self._tensors, to._tensors
+        for x, y in (("k_pages", "k_pages"), ("k_pages", "v_pages"), ("v_pages", "k_pages"), ("v_pages", "v_pages"),
+                     ("lens", "lens")):
+            if _meet(mine[x], its[y]):
+                raise ValueError("the destination shares memory with the cache (%s and %s)" % (y, x))
 
 
 class KVWorkspace:

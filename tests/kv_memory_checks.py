@@ -22,4 +22,30 @@ def tables(new, to_gpu, runs):
     assert S.KVCache(k, v, wide[:1, :0].expand(2, 0), n).max_pages == 0     # rows of nothing
 
 
-PARTS = ("tables",)
+def destinations(new, to_gpu, runs):
+    """Evictions into memory that is still to be read."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, seed=1, width=2, slack=6))
+    k, v, t, n = m.gk, m.gv, m.gtable, m.glens
+    mass = new(torch.rand, 2, 2, 32)
+    kept = new(torch.zeros, 2, 2, 8, dtype=torch.int32)
+    far = to_gpu(R.make([8, 8], 2, 64, 16, torch.bfloat16, seed=2))
+    lens = new(torch.zeros, 3, dtype=torch.int32)
+    apart = S.KVCache(k, v, t, lens[:2])
+
+    def into(cache, *to):
+        refused(cache.evict, mass, 8, to=S.KVCache(*to), kept=kept)
+
+    into(m.cache, k[1:], v[1:].clone(), far.gtable, far.glens)
+    into(m.cache, v[1:], k[1:], far.gtable, far.glens)
+    into(apart, far.gk, far.gv, far.gtable, lens[1:])
+    # K and V, and the two caches, as slices of one tensor: they interleave and do not meet
+    both = new(torch.zeros, 6, 4, 2, 16, 64, dtype=torch.bfloat16)
+    one = S.KVCache(both[:, 0], both[:, 1], t, n)
+    other = S.KVCache(both[:, 2], both[:, 3], far.gtable, far.glens)
+    t.copy_(torch.arange(4, dtype=torch.int32).reshape(2, 2))
+    far.gtable.copy_(torch.tensor([[4], [5]], dtype=torch.int32))
+    runs(one.evict, mass, 8, to=other, kept=kept)
+    runs(one.evict, mass, 8, to=S.KVCache(both[:, 0], both[:, 1], t, n), kept=kept)      # in place
+
+
+PARTS = ("tables", "destinations")
