@@ -71,6 +71,12 @@ def _span(t: torch.Tensor):
     return first, first + t.element_size() * (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())))
 
 
+def _reach(size, s0: int, s1: int) -> int:
+    """Bytes from the first to behind the last element of a 16-bit tensor of
+    three dimensions, the last contiguous (0 entries: no more than one)."""
+    return 2 * ((size[0] - 1) * s0 + (size[1] - 1) * s1 + size[2])
+
+
 def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
     """Whether some element of one tensor shares memory with one of the other
     (interleaved ones need not).  Their distance is a sum of strides, each
@@ -348,6 +354,11 @@ class KVCache:
             with torch.cuda.stream(stream):
                 out = torch.empty(size, dtype=q.dtype, device=dev)
         op, o0, o1 = _place(out, "output", True)
+        # the queries themselves, or apart from them: another workgroup's output
+        # must not land in queries that are still to be read
+        if (out is not q and op < qp + _reach(size, q0, q1) and qp < op + _reach(size, o0, o1) and
+                (op, o0, o1) != (qp, q0, q1) and _meet(q, out)):
+            raise ValueError("the output overlaps the queries without being the same")
         query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), *masses[:6], heads, window,
                              sinks, self.head_dim ** -0.5 if scale is None else scale, masses[6], 0)
         self._call("splitzip_kv_attend", stream, ctypes.byref(query), ws.buf.data_ptr(), ws.nbytes, self._status(status))

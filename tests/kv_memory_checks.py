@@ -48,4 +48,17 @@ def destinations(new, to_gpu, runs):
     runs(one.evict, mass, 8, to=S.KVCache(both[:, 0], both[:, 1], t, n), kept=kept)      # in place
 
 
-PARTS = ("tables", "destinations")
+def outputs(new, to_gpu, runs):
+    """Outputs that overlap the queries without being the same."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
+    ws = S.KVWorkspace(m.cache, 4)
+    packed = new(torch.zeros, 3, 8, 64, dtype=torch.bfloat16)
+    q = packed[:2, :4]
+    refused(m.cache.attend, q, ws, out=packed[1:, :4])
+    refused(m.cache.attend, q, ws, out=packed[:2, 2:6])
+    refused(m.cache.attend, q, ws, out=packed.view(-1)[:512].view(4, 2, 64).transpose(0, 1))
+    runs(m.cache.attend, q, ws, out=packed[:2, 4:])              # beside them
+    runs(m.cache.attend, q, ws, out=packed[:2, :4])              # in their place
+
+
+PARTS = ("tables", "destinations", "outputs")
