@@ -212,6 +212,8 @@ class KVCache:
             self._check_rows(k, v, cu, start)
         kp, k0, k1 = _place(k, "K rows", written)
         vp, v0, v1 = _place(v, "V rows", written)
+        if written and vp < kp + _reach(size, k0, k1) and kp < vp + _reach(size, v0, v1) and _meet(k, v):
+            raise ValueError("the K rows and the V rows overlap in memory")
         return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, size[0], 0, cu.data_ptr(),
                                         None if start is None else start.data_ptr()))
 

@@ -61,4 +61,16 @@ def outputs(new, to_gpu, runs):
     runs(m.cache.attend, q, ws, out=packed[:2, :4])              # in their place
 
 
-PARTS = ("tables", "destinations", "outputs")
+def gathered(new, to_gpu, runs):
+    """Rows of K and V gathered into each other."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, seed=1))
+    cu = new(torch.tensor, [0, 2, 4], dtype=torch.int32)
+    rows = new(torch.zeros, 6, 4, 64, dtype=torch.bfloat16)
+    refused(m.cache.gather, rows[:4, :2], rows[:4, :2], cu)
+    refused(m.cache.gather, rows[:4, :2], rows[1:5, 1:3], cu)
+    refused(m.cache.gather, rows[:4, 2:], rows[2:, 2:], cu)
+    runs(m.cache.gather, rows[:4, :2], rows[:4, 2:], cu)         # halves of the same rows
+    runs(m.cache.append, rows[:4, :2], rows[:4, :2], cu)         # read, they may be the same
+
+
+PARTS = ("tables", "destinations", "outputs", "gathered")
