@@ -184,6 +184,10 @@ class KVCache:
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
         self._row, self._cu, self._heads = (kv_heads, dim), (self.batch + 1,), (self.batch, kv_heads)
+        # pools that share memory (a latent that is K and V) are read like others;
+        # one pool as both can be written where K and V get the same values
+        self._one_pool = (k_pages.data_ptr(), ks) == (v_pages.data_ptr(), vs)
+        self._pools_meet = self._one_pool or _meet(k_pages, v_pages)
         self._shape = (self.batch, kv_heads, dim, self.dtype, self.device)
 
     # The kernels are given these tensors' memory once: in-place changes reach
@@ -214,6 +218,8 @@ class KVCache:
         vp, v0, v1 = _place(v, "V rows", written)
         if written and vp < kp + _reach(size, k0, k1) and kp < vp + _reach(size, v0, v1) and _meet(k, v):
             raise ValueError("the K rows and the V rows overlap in memory")
+        if self._pools_meet and not written and not (self._one_pool and (kp, k0, k1) == (vp, v0, v1)):
+            raise ValueError("K and V rows that differ cannot be written to pools that share memory")
         return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, size[0], 0, cu.data_ptr(),
                                         None if start is None else start.data_ptr()))
 
@@ -388,6 +394,8 @@ class KVCache:
             raise ValueError("the destination's table cannot hold %d tokens" % budget)
         if to is not self:
             self._apart(to)
+        if to._pools_meet and not (to._one_pool and self._one_pool and to.args.k != self.args.k):
+            raise ValueError("the K and V pools of the destination share memory")
         shape = (self.batch, self.kv_heads, budget)
         if mass is None:
             raise ValueError("an eviction needs the mass")

@@ -73,4 +73,27 @@ def gathered(new, to_gpu, runs):
     runs(m.cache.append, rows[:4, :2], rows[:4, :2], cu)         # read, they may be the same
 
 
-PARTS = ("tables", "destinations", "outputs", "gathered")
+def pools(new, to_gpu, runs):
+    """Pools of K and V that share memory: read, and written where both get
+    the same; an eviction in place would move their rows twice."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
+    far = to_gpu(R.make([8, 3], 2, 64, 16, torch.bfloat16, seed=2))
+    k, t, n = m.gk, m.gtable, m.glens
+    one, half = S.KVCache(k, k, t, n), S.KVCache(k[:-1], k[1:], t, n)
+    cu = new(torch.tensor, [0, 2, 4], dtype=torch.int32)
+    rows = new(torch.zeros, 2, 4, 2, 64, dtype=torch.bfloat16)
+    mass, kept = new(torch.rand, 2, 2, 32), new(torch.zeros, 2, 2, 8, dtype=torch.int32)
+    runs(one.attend, m.gq, S.KVWorkspace(one, 4), out=torch.zeros_like(m.gq))
+    runs(one.gather, rows[0], rows[1], cu)
+    runs(one.append, rows[0], rows[0], cu)
+    refused(one.append, rows[0], rows[1], cu)
+    refused(half.append, rows[0], rows[0], cu)
+    refused(one.evict, mass, 8, kept=kept)
+    refused(half.evict, mass, 8, kept=kept)
+    to = S.KVCache(far.gk, far.gk, far.gtable, far.glens)
+    refused(m.cache.evict, mass, 8, to=to, kept=kept)
+    runs(one.evict, mass, 8, to=to, kept=kept)
+    runs(half.evict, mass, 8, to=far.cache, kept=kept)
+
+
+PARTS = ("tables", "destinations", "outputs", "gathered", "pools")
