@@ -306,8 +306,7 @@ class KVCache:
         strides = out_strides if mass is mass_out else self._mass(mass, "mass", False)
         if mass.shape[2] != mass_out.shape[2]:
             raise ValueError("the masses differ in length: %d and %d" % (mass.shape[2], mass_out.shape[2]))
-        (a0, a1), (b0, b1) = _span(mass), _span(mass_out)
-        if a0 < b1 and b0 < a1 and (a0, strides) != (b0, out_strides):
+        if (mass.data_ptr(), strides) != (mass_out.data_ptr(), out_strides) and _meet(mass, mass_out):
             raise ValueError("the mass and its output overlap without being the same")
         return (mass.data_ptr(), mass_out.data_ptr(), *strides, *out_strides, mass.shape[2])
 

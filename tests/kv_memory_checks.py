@@ -96,4 +96,17 @@ def pools(new, to_gpu, runs):
     runs(half.evict, mass, 8, to=far.cache, kept=kept)
 
 
-PARTS = ("tables", "destinations", "outputs", "gathered", "pools")
+def masses(new, to_gpu, runs):
+    """A mass and its output as slices of one tensor."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
+    ws = S.KVWorkspace(m.cache, 4, mass=True)
+    out, kept = torch.zeros_like(m.gq), new(torch.zeros, 2, 2, 8, dtype=torch.int32)
+    both = new(torch.zeros, 2, 4, 80)
+    for a, b in ((both[:, :2, :40], both[:, :2, 40:]), (both[:, ::2, :32], both[:, 1::2, :32])):
+        runs(m.cache.attend, m.gq, ws, out=out, mass=a, mass_out=b)
+        runs(m.cache.evict, a, 8, kept=kept, mass_out=b)
+    refused(m.cache.attend, m.gq, ws, out=out, mass=both[:, :2, :40], mass_out=both[:, 1:3, :40])
+    refused(m.cache.evict, both[:, :2, :40], 8, kept=kept, mass_out=both[:, :2, 39:79])
+
+
+PARTS = ("tables", "destinations", "outputs", "gathered", "pools", "masses")
