@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import _abi
 from .codec import _device_or_pinned, _same_gpu, _status_ptr
@@ -123,6 +124,8 @@ def _plain(t: torch.Tensor, dtype, dims: int, what: str) -> None:
 def _no_grad(t: torch.Tensor, what: str) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError("the %s requires a gradient, and the cache computes none" % what)
+    if _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None:
+        raise ValueError("the %s has a tangent, and the cache computes none" % what)
 
 
 def _fixed(name: str):
@@ -212,7 +215,8 @@ class KVCache:
         size = k.shape
         if not (k.dtype is v.dtype is self.dtype and size == v.shape and len(size) == 3 and size[1:] == self._row and
                 k.device == v.device == cu.device == self.device and cu.dtype is torch.int32 and cu.shape == self._cu and
-                start is None and cu.is_contiguous() and not (k.requires_grad or v.requires_grad)):
+                start is None and cu.is_contiguous() and not (k.requires_grad or v.requires_grad) and
+                _forward._current_level < 0):
             self._check_rows(k, v, cu, start)
         kp, k0, k1 = _place(k, "K rows", written)
         vp, v0, v1 = _place(v, "V rows", written)
@@ -284,7 +288,8 @@ class KVCache:
         if mass_out is None:
             mass_out = mass
         size, f32 = mass_out.shape, torch.float32
-        if len(size) == 3 and size[:2] == self._heads and mass_out.dtype is f32 and mass_out.device == self.device:
+        if (len(size) == 3 and size[:2] == self._heads and mass_out.dtype is f32 and mass_out.device == self.device and
+                _forward._current_level < 0):
             p, (s0, s1, s2) = mass_out.data_ptr(), mass_out.stride()
             if s2 == 1 and s1 >= size[2] and s0 >= s1 * size[1] and not mass_out.requires_grad:
                 if mass is mass_out:
@@ -332,7 +337,7 @@ class KVCache:
         if not q.device == ws.buf.device == dev:
             self._here(q, "queries")
             self._here(ws.buf, "workspace")
-        if q.requires_grad:
+        if q.requires_grad or _forward._current_level >= 0:
             _no_grad(q, "queries")
         heads = size[1]
         if heads < 1 or heads % self.kv_heads:
@@ -348,13 +353,14 @@ class KVCache:
                 raise ValueError("the output must be shaped like the queries")
             if out.device != dev:
                 self._here(out, "output")
-            if out.requires_grad:
+            if out.requires_grad or _forward._current_level >= 0:
                 _no_grad(out, "output")
         if lse is not None:
             _plain(lse, torch.float32, 2, "lse")
             if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
                 raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))
             self._here(lse, "lse")
+            _no_grad(lse, "lse")
         masses = _NO_MASS if mass is None and mass_out is None else self._mass_pair(mass, mass_out)
         qp, q0, q1 = _place(q, "queries", False)
         if out is None:

@@ -1,7 +1,8 @@
 """More of what the tensor-level calls of the key-value cache refuse: tensors
-that meet in memory.  Written like kv_checks, for a run without a GPU and one
+that meet in memory, and those of forward mode.  Written like kv_checks, for a run without a GPU and one
 with it."""
 import torch
+from torch.autograd import forward_ad
 
 import lossless_bf16_tensor_splitzip_amd as S
 import kv_reference as R
@@ -109,4 +110,33 @@ def masses(new, to_gpu, runs):
     refused(m.cache.evict, both[:, :2, :40], 8, kept=kept, mass_out=both[:, :2, 39:79])
 
 
-PARTS = ("tables", "destinations", "outputs", "gathered", "pools", "masses")
+def tangents(new, to_gpu, runs):
+    """Tensors of forward mode: the tangent would be lost without a word."""
+    m = to_gpu(R.make([20, 3], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
+    ws = S.KVWorkspace(m.cache, 4, mass=True)
+    out, kept = torch.zeros_like(m.gq), new(torch.zeros, 2, 2, 8, dtype=torch.int32)
+    cu = new(torch.tensor, [0, 2, 4], dtype=torch.int32)
+    rows, mass = new(torch.zeros, 4, 2, 64, dtype=torch.bfloat16), new(torch.zeros, 2, 2, 32)
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t.clone(), torch.ones_like(t))
+
+        refused(m.cache.attend, dual(m.gq), ws, out=out)
+        refused(m.cache.attend, m.gq, ws, out=dual(out))
+        refused(m.cache.attend, m.gq, ws, out=out, lse=dual(new(torch.zeros, 2, 4)))
+        refused(m.cache.attend, m.gq, ws, out=out, mass=dual(mass))
+        refused(m.cache.attend, m.gq, ws, out=out, mass=dual(mass), mass_out=mass)
+        refused(m.cache.append, dual(rows), rows, cu)
+        refused(m.cache.append, rows, dual(rows), cu)
+        refused(m.cache.gather, dual(rows), rows.clone(), cu)
+        refused(m.cache.evict, dual(mass), 8, kept=kept)
+        refused(S.KVCache, dual(m.gk), m.gv, m.gtable, m.glens)
+        with torch.no_grad():                                    # which leaves forward mode on
+            refused(m.cache.attend, dual(m.gq), ws, out=out)
+        runs(m.cache.attend, m.gq, ws, out=out, mass=mass)
+        runs(m.cache.append, rows, rows.clone(), cu)
+        runs(m.cache.evict, mass, 8, kept=kept)
+    runs(m.cache.attend, m.gq, ws, out=out)
+
+
+PARTS = ("tables", "destinations", "outputs", "gathered", "pools", "masses", "tangents")
