@@ -62,8 +62,9 @@ extern "C" {
 /* Limits: head_dim a multiple of 8 in 8..256; all strides multiples of 8 (16
  * bytes) and pools 16-byte aligned; 1..65536 slots a page; max_pages *
  * page_size below 2^31; rows of the table at least max_pages apart;
- * num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV heads; the pools' largest offset below 2^40 elements.  A page that the table
- * names twice (for two sequences or in one) may be read, not written. */
+ * num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV heads; the pools'
+ * largest offset below 2^40 elements.  A page that the table names twice (for
+ * two sequences or in one) may be read, not written. */
 typedef struct splitzip_kv_cache {
     uint16_t *k, *v;             /* pools (bf16 or fp16 bit patterns)            */
     uint64_t k_stride[3];        /* elements between pages, heads, slots         */
@@ -83,8 +84,9 @@ typedef struct splitzip_kv_cache {
 
 /* Rows outside the cache: element d of row r, head h is
  * k[r * k_stride[0] + h * k_stride[1] + d].  Rows cu[b] .. cu[b+1]-1 belong to
- * sequence b and to its positions start[b], start[b]+1, ...; with start NULL
- * they are its last ones, start[b] = lens[b] - (cu[b+1] - cu[b]). */
+ * sequence b and to its positions start[b], start[b]+1, ... (lens is not looked
+ * at then); with start NULL they are its last ones, start[b] = lens[b] -
+ * (cu[b+1] - cu[b]). */
 typedef struct splitzip_kv_rows {
     uint16_t *k, *v;
     uint64_t k_stride[2];        /* elements between rows, heads (multiples of 8) */
@@ -145,8 +147,8 @@ typedef struct splitzip_kv_budget {
  * library. */
 void splitzip_kv_struct_sizes(size_t sizes[4]);
 
-/* Copy rows into the cache / cached tokens into rows.  lens already counts the
- * appended tokens.  Rows behind cu[batch] are left alone (an append does not
+/* Copy rows into the cache / cached tokens into rows.  With start NULL, lens
+ * already counts the appended tokens.  Rows behind cu[batch] are left alone (an append does not
  * read them, a gather does not write them).  Bit-exact copies.
  * Errors: INVALID, HIP. */
 int splitzip_kv_append(const splitzip_kv_cache *cache, const splitzip_kv_rows *rows,

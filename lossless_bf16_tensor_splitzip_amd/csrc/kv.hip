@@ -125,8 +125,9 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
             if (lo > 0 && lo <= a.c.batch) {
                 const uint32_t b = lo - 1;
                 const int64_t first = a.cu[b], end = a.cu[b + 1];
-                const uint32_t len = seq_len(a.c, b, a.status);
-                const int64_t pos = (a.start ? (int64_t)a.start[b] : (int64_t)len - (end - first)) + ((int64_t)r - first);
+                // with first positions given, a length need not be set yet
+                const int64_t from = a.start ? (int64_t)a.start[b] : (int64_t)seq_len(a.c, b, a.status) - (end - first);
+                const int64_t pos = from + ((int64_t)r - first);
                 uint32_t page, slot;
                 if (first < 0 || first > (int64_t)r || end > (int64_t)a.rows || pos < 0 || pos >= (int64_t)a.c.max_len) {
                     report(a.status, SPLITZIP_KV_BAD_ROWS);

@@ -253,8 +253,8 @@ class KVCache:
         """Write rows ``k`` and ``v`` [rows, kv_heads, head_dim] (device or
         pinned host memory) into the cache.  Rows cu[b] .. cu[b+1]-1 (``cu``
         int32 [batch + 1]) go to positions start[b], start[b]+1, ... of
-        sequence b; with ``start`` None they are its last ones: ``lens``
-        counts them already.  Rows behind cu[batch] are not read."""
+        sequence b, whatever its length; with ``start`` None they are its last
+        ones: ``lens`` counts them already.  Rows behind cu[batch] are not read."""
         rows = self._rows(k, v, cu, start, False)
         self._call("splitzip_kv_append", stream, rows, self._status(status))
 

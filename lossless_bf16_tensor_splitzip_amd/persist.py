@@ -205,24 +205,26 @@ def pack_sequence(name: str, cache, b: int, ws, threshold: float = COVERAGE_GATE
     codebook of its own.  Returns ((K entry, blob), (V entry, blob)), named
     ``name``.k and ``name``.v; the cache is left as it is.  ``ws`` is a
     ``Workspace`` for kv_heads * tokens * head_dim elements.  Reads the
-    sequence's length back, so it synchronises with the device."""
+    sequence's length back (one outside its table is an error), so it
+    synchronises with the device."""
     import torch
 
     _check_sequence(cache, b)
-    n = min(max(int(cache.lens[b].item()), 0), cache.max_pages * cache.page_size)
+    n, most = int(cache.lens[b].item()), cache.max_pages * cache.page_size
+    if not 0 <= n <= most:
+        raise ValueError("sequence %d has a length of %d, and its table holds 0 to %d tokens" % (b, n, most))
     k, v = (torch.empty(cache.kv_heads, n, cache.head_dim, dtype=cache.dtype, device=cache.device)
             for _ in range(2))
     status = torch.zeros(1, dtype=torch.int32, device=cache.device)
     cache.gather(k.transpose(0, 1), v.transpose(0, 1), _only(cache, b, n), status=status)
-    if int(status.item()):
-        raise ValueError("the table of sequence %d names pages outside the pool" % b)
+    _check_placed(status, b)
     return pack(name + ".k", k, ws, threshold), pack(name + ".v", v, ws, threshold)
 
 
 def unpack_sequence(packed, cache, b: int) -> int:
     """Rebuild what ``pack_sequence`` returned as the tokens of sequence ``b``
-    of a cache whose table row names enough pages for them; its length is set.
-    Returns the number of tokens."""
+    of a cache whose table row names enough pages for them; its length, whatever
+    it was, is set.  Returns the number of tokens."""
     import torch
 
     _check_sequence(cache, b)
@@ -238,8 +240,7 @@ def unpack_sequence(packed, cache, b: int) -> int:
     status = torch.zeros(1, dtype=torch.int32, device=cache.device)
     start = torch.zeros(cache.batch, dtype=torch.int32, device=cache.device)
     cache.append(k.transpose(0, 1), v.transpose(0, 1), _only(cache, b, n), start=start, status=status)
-    if int(status.item()):
-        raise ValueError("the table of sequence %d names pages outside the pool" % b)
+    _check_placed(status, b)
     cache.lens[b] = n
     return n
 
@@ -247,6 +248,16 @@ def unpack_sequence(packed, cache, b: int) -> int:
 def _check_sequence(cache, b: int) -> None:
     if not 0 <= b < cache.batch:
         raise ValueError("sequence %d of a batch of %d" % (b, cache.batch))
+
+
+def _check_placed(status, b: int) -> None:
+    from . import _abi
+
+    bits = int(status.item())
+    if bits & _abi.KV_BAD_PAGE:
+        raise ValueError("the table of sequence %d names pages outside the pool" % b)
+    if bits:
+        raise ValueError("the rows of sequence %d have no place in its table (status %d)" % (b, bits))
 
 
 def _only(cache, b: int, n: int):
