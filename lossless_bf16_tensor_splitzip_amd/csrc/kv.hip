@@ -371,6 +371,12 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     // fp16 weights are held times 2^15: their smallest normal step then lies 2^-29
     // below the largest weight instead of 2^-14.
     constexpr float kLift = BF16 ? 0.f : 15.f;
+    // The first part of a weight is 0 only where the weight is, so that an
+    // infinity in V comes out as one: fp16 would round weights below 2^-40 of the
+    // largest to 0, and 0 times infinity is a NaN.  The median of p, 2^102 p and
+    // the type's smallest step is p, or that step, or 0; the second part then
+    // takes the step away again.
+    auto at_least = [](float p) { return BF16 ? p : __builtin_amdgcn_fmed3f(p, p * 0x1p102f, 0x1p-24f); };
     __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
     __shared__ float s_o[kWaves][16][LD];
     __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16], s_top[16], s_sum[16];
@@ -637,7 +643,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                     const float p0 = __builtin_amdgcn_exp2f(y[i] - use), p1 = __builtin_amdgcn_exp2f(y[i + 1] - use);
                     l[t] += p0 + p1;
                     float r0, r1;
-                    hi[t][i / 2] = pack2<BF16>(p0, p1);
+                    hi[t][i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
                     unpack2<BF16>(hi[t][i / 2], r0, r1);
                     lo[t][i / 2] = pack2<BF16>(p0 - r0, p1 - r1);
                 }
@@ -656,8 +662,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (int w = 0; w < VW; ++w)
 #pragma unroll
                 for (int odd = 0; odd < 2; ++odd) {
-                    // An infinity in V counts once: times a low part that is 0 or
-                    // negative it would make a NaN.
+                    // An infinity in V counts once, with the first part: times a
+                    // second one that is 0 or negative it would make a NaN.
                     u32x4 col, fin;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
