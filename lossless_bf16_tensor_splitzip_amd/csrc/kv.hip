@@ -607,7 +607,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             }
             if (more) load_k(buf ^ 1);
 
-            u32x4 hi[NT], lo[NT];
+            u32x4 hi[NT], lo[NT], rest[BF16 ? NT : 1];
             const uint32_t mine = (valid >> (g * 4) & 15u) | (valid >> (16 + g * 4) & 15u) << 4;     // of its 8 tokens
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -637,15 +637,24 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    // The weight as a sum of two 16-bit numbers: one alone would
-                    // add an error as large as the output's own rounding, and the
-                    // second product is hidden behind the loads (0 to 3 %).
+                    // The weight as a sum of 16-bit numbers, as many as hold the
+                    // bits that 32 have: three of 8 in bf16, two of 11 in fp16.
+                    // One alone would add an error as large as the output's own
+                    // rounding, two in bf16 one of 2^-16, which moved 0.1 % of the
+                    // outputs by a step.  The further products are hidden behind
+                    // the loads (second 0 to 3 %, third 0 to 1; with 32 and 64
+                    // rows a KV head 62.3 us become 65.4 and 79.8 85.1).
                     const float p0 = __builtin_amdgcn_exp2f(y[i] - use), p1 = __builtin_amdgcn_exp2f(y[i + 1] - use);
                     l[t] += p0 + p1;
                     float r0, r1;
                     hi[t][i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
                     unpack2<BF16>(hi[t][i / 2], r0, r1);
                     lo[t][i / 2] = pack2<BF16>(p0 - r0, p1 - r1);
+                    if constexpr (BF16) {
+                        float s0, s1;
+                        unpack2<BF16>(lo[t][i / 2], s0, s1);
+                        rest[t][i / 2] = pack2<BF16>(p0 - r0 - s0, p1 - r1 - s1);
+                    }
                 }
             }
             if (valid != 0xffffffffu) {
@@ -662,8 +671,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             for (int w = 0; w < VW; ++w)
 #pragma unroll
                 for (int odd = 0; odd < 2; ++odd) {
-                    // An infinity in V counts once, with the first part: times a
-                    // second one that is 0 or negative it would make a NaN.
+                    // An infinity in V counts once, with the first part: times
+                    // another that is 0 or negative it would make a NaN.
                     u32x4 col, fin;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -674,6 +683,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                     for (int t = 0; t < NT; ++t) {
                         o[t][2 * w + odd] = mfma<BF16>(col, hi[t], o[t][2 * w + odd]);
                         o[t][2 * w + odd] = mfma<BF16>(fin, lo[t], o[t][2 * w + odd]);
+                        if constexpr (BF16) o[t][2 * w + odd] = mfma<BF16>(fin, rest[t], o[t][2 * w + odd]);
                     }
                 }
             if (more) load_v(buf ^ 1);
