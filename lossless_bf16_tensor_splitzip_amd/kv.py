@@ -187,6 +187,7 @@ class KVCache:
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
         self._row, self._cu, self._heads = (kv_heads, dim), (self.batch + 1,), (self.batch, kv_heads)
+        self._spans = [(name, _span(self._tensors[name])) for name in ("k_pages", "v_pages", "lens")]
         # pools that share memory (a latent that is K and V) are read like others;
         # one pool as both can be written where K and V get the same values
         self._one_pool = (k_pages.data_ptr(), ks) == (v_pages.data_ptr(), vs)
@@ -423,13 +424,13 @@ class KVCache:
         """Refuses a destination that would overwrite what is still to be read
         (one with a start in common is the library's to judge: the cache itself
         in all fields, or refused)."""
-        if any(getattr(self.args, f) == getattr(to.args, f) for f in ("k", "v", "table", "lens")):
+        a, b = self.args, to.args
+        if a.k == b.k or a.v == b.v or a.table == b.table or a.lens == b.lens:
             return
-        mine, its = self._tensors, to._tensors
-        for x, y in (("k_pages", "k_pages"), ("k_pages", "v_pages"), ("v_pages", "k_pages"), ("v_pages", "v_pages"),
-                     ("lens", "lens")):
-            if _meet(mine[x], its[y]):
-                raise ValueError("the destination shares memory with the cache (%s and %s)" % (y, x))
+        for x, (p, p_end) in self._spans:
+            for y, (q, q_end) in to._spans:
+                if p < q_end and q < p_end and _meet(self._tensors[x], to._tensors[y]):
+                    raise ValueError("the destination shares memory with the cache (%s and %s)" % (y, x))
 
 
 class KVWorkspace:
