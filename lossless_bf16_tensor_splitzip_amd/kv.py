@@ -187,7 +187,7 @@ class KVCache:
         self._ref = ctypes.byref(self.args)
         self._index = self.device.index
         self._row, self._cu, self._heads = (kv_heads, dim), (self.batch + 1,), (self.batch, kv_heads)
-        self._spans = [(name, _span(self._tensors[name])) for name in ("k_pages", "v_pages", "lens")]
+        self._spans = _span(k_pages), _span(v_pages), _span(lens)
         # pools that share memory (a latent that is K and V) are read like others;
         # one pool as both can be written where K and V get the same values
         self._one_pool = (k_pages.data_ptr(), ks) == (v_pages.data_ptr(), vs)
@@ -331,11 +331,11 @@ class KVCache:
         weight every token received, summed over its KV head's query heads, is
         added to it: in place, or into ``mass_out``, whose entries up to the
         length are all written (with ``mass_out`` alone, starting from 0)."""
-        size, dev = q.shape, self.device
+        size, index = q.shape, self._index
         if q.dtype is not self.dtype or len(size) != 3 or size[0] != self.batch or size[2] != self.head_dim:
             raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
                              % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(size)))
-        if not q.device == ws.buf.device == dev:
+        if not q.get_device() == ws.buf.get_device() == index:
             self._here(q, "queries")
             self._here(ws.buf, "workspace")
         if q.requires_grad or _forward._current_level >= 0:
@@ -352,7 +352,7 @@ class KVCache:
         if out is not None:
             if out.dtype is not self.dtype or out.shape != size:
                 raise ValueError("the output must be shaped like the queries")
-            if out.device != dev:
+            if out.get_device() != index:
                 self._here(out, "output")
             if out.requires_grad or _forward._current_level >= 0:
                 _no_grad(out, "output")
@@ -366,12 +366,12 @@ class KVCache:
         qp, q0, q1 = _place(q, "queries", False)
         if out is None:
             with torch.cuda.stream(stream):
-                out = torch.empty(size, dtype=q.dtype, device=dev)
+                out = torch.empty(size, dtype=q.dtype, device=self.device)
         op, o0, o1 = _place(out, "output", True)
         # the queries themselves, or apart from them: another workgroup's output
         # must not land in queries that are still to be read
-        if (out is not q and op < qp + _reach(size, q0, q1) and qp < op + _reach(size, o0, o1) and
-                (op, o0, o1) != (qp, q0, q1) and _meet(q, out)):
+        if (out is not q and op < qp + 2 * ((size[0] - 1) * q0 + (heads - 1) * q1 + size[2]) and
+                qp < op + _reach(size, o0, o1) and (op, o0, o1) != (qp, q0, q1) and _meet(q, out)):
             raise ValueError("the output overlaps the queries without being the same")
         query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), *masses[:6], heads, window,
                              sinks, self.head_dim ** -0.5 if scale is None else scale, masses[6], 0)
@@ -427,9 +427,13 @@ class KVCache:
         a, b = self.args, to.args
         if a.k == b.k or a.v == b.v or a.table == b.table or a.lens == b.lens:
             return
-        for x, (p, p_end) in self._spans:
-            for y, (q, q_end) in to._spans:
-                if p < q_end and q < p_end and _meet(self._tensors[x], to._tensors[y]):
+        (k, k_end), (v, v_end), (n, n_end) = self._spans
+        (tk, tk_end), (tv, tv_end), (tn, tn_end) = to._spans
+        if (k < tk_end and tk < k_end or k < tv_end and tv < k_end or v < tk_end and tk < v_end or
+                v < tv_end and tv < v_end or n < tn_end and tn < n_end):
+            for x, y in (("k_pages", "k_pages"), ("k_pages", "v_pages"), ("v_pages", "k_pages"),
+                         ("v_pages", "v_pages"), ("lens", "lens")):
+                if _meet(self._tensors[x], to._tensors[y]):
                     raise ValueError("the destination shares memory with the cache (%s and %s)" % (y, x))
 
 
