@@ -1530,7 +1530,8 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     else launch_attend<false>(a, P.blocks, grid_x, s);
     int rc = launched();
     if (rc) return rc;
-    const uint32_t parts = a.logits ? (uint32_t)((P.logit_stride - 1) / kMassTokens + 1) : 0;
+    // a mass of no tokens: one part that reports the sequences that have some
+    const uint32_t parts = a.logits ? (uint32_t)((P.logit_stride - 1) / kMassTokens + 1) : Q.mass_out ? 1 : 0;
     if (a.runs || parts) {
         const dim3 grid((a.runs ? Q.heads : 0) + parts * cache->kv_heads, cache->batch);
         if (bf16) k_join<true><<<grid, kJoinThreads, 0, s>>>(a);

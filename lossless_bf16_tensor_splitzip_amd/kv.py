@@ -363,6 +363,8 @@ class KVCache:
             self._here(lse, "lse")
             _no_grad(lse, "lse")
         masses = _NO_MASS if mass is None and mass_out is None else self._mass_pair(mass, mass_out)
+        if masses[1] == 0:      # a mass of no tokens has no address: one that is not written to stands for it
+            masses = (None, self.args.lens, 0, 0, 0, 0, 0)
         qp, q0, q1 = _place(q, "queries", False)
         if out is None:
             with torch.cuda.stream(stream):
