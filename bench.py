@@ -54,7 +54,8 @@ def parse():
                          "at 2^16, 2^18, ..., 2^30 elements and print them as one JSON line")
     ap.add_argument("--kv", metavar="CASE", nargs="?", const="all",
                     help="instead of the benchmark, time the key-value cache operators on the cases "
-                         "of perf/operators.py (or the one named) and print them as one JSON line")
+                         "of perf/operators.py (or the one named) and on forms that they leave "
+                         "out (forms: only those), and print them as one JSON line")
     ap.add_argument("--probes", action="store_true",
                     help="instead of the benchmark, run the probes of the part's costs that the "
                          "design rests on (reference-stream library) and print them as one JSON line")
@@ -429,6 +430,83 @@ def kv_operators(only=None):
                              "floor_us": round(nbytes / rate / 1e3, 2),
                              "GBps": round(nbytes / us["kernel"] / 1e3, 0)}
         del states
+    if only in (None, "forms"):
+        out["forms"] = kv_forms(P, timed, rate)
+    return out
+
+
+def kv_forms(P, timed, rate):
+    """The forms of the key-value cache operators that the cases leave out:
+    evictions in place (all masses distinct, so that nearly every row behind the
+    first evicted one moves), tables and masses far wider than the sequences,
+    masses of more than 32768 tokens, rows in pinned host memory.  us a pass, and
+    the floor at the copy's rate."""
+    import statistics
+
+    import torch
+
+    import lossless_bf16_tensor_splitzip_amd as S
+
+    P.own = True
+    out = {}
+
+    def note(name, fn, nbytes, passes=40, less=None):
+        timed(fn, 6)
+        us = statistics.median(timed(fn, passes) - (timed(less, passes) if less else 0.0) for _ in range(7))
+        out[name] = {"us": round(us, 2), "floor_us": round(nbytes / rate / 1e3, 2)}
+
+    def evict(name, batch, longest, budget, page=16, holds=0, in_place=False):
+        case = dict(op="evict", batch=batch, longest=longest, spread="same", budget=budget, sinks=4, recent=256,
+                    kv_heads=8, dim=128, page=page, dtype="bf16", layout="hnd")
+        states = [P.prepare(case, seed) for seed in range(2)]
+        full = states[0].lens.clone()
+        for st in states:
+            st.mass = torch.rand(batch, 8, longest, device="cuda").argsort(2).float() / longest
+            if holds:       # a table and masses for that many tokens
+                st.mass = torch.nn.functional.pad(st.mass, (0, holds - longest))
+                st.mass_out = torch.empty_like(st.mass)
+                st.table = torch.nn.functional.pad(st.table, (0, holds // page - st.table.shape[1]))
+                st.cache = S.KVCache(st.k, st.v, st.table, st.lens)
+
+        def run(k):
+            st = states[k % 2]
+            if in_place:
+                st.lens.copy_(full)
+            st.cache.evict(st.mass, budget, sinks=4, recent=256, to=None if in_place else st.to, kept=st.kept,
+                           mass_out=st.mass_out)
+
+        note(name, run, P.work(case)["bytes"], less=(lambda k: states[k % 2].lens.copy_(full)) if in_place else None)
+
+    evict("evict_in_place_16x4096_to_2048", 16, 4096, 2048, in_place=True)
+    evict("evict_in_place_32768_to_8192", 1, 32768, 8192, 64, in_place=True)
+    evict("evict_in_place_32768_to_32000", 1, 32768, 32000, 64, in_place=True)
+    evict("evict_in_place_64x4096_to_4000", 64, 4096, 4000, in_place=True)
+    evict("evict_16x4096_to_2048", 16, 4096, 2048)
+    evict("evict_16x4096_to_2048_table_for_16384", 16, 4096, 2048, holds=16384)
+    evict("evict_16x4096_to_2048_table_for_131072", 16, 4096, 2048, holds=131072)
+    evict("evict_32768_to_8192", 1, 32768, 8192, 64)
+    evict("evict_32768_to_8192_table_for_131072", 1, 32768, 8192, 64, holds=131072)
+    evict("evict_131072_to_32768", 1, 131072, 32768, 64)
+
+    for batch, longest in ((1024, 64), (512, 64), (1024, 300), (64, 300)):
+        case = dict(op="attend", batch=batch, longest=longest, spread="same", heads=32, kv_heads=8, dim=128, page=16,
+                    dtype="bf16", layout="hnd", window=0, sinks=0, mass=False)
+        states = [P.prepare(case, seed) for seed in range(2)]
+        for width in (0, 512):
+            for st in states:
+                if width:
+                    st.table = torch.nn.functional.pad(st.table, (0, width - st.table.shape[1]))
+                    st.cache = S.KVCache(st.k, st.v, st.table, st.lens)
+                    st.ws = S.KVWorkspace(st.cache, 32)
+            note("attend_%dx%d%s" % (batch, longest, "_table_for_8192" if width else ""),
+                 lambda k: P.run(states[k % 2]), P.work(case)["bytes"])
+
+    case = dict(op="gather", batch=1, longest=32768, spread="same", new="all", kv_heads=8, dim=128, page=64,
+                dtype="bf16", layout="nhd")
+    st = P.prepare(case, 0)
+    k, v = (torch.empty(8, 32768, 128, dtype=torch.bfloat16).pin_memory().transpose(0, 1) for _ in range(2))
+    note("gather_32768_pinned", lambda i: st.cache.gather(k, v, st.cu), P.work(case)["bytes"], passes=8)
+    note("append_32768_pinned", lambda i: st.cache.append(k, v, st.cu), P.work(case)["bytes"], passes=8)
     return out
 
 
