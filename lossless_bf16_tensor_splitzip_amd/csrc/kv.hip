@@ -196,8 +196,8 @@ __global__ __launch_bounds__(kRowThreads) void k_rows(RowArgs a) {
 // 32768 tokens of one sequence 37 us against 30.)
 //
 // 32 sequences of 32768 tokens, 8 KV heads of 128, 8 query heads each: 4.30 GB
-// in 643 us, 6.7 TB/s, the rate of a bare read stream.  One sequence: 30 us, 26
-// of them here and 4.5 in the join's launch.  48 sequences of 0 to 8192: 43 us.
+// in 642 us, 6.7 TB/s, the rate of a bare read stream.  One sequence: 30 us, 26
+// of them here and 4.5 in the join's launch.  48 sequences of 0 to 8192: 44 us.
 // A run without any token takes 4 (dim 64) to 6.5 us (24 rows of dim 256).
 
 constexpr int kWaves = 4;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             total = blk.total;
         } else {
             // Every wave sums some blocks, then all of them look at the sums
-            // (1024 sequences of 64 tokens in a table for 8192: 92 us, and 214
+            // (1024 sequences of 64 tokens in a table for 8192: 96 us, and 214
             // where every wave and every join read all of the lengths).
             for (uint32_t i = wave; i < blocks; i += kWaves) {
                 const uint32_t b = i * 64 + lane;
@@ -532,8 +532,8 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             return (uint32_t)__ballot(ok);
         };
         // Rows of whole cache lines pass the caches by (32 sequences of 32768 tokens
-        // 644 us, through them 718); others share lines with their neighbours and
-        // go through them (dim 80, 16 x 8192 tokens: 85 us, past them 113).
+        // 642 us, through them 722); others share lines with their neighbours and
+        // go through them (dim 80, 16 x 8192 tokens: 70 us, past them 88).
         auto load_kv = [](const uint16_t *p) { return EXACT ? load_once(p) : *(const u32x4 *)p; };
         auto load_kv8 = [](const uint16_t *p) {
             return EXACT ? __builtin_nontemporal_load((const u32x2 *)p) : *(const u32x2 *)p;
@@ -1023,7 +1023,8 @@ constexpr int kSelHeld = 32;       // masses a thread can hold
 
 // One workgroup per sequence and KV head: 8 us for 4096 tokens, 19 us for 32768
 // (3 until the masses are there, 4.5, 2 and 2 for the passes, 5.5 to count and
-// place what stays; the instructions of one compute unit bound it).  Wave w has the run of tokens from
+// place what stays; the instructions of one compute unit bound it), 180 us for
+// 131072, whose masses are read again by every pass.  Wave w has the run of tokens from
 // w * span; lane l its tokens l, l + 64, ..., HELD of them in registers (all
 // of them where span is at most 64 HELD, and then the masses are read once);
 // HELD 0: read again by every pass.
@@ -1176,8 +1177,9 @@ __global__ __launch_bounds__(kSelThreads) void k_select(EvictArgs a) {
 
 constexpr int kMoveThreads = 512;
 // Rows a thread moves at a time: apart from the source, where workgroups are
-// many, and in place, where one has a whole column (32000 of 32768 tokens kept,
-// 8 KV heads: 218 us with 2, 145 with 4, 111 with 8).
+// many, and in place, where one has a whole column (one sequence of 32768
+// tokens, 8 KV heads of 128, all masses distinct: to 8192 98 us with 2, 70 with
+// 4, 55 with 8, to 32000 366, 242 and 186).
 constexpr int kMoveApart = 4, kMoveInPlace = 8;
 constexpr uint32_t kMoveParts = 65536;
 constexpr uint32_t kMoveRows = 64;      // most rows side by side in a workgroup
@@ -1189,9 +1191,9 @@ __host__ __device__ inline uint32_t move_rows(uint32_t chunk) { return kMoveThre
 // step itself: they wait until all its loads have arrived (the barrier), and
 // steps need no other order.  Columns share nothing.  Memory bounds it where
 // there are workgroups enough: 16 x 4096 tokens of 8 heads of 128 to half,
-// 268 MB, in 50 us.  In place with few columns a step's three loads in turn do
-// (one sequence of 32768 tokens of 8 heads to 8192 in 59 us, selection included);
-// looking the next step's places up ahead gained nothing.
+// 268 MB, in 54 us, in place too.  In place with few columns a step's three loads
+// in turn do (one sequence of 32768 tokens of 8 heads to 8192 in 55 us, selection
+// included); looking the next step's places up ahead gained nothing.
 template <bool LINES, int U>
 __global__ __launch_bounds__(kMoveThreads) void k_move(EvictArgs a) {
     __shared__ uint64_t from[kMoveRows * U], dest[kMoveRows * U];
@@ -1364,9 +1366,9 @@ struct AttendPlan {
 };
 
 // As many runs as workgroups are resident on 256 compute units, which the
-// registers of k_attend decide.  16 sequences of 8192 tokens, us: dim 64 122
-// with 512 runs, 113 with 768, 124 with 1024; dim 128 103, 108, 102; dim 256
-// 97 with 256, 100 with 512, 104 with 768; 2 sequences, dim 256 21 and 27.
+// registers of k_attend decide.  16 sequences of 8192 tokens, 8 KV heads, us with
+// 256, 512, 768 and 1024 runs: dim 64 71, 54, 52, 57; dim 128 96, 91, 94, 92;
+// dim 256 171, 175, 185, 185; 2 sequences, dim 256 31, 36, 43, 48.
 inline uint32_t runs_for(uint32_t dim, uint32_t blocks) {
     return dim <= 64 ? (blocks == 1 ? 768 : blocks == 2 ? 512 : 256) : dim <= 128 && blocks == 1 ? 512 : 256;
 }
@@ -1381,8 +1383,9 @@ bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, 
     // K and V are read once for every row tile: of 64 rows, or 32 where the
     // accumulators of 64 would not fit the registers, or where there is so little
     // to read that more and shorter workgroups win (64 rows against 32, dim 128,
-    // 64 rows a KV head, us: 256 units 20 and 16, 512 25 and 23, 768 35.2 and
-    // 34.2, 8192 133 and 201).
+    // 64 rows a KV head, us: 256 units 24 and 18, 512 26 and 24, 768 35.3 and
+    // 33.9, 8192 147 and 213).  Units are of what the table can hold: the lengths
+    // are on the device.
     const uint32_t most = c->head_dim <= 128 && kv_units >= 1024 ? 64 : 32;
     p.row_tiles = (p.group - 1) / most + 1;
     p.rows = (p.group - 1) / p.row_tiles + 1;
@@ -1514,9 +1517,9 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
     const uint32_t units = seen ? (uint32_t)((seen - 1) / kUnit + 1) : 1;
     // Whole, with few units a KV head: no join (5 us), no search for the run's
     // place.  Split/whole in us, KV heads by units (dim 128, batches of equal and
-    // of ragged lengths): 64 x 2 11.1/9.6 and 10.8/9.0, 64 x 4 11.7/14.5 and
-    // 11.1/13.5, 256 x 4 22.0/16.8 and 14.3/14.0, 256 x 8 33.4/28.5 and 17.0/23.7,
-    // 2048 x 4 107/98 and 50/38, 2048 x 32 666/727 and 132/161.
+    // of ragged lengths): 64 x 2 11.1/8.5 and 10.5/7.8, 64 x 4 11.5/14.1 and
+    // 11.1/13.2, 256 x 4 20.0/16.1 and 13.1/13.6, 256 x 8 30.3/27.3 and 16.1/23.6,
+    // 2048 x 4 96/89 and 41/38, 2048 x 32 650/643 and 123/155.
     const uint64_t tiles = (uint64_t)cache->batch * cache->kv_heads * P.row_tiles;
     const bool whole = tiles < 1u << 24 && (units <= 2 || (units <= 4 && tiles >= 256));      // a grid's limit
     a.runs = whole ? 0 : tiles * units < P.runs ? (uint32_t)(tiles * units) : P.runs;
@@ -1585,6 +1588,9 @@ int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *t
     a.chunks = (pieces + a.chunk - 1) / a.chunk;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const dim3 heads(cache->kv_heads, cache->batch);
+    // By the longest there can be; the lengths are on the device.  16 x 4096 tokens
+    // in a table and masses for 4096, 16384 and 131072: 7.2, 12.1 and 10.5 us, one
+    // sequence of 32768 in those for 32768 and 131072 19 and 45.
     const uint64_t longest = all < B.mass_len ? all : B.mass_len;
     if (longest <= 4 * kSelThreads) k_select<4><<<heads, kSelThreads, 0, s>>>(a);
     else if (longest <= kSelHeld * kSelThreads) k_select<kSelHeld><<<heads, kSelThreads, 0, s>>>(a);
@@ -1602,9 +1608,10 @@ int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *t
         a.per_wg *= step;
     }
     const dim3 grid(parts, cache->kv_heads * 2 * a.chunks, cache->batch);
-    // Apart, rows of whole cache lines pass the caches by, as in k_attend; what is
-    // moved in place stays in them (through them 75 us, past them 87: 64 x 4096 to
-    // 4000 tokens of 8 heads).
+    // Apart, rows of whole cache lines pass the caches by, as in k_attend; in place
+    // they go through them (8 heads of 128, all masses distinct, through and past
+    // them: 32768 to 8192 tokens 55 and 68 us, to 32000 186 and 209, 16 x 4096 to
+    // 2048 59 and 62, 64 x 4096 to 4000 438 and 433).
     if (share) k_move<false, kMoveInPlace><<<grid, kMoveThreads, 0, s>>>(a);
     else if (cache->head_dim % 64 == 0) k_move<true, kMoveApart><<<grid, kMoveThreads, 0, s>>>(a);
     else k_move<false, kMoveApart><<<grid, kMoveThreads, 0, s>>>(a);
