@@ -112,6 +112,12 @@ def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
     return found(p - q, 0)
 
 
+def _same(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two tensors of one shape and type are the same elements."""
+    return x.data_ptr() == y.data_ptr() and all(
+        a == b for n, a, b in zip(x.shape, x.stride(), y.stride()) if n > 1)
+
+
 def _plain(t: torch.Tensor, dtype, dims: int, what: str) -> None:
     if not t.is_cuda:
         raise ValueError("the %s must be on the GPU" % what)
@@ -223,7 +229,7 @@ class KVCache:
         vp, v0, v1 = _place(v, "V rows", written)
         if written and vp < kp + _reach(size, k0, k1) and kp < vp + _reach(size, v0, v1) and _meet(k, v):
             raise ValueError("the K rows and the V rows overlap in memory")
-        if self._pools_meet and not written and not (self._one_pool and (kp, k0, k1) == (vp, v0, v1)):
+        if self._pools_meet and not written and not (self._one_pool and _same(k, v)):
             raise ValueError("K and V rows that differ cannot be written to pools that share memory")
         return ctypes.byref(_abi.KVRows(kp, vp, k0, k1, v0, v1, size[0], 0, cu.data_ptr(),
                                         None if start is None else start.data_ptr()))
@@ -373,7 +379,7 @@ class KVCache:
         # the queries themselves, or apart from them: another workgroup's output
         # must not land in queries that are still to be read
         if (out is not q and op < qp + 2 * ((size[0] - 1) * q0 + (heads - 1) * q1 + size[2]) and
-                qp < op + _reach(size, o0, o1) and (op, o0, o1) != (qp, q0, q1) and _meet(q, out)):
+                qp < op + _reach(size, o0, o1) and not _same(q, out) and _meet(q, out)):
             raise ValueError("the output overlaps the queries without being the same")
         query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), *masses[:6], heads, window,
                              sinks, self.head_dim ** -0.5 if scale is None else scale, masses[6], 0)

@@ -60,6 +60,9 @@ def outputs(new, to_gpu, runs):
     refused(m.cache.attend, q, ws, out=packed.view(-1)[:512].view(4, 2, 64).transpose(0, 1))
     runs(m.cache.attend, q, ws, out=packed[:2, 4:])              # beside them
     runs(m.cache.attend, q, ws, out=packed[:2, :4])              # in their place
+    one = to_gpu(R.make([20], 2, 64, 16, torch.bfloat16, heads=4, seed=1))
+    q = packed[:1, :4]                                           # of one sequence, whatever its stride
+    runs(one.cache.attend, q, S.KVWorkspace(one.cache, 4), out=q.as_strided((1, 4, 64), (8, 64, 1)))
 
 
 def gathered(new, to_gpu, runs):
@@ -87,6 +90,7 @@ def pools(new, to_gpu, runs):
     runs(one.attend, m.gq, S.KVWorkspace(one, 4), out=torch.zeros_like(m.gq))
     runs(one.gather, rows[0], rows[1], cu)
     runs(one.append, rows[0], rows[0], cu)
+    runs(one.append, rows[0, :1], rows[0, :1].as_strided((1, 2, 64), (8, 64, 1)), cu)
     refused(one.append, rows[0], rows[1], cu)
     refused(half.append, rows[0], rows[0], cu)
     refused(one.evict, mass, 8, kept=kept)
