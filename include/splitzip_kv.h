@@ -104,7 +104,7 @@ typedef struct splitzip_kv_query {
                                     i reads KV head i / (heads / kv_heads)       */
     uint64_t q_stride[2];        /* multiples of 8                               */
     uint16_t *out;               /* laid out like q, with strides of its own; may
-                                    be q itself                                  */
+                                    be q itself, and else shares no memory with it */
     uint64_t out_stride[2];
     float *lse;                  /* NULL, or [batch][heads]: log of the sum of
                                     exp(logit); -inf where nothing is visible    */
@@ -148,8 +148,10 @@ typedef struct splitzip_kv_budget {
 void splitzip_kv_struct_sizes(size_t sizes[4]);
 
 /* Copy rows into the cache / cached tokens into rows.  With start NULL, lens
- * already counts the appended tokens.  Rows behind cu[batch] are left alone (an append does not
- * read them, a gather does not write them).  Bit-exact copies.
+ * already counts the appended tokens.  Rows behind cu[batch] are left alone (an
+ * append does not read them, a gather does not write them).  Bit-exact copies.
+ * What is written shares no memory with what is read, nor its K with its V
+ * (where both pools are one, K and V rows may be one).
  * Errors: INVALID, HIP. */
 int splitzip_kv_append(const splitzip_kv_cache *cache, const splitzip_kv_rows *rows,
                        int32_t *d_status, void *stream);
@@ -188,7 +190,8 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
  * kv_heads, head_dim and dtype.  It is the cache itself (same table, pools and
  * lens: compaction in place) or pages and lens that share no memory with it;
  * a `to` that shares its table or lens or a pool's start with the cache is
- * taken as in place and must be equal to it in all fields.  to's table must
+ * taken as in place and must be equal to it in all fields.  Its K and V pools
+ * share no memory in place.  to's table must
  * hold budget tokens, or its width the whole cache's.
  * Errors: INVALID (also sinks + recent > budget, budget 0), HIP. */
 int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *to,

@@ -152,10 +152,12 @@ class KVCache:
     expanded) and ``lens`` int32 [batch].  It holds the caller's tensors and
     allocates nothing; table and lens may be changed between calls.
 
-    Every call takes ``status``, an int32 tensor that the caller has set to 0:
-    bits _abi.KV_BAD_PAGE (a page number outside the pools: its tokens are left
-    out), KV_BAD_LEN (a length outside the table or the mass: cut) and
-    KV_BAD_ROWS (rows without a place: left out) are ORed into it."""
+    Every call takes ``stream`` (None: the current one), on which its tensors
+    must be ready and be kept until it has run, and ``status``, an int32 tensor
+    that the caller has set to 0: bits _abi.KV_BAD_PAGE (a page number outside
+    the pools: its tokens are left out), KV_BAD_LEN (a length outside the table
+    or the mass: cut) and KV_BAD_ROWS (rows without a place: left out) are ORed
+    into it."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
         if k_pages.dtype not in _DTYPES:
@@ -330,7 +332,8 @@ class KVCache:
         head_dim], over its cached tokens: all, or with ``window`` the last
         ``window`` and the first ``sinks``.  ``scale`` defaults to
         head_dim ** -0.5.  Returns ``out``, shaped like q; a sequence with
-        nothing visible gives zeros; ``out`` may be ``q``.
+        nothing visible gives zeros; ``out`` may be ``q``, else they must not
+        overlap.
 
         ``lse`` (float32 [batch, heads]) receives the log of the sum of
         exponentials.  With ``mass`` (float32 [batch, kv_heads, tokens]) the
