@@ -49,6 +49,9 @@ extern "C" {
                                     or a first position below 0 or rows that
                                     pass the table's end                         */
 
+#define SPLITZIP_KV_NO_PAGE 8    /* no page left: a sequence is shorter than asked for */
+#define SPLITZIP_KV_BAD_PARENT 16 /* a parent outside the batch: the sequence is left */
+
 /* No window: every cached token is visible. */
 #define SPLITZIP_KV_ALL 0xffffffffu
 
@@ -58,13 +61,16 @@ extern "C" {
 #define SPLITZIP_KV_MAX_KV_HEADS 4096u
 #define SPLITZIP_KV_MAX_HEADS 65535u
 #define SPLITZIP_KV_MAX_ROWS 0x7fffffffu
+#define SPLITZIP_KV_MAX_PAGES 0x1000000u  /* of the operators on pages */
+#define SPLITZIP_KV_MAX_LAYERS 1024u
 
 /* Limits: head_dim a multiple of 8 in 8..256; all strides multiples of 8 (16
  * bytes) and pools 16-byte aligned; 1..65536 slots a page; max_pages *
  * page_size below 2^31; rows of the table at least max_pages apart;
  * num_pages in 1..2^31-1; batch 0..65535; 1..4096 KV heads; the pools'
  * largest offset below 2^40 elements.  A page that the table names twice (for
- * two sequences or in one) may be read, not written. */
+ * two sequences or in one) may be read, not written; splitzip_kv_pages_resize
+ * sees to it that none is. */
 typedef struct splitzip_kv_cache {
     uint16_t *k, *v;             /* pools (bf16 or fp16 bit patterns)            */
     uint64_t k_stride[3];        /* elements between pages, heads, slots         */
@@ -196,6 +202,71 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
  * Errors: INVALID (also sinks + recent > budget, budget 0), HIP. */
 int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *to,
                       const splitzip_kv_budget *budget, int32_t *d_status, void *stream);
+
+/* Who has which pages: the pools of a model's layers, which share one table
+ * and lengths, and how many table entries name each page.  A page that none
+ * names is free.  The cache gives table, lens, shape and strides of all
+ * layers (its own k and v are not looked at); table and lens are written. */
+typedef struct splitzip_kv_pages {
+    const splitzip_kv_cache *cache;
+    uint16_t *const *k, *const *v;   /* [layers], in host memory: the layers' pools   */
+    uint32_t layers;                 /* 1..SPLITZIP_KV_MAX_LAYERS                     */
+    uint32_t reserved;
+    void *state;                     /* device memory; its first num_pages int32 are
+                                        the counts, to be read; the rest, and the
+                                        counts between calls, are the operators'     */
+    size_t state_bytes;
+} splitzip_kv_pages;
+
+size_t splitzip_kv_pages_struct_size(void);
+
+/* Bytes of state for caches of this shape (batch and num_pages; no pointer is
+ * read), 0 for invalid shapes: more than SPLITZIP_KV_MAX_PAGES pages, pages of
+ * 32 GiB.  Calls on one state must run one after another.  batch * max_pages
+ * must be below 2^31, the layers' pools share no memory. */
+size_t splitzip_kv_pages_state_size(const splitzip_kv_cache *cache);
+
+/* Count: the state from the table.  Entries within a sequence's length name
+ * its pages, those behind are set to -1.  The first call on a state, and the
+ * one after the table has been written by others.  (An entry outside the pool
+ * within a length becomes -1: SPLITZIP_KV_BAD_PAGE.)
+ * Errors of all page operators: INVALID, WORKSPACE (a state too small), HIP. */
+int splitzip_kv_pages_count(const splitzip_kv_pages *pages, int32_t *d_status, void *stream);
+
+/* Fork: sequence b becomes a copy of sequence parents[b], all at once: the
+ * same pages, also the last one that is not full, and the length.  Parent -1
+ * frees the sequence (no page, length 0), b itself leaves it.  Nothing is
+ * copied but table and lengths. */
+int splitzip_kv_pages_fork(const splitzip_kv_pages *pages, const int32_t *parents, int32_t *d_status, void *stream);
+
+/* Resize: the sequences' lengths become lens (device memory; may be the
+ * cache's own, which frees the pages behind them).  Pages behind a new length
+ * are freed first.  Then, in the order of sequences, each is given the pages
+ * that positions up to its new length need, and where it grows from within a
+ * page that others name, a page of its own first, to which the slots in use
+ * are copied in every layer (of the sequences that all grow in one page that
+ * no other names the first keeps it).  The pages given are the free ones in
+ * ascending order.  When they run out a sequence's length becomes what its
+ * pages hold, or stays as it was if its copy could not be had
+ * (SPLITZIP_KV_NO_PAGE).  The tokens from the old length on are the caller's
+ * to append. */
+int splitzip_kv_pages_resize(const splitzip_kv_pages *pages, const int32_t *lens, int32_t *d_status, void *stream);
+
+/* Compact: with n pages in use, the pages in use from n on move to the free
+ * ones below, the last to the first, in every layer; table and counts follow.
+ * moved (NULL or [num_pages]): the new number of each page, -1 for free ones;
+ * used (NULL or one int32): n. */
+int splitzip_kv_pages_compact(const splitzip_kv_pages *pages, int32_t *moved, int32_t *used, int32_t *d_status,
+                              void *stream);
+
+/* Copy: K and V of pages src[i] of `from` to pages dst[i] of `to`, i < n, in
+ * every layer, whatever the strides.  Both have the same layers, page_size,
+ * kv_heads, head_dim and dtype; tables, lengths and state are not looked at.
+ * No page is named in dst twice, nor in dst and src where `to` has the pools
+ * of `from`; other pools share no memory.  Pairs with a page outside its pool
+ * are left out (SPLITZIP_KV_BAD_PAGE). */
+int splitzip_kv_pages_copy(const splitzip_kv_pages *from, const splitzip_kv_pages *to, const int32_t *src,
+                           const int32_t *dst, uint32_t n, int32_t *d_status, void *stream);
 
 #ifdef __cplusplus
 }

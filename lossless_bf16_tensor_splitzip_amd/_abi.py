@@ -172,6 +172,10 @@ KV_ALL = 0xFFFFFFFF
 KV_BAD_PAGE = 1
 KV_BAD_LEN = 2
 KV_BAD_ROWS = 4
+KV_NO_PAGE = 8
+KV_BAD_PARENT = 16
+KV_MAX_PAGES = 1 << 24
+KV_MAX_LAYERS = 1024
 
 _U32 = ctypes.c_uint32
 
@@ -220,6 +224,14 @@ class KVBudget(ctypes.Structure):
     ]
 
 
+class KVPagesArgs(ctypes.Structure):
+    """Mirror of splitzip_kv_pages."""
+    _fields_ = [
+        ("cache", _P), ("k", _P), ("v", _P), ("layers", _U32), ("reserved", _U32),
+        ("state", _P), ("state_bytes", _SZ),
+    ]
+
+
 KV_STRUCTS = (KVCacheArgs, KVRows, KVQuery, KVBudget)
 
 KV_SIGNATURES = {
@@ -229,6 +241,13 @@ KV_SIGNATURES = {
     "splitzip_kv_attend_workspace_size": (_SZ, [_P, _U32, _U32]),
     "splitzip_kv_attend": (ctypes.c_int, [_P, _P, _P, _SZ, _P, _P]),
     "splitzip_kv_evict": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+    "splitzip_kv_pages_struct_size": (_SZ, []),
+    "splitzip_kv_pages_state_size": (_SZ, [_P]),
+    "splitzip_kv_pages_count": (ctypes.c_int, [_P, _P, _P]),
+    "splitzip_kv_pages_fork": (ctypes.c_int, [_P, _P, _P, _P]),
+    "splitzip_kv_pages_resize": (ctypes.c_int, [_P, _P, _P, _P]),
+    "splitzip_kv_pages_compact": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+    "splitzip_kv_pages_copy": (ctypes.c_int, [_P, _P, _P, _P, _U32, _P, _P]),
 }
 
 _kv = None
@@ -250,7 +269,8 @@ def kv_lib():
         fn.argtypes = args
     sizes = (ctypes.c_size_t * len(KV_STRUCTS))()
     handle.splitzip_kv_struct_sizes(sizes)
-    if list(sizes) != [ctypes.sizeof(t) for t in KV_STRUCTS]:
+    if list(sizes) != [ctypes.sizeof(t) for t in KV_STRUCTS] or \
+            handle.splitzip_kv_pages_struct_size() != ctypes.sizeof(KVPagesArgs):
         raise RuntimeError("struct layout mismatch between the library and the binding")
     _kv = handle
     return handle
@@ -408,3 +428,32 @@ def splitzip_kv_attend(cache, query, d_ws: int, ws_bytes: int, d_status: int, st
 def splitzip_kv_evict(cache, to, budget, d_status: int, stream: int) -> int:
     return kv_lib().splitzip_kv_evict(ctypes.byref(cache), ctypes.byref(to), ctypes.byref(budget),
                                       d_status, stream)
+
+
+def splitzip_kv_pages_struct_size() -> int:
+    return kv_lib().splitzip_kv_pages_struct_size()
+
+
+def splitzip_kv_pages_state_size(cache) -> int:
+    return kv_lib().splitzip_kv_pages_state_size(ctypes.byref(cache))
+
+
+def splitzip_kv_pages_count(pages, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_pages_count(ctypes.byref(pages), d_status, stream)
+
+
+def splitzip_kv_pages_fork(pages, parents: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_pages_fork(ctypes.byref(pages), parents, d_status, stream)
+
+
+def splitzip_kv_pages_resize(pages, lens: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_pages_resize(ctypes.byref(pages), lens, d_status, stream)
+
+
+def splitzip_kv_pages_compact(pages, moved: int, used: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_pages_compact(ctypes.byref(pages), moved, used, d_status, stream)
+
+
+def splitzip_kv_pages_copy(from_pages, to_pages, src: int, dst: int, n: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_pages_copy(ctypes.byref(from_pages), ctypes.byref(to_pages), src, dst, n, d_status,
+                                           stream)

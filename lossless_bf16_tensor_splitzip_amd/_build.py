@@ -13,7 +13,7 @@ SRC = os.path.join(PKG, "csrc", "splitzip.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsplitzip.so")
-KV_SRC = os.path.join(PKG, "csrc", "kv.hip")
+KV_SRC = [os.path.join(PKG, "csrc", name) for name in ("kv.hip", "kv_pages.hip")]
 KV_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_kv.so")
 CEILING_SRC = os.path.join(PKG, "csrc", "ceiling.hip")
 CEILING_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_ceiling.so")
@@ -36,10 +36,10 @@ def hipcc() -> str:
     return cand if os.path.exists(cand) else "hipcc"
 
 
-def _compile(src: str, lib_path: str, verbose: bool) -> str:
+def _compile(src, lib_path: str, verbose: bool) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = lib_path + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE, src, "-o", tmp]
+    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE] + ([src] if isinstance(src, str) else src) + ["-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln]
