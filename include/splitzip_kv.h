@@ -203,6 +203,36 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
 int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *to,
                       const splitzip_kv_budget *budget, int32_t *d_status, void *stream);
 
+/* Sequences with their first tokens in common: group g has sequences cu[g] ..
+ * cu[g+1]-1 of the batch, and of them the first shared[g] tokens (no more than
+ * its first sequence has) are the same.  Sequences in no group have none. */
+typedef struct splitzip_kv_groups {
+    const int32_t *cu;           /* [groups + 1], ascending                        */
+    const int32_t *shared;       /* [groups]                                       */
+    uint32_t groups;             /* 0..65535                                       */
+    uint32_t reserved;
+} splitzip_kv_groups;
+
+size_t splitzip_kv_groups_struct_size(void);
+
+/* As splitzip_kv_attend_workspace_size, for splitzip_kv_attend_shared with up
+ * to `groups` groups (0 and 1: the same as more). */
+size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t groups);
+
+/* What splitzip_kv_attend computes (window ALL, no mass), where K and V of the
+ * tokens that a group has in common are read once for all its sequences,
+ * through the table row of its first one: the others need only have the same
+ * values there, mostly in the same pages.  A sequence that is shorter than the
+ * tokens in common attends on its own.  The weights of the tokens in common
+ * are rounded to the cache's type once (half a step of it each); all other
+ * sums are held as in splitzip_kv_attend.  Ranges that decrease or leave the
+ * batch: BAD_ROWS, no tokens in common (where ranges overlap by that, their
+ * sequences' outputs mean nothing); shared below 0: BAD_LEN, taken as 0.
+ * Errors: INVALID (also a window or mass), WORKSPACE, HIP. */
+int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_query *query,
+                              const splitzip_kv_groups *groups, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                              void *stream);
+
 /* Who has which pages: the pools of a model's layers, which share one table
  * and lengths, and how many table entries name each page.  A page that none
  * names is free.  The cache gives table, lens, shape and strides of all

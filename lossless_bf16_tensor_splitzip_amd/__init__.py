@@ -19,9 +19,9 @@ from ._abi import CHUNK, Codebook, Meta, SplitZipError, lib  # noqa: F401
 from . import persist  # noqa: F401
 from .codec import (Batch, Workspace, calibrate, decode, decode_slot, decode_slots,  # noqa: F401
                     encode, payload_for, payload_size, read_codebook, read_meta)
-from .kv import KVCache, KVWorkspace  # noqa: F401
+from .kv import KVCache, KVSharedWorkspace, KVWorkspace  # noqa: F401
 from .kv_pages import KVPages  # noqa: F401
 
-__all__ = ["CHUNK", "Batch", "Codebook", "KVCache", "KVPages", "KVWorkspace", "Meta", "SplitZipError", "Workspace", "calibrate", "encode",
+__all__ = ["CHUNK", "Batch", "Codebook", "KVCache", "KVPages", "KVSharedWorkspace", "KVWorkspace", "Meta", "SplitZipError", "Workspace", "calibrate", "encode",
            "decode", "decode_slot", "decode_slots", "payload_for", "payload_size", "read_codebook", "read_meta",
            "lib", "persist"]

@@ -176,6 +176,7 @@ KV_NO_PAGE = 8
 KV_BAD_PARENT = 16
 KV_MAX_PAGES = 1 << 24
 KV_MAX_LAYERS = 1024
+KV_MAX_GROUPS = 65535
 
 _U32 = ctypes.c_uint32
 
@@ -224,6 +225,11 @@ class KVBudget(ctypes.Structure):
     ]
 
 
+class KVGroups(ctypes.Structure):
+    """Mirror of splitzip_kv_groups."""
+    _fields_ = [("cu", _P), ("shared", _P), ("groups", _U32), ("reserved", _U32)]
+
+
 class KVPagesArgs(ctypes.Structure):
     """Mirror of splitzip_kv_pages."""
     _fields_ = [
@@ -241,6 +247,9 @@ KV_SIGNATURES = {
     "splitzip_kv_attend_workspace_size": (_SZ, [_P, _U32, _U32]),
     "splitzip_kv_attend": (ctypes.c_int, [_P, _P, _P, _SZ, _P, _P]),
     "splitzip_kv_evict": (ctypes.c_int, [_P, _P, _P, _P, _P]),
+    "splitzip_kv_groups_struct_size": (_SZ, []),
+    "splitzip_kv_shared_workspace_size": (_SZ, [_P, _U32, _U32]),
+    "splitzip_kv_attend_shared": (ctypes.c_int, [_P, _P, _P, _P, _SZ, _P, _P]),
     "splitzip_kv_pages_struct_size": (_SZ, []),
     "splitzip_kv_pages_state_size": (_SZ, [_P]),
     "splitzip_kv_pages_count": (ctypes.c_int, [_P, _P, _P]),
@@ -270,6 +279,7 @@ def kv_lib():
     sizes = (ctypes.c_size_t * len(KV_STRUCTS))()
     handle.splitzip_kv_struct_sizes(sizes)
     if list(sizes) != [ctypes.sizeof(t) for t in KV_STRUCTS] or \
+            handle.splitzip_kv_groups_struct_size() != ctypes.sizeof(KVGroups) or \
             handle.splitzip_kv_pages_struct_size() != ctypes.sizeof(KVPagesArgs):
         raise RuntimeError("struct layout mismatch between the library and the binding")
     _kv = handle
@@ -428,6 +438,19 @@ def splitzip_kv_attend(cache, query, d_ws: int, ws_bytes: int, d_status: int, st
 def splitzip_kv_evict(cache, to, budget, d_status: int, stream: int) -> int:
     return kv_lib().splitzip_kv_evict(ctypes.byref(cache), ctypes.byref(to), ctypes.byref(budget),
                                       d_status, stream)
+
+
+def splitzip_kv_groups_struct_size() -> int:
+    return kv_lib().splitzip_kv_groups_struct_size()
+
+
+def splitzip_kv_shared_workspace_size(cache, heads: int, groups: int) -> int:
+    return kv_lib().splitzip_kv_shared_workspace_size(ctypes.byref(cache), heads, groups)
+
+
+def splitzip_kv_attend_shared(cache, query, groups, d_ws: int, ws_bytes: int, d_status: int, stream: int) -> int:
+    return kv_lib().splitzip_kv_attend_shared(ctypes.byref(cache), ctypes.byref(query), ctypes.byref(groups), d_ws, ws_bytes,
+                                              d_status, stream)
 
 
 def splitzip_kv_pages_struct_size() -> int:

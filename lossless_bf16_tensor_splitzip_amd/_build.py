@@ -13,7 +13,7 @@ SRC = os.path.join(PKG, "csrc", "splitzip.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsplitzip.so")
-KV_SRC = [os.path.join(PKG, "csrc", name) for name in ("kv.hip", "kv_pages.hip")]
+KV_SRC = [os.path.join(PKG, "csrc", name) for name in ("kv.hip", "kv_shared.hip", "kv_pages.hip")]
 KV_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_kv.so")
 CEILING_SRC = os.path.join(PKG, "csrc", "ceiling.hip")
 CEILING_LIB_PATH = os.path.join(LIB_DIR, "libsplitzip_ceiling.so")

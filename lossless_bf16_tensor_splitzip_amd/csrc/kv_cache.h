@@ -98,6 +98,8 @@ __device__ inline uint32_t lanes_below(uint64_t mask) {
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+
 inline int launched() { return hipGetLastError() == hipSuccess ? SPLITZIP_OK : SPLITZIP_ERR_HIP; }
 
 constexpr uint64_t kMaxOffset = 1ull << 40;      // elements

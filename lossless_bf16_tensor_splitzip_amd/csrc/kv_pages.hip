@@ -505,7 +505,6 @@ __global__ __launch_bounds__(kCopyThreads) void k_copy(CopyArgs a, Pools from, P
 // Host side
 // ---------------------------------------------------------------------------
 
-inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 inline uint32_t blocks_of(uint32_t pages) { return (pages - 1) / kBlock + 1; }
 
 bool pages_shape_ok(const splitzip_kv_cache *c) {

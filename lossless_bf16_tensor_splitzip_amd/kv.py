@@ -389,6 +389,65 @@ class KVCache:
         self._call("splitzip_kv_attend", stream, ctypes.byref(query), ws.buf.data_ptr(), ws.nbytes, self._status(status))
         return out
 
+    def attend_shared(self, q: torch.Tensor, cu: torch.Tensor, shared: torch.Tensor, ws: "KVSharedWorkspace",
+                      out: torch.Tensor | None = None, scale: float | None = None, lse: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """``attend`` over all cached tokens for a batch whose sequences begin
+        alike: sequences cu[g] .. cu[g+1]-1 (``cu`` int32 [groups + 1],
+        ascending) have their first ``shared``[g] tokens (int32 [groups], no
+        more than the first of them has) in common, and these are read once for
+        the group, through the table row of its first sequence.  The others
+        need the same values there, as after ``KVPages.fork``; one that is
+        shorter attends on its own, as do sequences outside ``cu``.  The
+        weights of tokens in common are rounded to the cache's type.  ``out``
+        and ``lse`` as in ``attend``."""
+        size, index = q.shape, self._index
+        if q.dtype is not self.dtype or len(size) != 3 or size[0] != self.batch or size[2] != self.head_dim:
+            raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
+                             % (self.dtype, self.batch, self.head_dim, q.dtype, tuple(size)))
+        if not q.get_device() == ws.buf.get_device() == cu.get_device() == shared.get_device() == index:
+            for t, what in ((q, "queries"), (ws.buf, "workspace"), (cu, "group ranges"), (shared, "tokens in common")):
+                self._here(t, what)
+        if q.requires_grad or _forward._current_level >= 0:
+            _no_grad(q, "queries")
+        heads = size[1]
+        if heads < 1 or heads % self.kv_heads:
+            raise ValueError("%d query heads do not divide over %d KV heads" % (heads, self.kv_heads))
+        groups = shared.shape[0] if shared.dim() == 1 else -1
+        if not (cu.dtype is shared.dtype is torch.int32 and cu.shape == (groups + 1,) and cu.is_contiguous() and
+                shared.is_contiguous()):
+            raise ValueError("group ranges and tokens in common must be contiguous int32 [groups + 1] and [groups], got %s %s and %s %s"
+                             % (cu.dtype, tuple(cu.shape), shared.dtype, tuple(shared.shape)))
+        if groups > _abi.KV_MAX_GROUPS:
+            raise ValueError("at most %d groups, got %d" % (_abi.KV_MAX_GROUPS, groups))
+        if out is not None:
+            if out.dtype is not self.dtype or out.shape != size:
+                raise ValueError("the output must be shaped like the queries")
+            if out.get_device() != index:
+                self._here(out, "output")
+            if out.requires_grad or _forward._current_level >= 0:
+                _no_grad(out, "output")
+        if lse is not None:
+            _plain(lse, torch.float32, 2, "lse")
+            if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))
+            self._here(lse, "lse")
+            _no_grad(lse, "lse")
+        qp, q0, q1 = _place(q, "queries", False)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(size, dtype=q.dtype, device=self.device)
+        op, o0, o1 = _place(out, "output", True)
+        if (out is not q and op < qp + 2 * ((size[0] - 1) * q0 + (heads - 1) * q1 + size[2]) and
+                qp < op + _reach(size, o0, o1) and not _same(q, out) and _meet(q, out)):
+            raise ValueError("the output overlaps the queries without being the same")
+        query = _abi.KVQuery(qp, q0, q1, op, o0, o1, None if lse is None else lse.data_ptr(), *_NO_MASS[:6], heads,
+                             _abi.KV_ALL, 0, self.head_dim ** -0.5 if scale is None else scale, 0, 0)
+        of = _abi.KVGroups(cu.data_ptr(), shared.data_ptr(), groups, 0)
+        self._call("splitzip_kv_attend_shared", stream, ctypes.byref(query), ctypes.byref(of), ws.buf.data_ptr(), ws.nbytes,
+                   self._status(status))
+        return out
+
     def evict(self, mass: torch.Tensor, budget: int, sinks: int = 0, recent: int = 0, to: "KVCache | None" = None,
               kept: torch.Tensor | None = None, mass_out: torch.Tensor | None = None,
               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -462,3 +521,15 @@ class KVWorkspace:
 
     def _buffer(self, nbytes: int, device) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+class KVSharedWorkspace(KVWorkspace):
+    """Device scratch for ``KVCache.attend_shared`` on caches shaped like
+    ``cache`` with ``heads`` query heads and up to ``groups`` groups.  One
+    workspace per stream that runs such calls concurrently."""
+
+    def __init__(self, cache: KVCache, heads: int, groups: int = _abi.KV_MAX_GROUPS):
+        self.nbytes = _abi.splitzip_kv_shared_workspace_size(cache.args, heads, groups)
+        if not self.nbytes:
+            raise ValueError("no workspace for %d query heads over %d KV heads in %d groups" % (heads, cache.kv_heads, groups))
+        self.buf = self._buffer(self.nbytes, cache.device)
