@@ -112,7 +112,9 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
     constexpr int PR = DP / 8;               // 16-byte pieces of a row
     constexpr int NP = T * PR / kSharedThreads;      // pieces a thread stages of K, of V
     constexpr int ST = T / 16;
-    constexpr float kLift = BF16 ? 0.f : 15.f;       // as in k_attend
+    // fp16 weights are held times 2^11, up to 2^4 above what the maximum of before
+    // allows: no more than 2^15, and steps of 2^-35 of the largest or less.
+    constexpr float kSlack = 4.f, kLift = BF16 ? 0.f : 11.f;
     auto at_least = [](float p) { return BF16 ? p : __builtin_amdgcn_fmed3f(p, p * 0x1p102f, 0x1p-24f); };
     // A row's pieces are stored in an order of its own, so that 16 lanes that
     // read one piece of 16 rows meet all banks.
@@ -120,12 +122,24 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
         return row * PR + (DP % 128 == 0 ? piece ^ (row & 15) : piece ^ (row >> 1 & 7));
     };
     __shared__ u32x4 s_k[2][T * PR], s_v[2][T * PR];
-    __shared__ uint8_t s_ok[2][T];
+    __shared__ uint64_t off_k[4][T], off_v[4][T], s_valid[4];      // of tiles, in turn
     uint32_t *s_block = (uint32_t *)s_k;
     static_assert(sizeof s_k >= 4 * kMaxBlocks, "sums of all blocks");
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim, kvh = a.c.kv_heads;
+    // This lane's places in a tile: where it puts its pieces, and what it reads
+    // of the first 16 rows (further ones are a constant away).
+    uint32_t put[NP], k_at[KS], v_at[4], v8_at[4];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) put[k] = spot((tid + k * kSharedThreads) / PR, (tid + k * kSharedThreads) % PR);
+#pragma unroll
+    for (int j = 0; j < KS; ++j) k_at[j] = spot(c16, j * 4 + g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v_at[i] = spot(g * 4 + i, c16);
+        v8_at[i] = spot(g * 4 + i, P16 * 16 + (c16 >> 1)) * 2 + (c16 & 1);
+    }
 
     if (blockIdx.x >= a.runs) {      // what every sequence has in common with its group
         const uint32_t b = (blockIdx.x - a.runs) * kSharedThreads + tid;
@@ -230,60 +244,74 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
             for (int j = 0; j < VC; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        // Staging: this thread's pieces of a tile, and the page numbers of the
-        // next one's.
+        // Staging: this thread's pieces of a tile.  A row's place is found by one
+        // lane, two tiles ahead (the waves take turns), from a page number loaded
+        // a tile before; the pieces' threads take it from LDS.
         const uint16_t *k_head = a.c.k + h * a.c.ks[1], *v_head = a.c.v + h * a.c.vs[1];
-        uint32_t page[NP];
         u32x4 kx[NP], vx[NP];
-        uint32_t ok = 0;
         auto row_of = [&](int k) { return (tid + k * kSharedThreads) / PR; };
         auto piece_of = [&](int k) { return (tid + k * kSharedThreads) % PR; };
-        auto pages_at = [&](uint32_t t0) {
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                const uint32_t t = t0 + row_of(k);
-                page[k] = t < end ? (uint32_t)table[div(t, a.c.page)] : 0xffffffffu;
-            }
+        const uint32_t tile0 = unit0, tile_end = (end - 1) / T + 1;
+        auto page_at = [&](uint32_t n) {
+            const uint32_t t = n * T + lane;
+            return lane < T && t < end ? (uint32_t)table[div(t, a.c.page)] : 0xffffffffu;
         };
-        auto fetch = [&](uint32_t t0) {
-            ok = 0;
+        auto place = [&](uint32_t n, uint32_t page) {
+            const uint32_t t = n * T + lane;
+            const bool in = lane < T && t < end, ok = in && page < a.c.num_pages;
+            if (in && !ok) report(a.status, SPLITZIP_KV_BAD_PAGE);
+            const uint32_t slot = t - div(t, a.c.page) * a.c.page.d;
+            if (lane < T) {
+                off_k[n & 3][lane] = ok ? page * a.c.ks[0] + slot * a.c.ks[2] : 0;
+                off_v[n & 3][lane] = ok ? page * a.c.vs[0] + slot * a.c.vs[2] : 0;
+            }
+            const uint64_t mask = __ballot(ok);
+            if (lane == 0) s_valid[n & 3] = mask;
+        };
+        auto valid_of = [&](uint32_t n) {
+            const uint64_t x = s_valid[n & 3];
+            return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+        };
+        auto fetch = [&](uint32_t n) {
+            const uint64_t valid = valid_of(n);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const uint32_t t = t0 + row_of(k), piece = piece_of(k);
+                const uint32_t row = row_of(k), piece = piece_of(k);
                 kx[k] = vx[k] = u32x4{0, 0, 0, 0};
-                if (t < end && page[k] >= a.c.num_pages) report(a.status, SPLITZIP_KV_BAD_PAGE);
-                if (t >= end || page[k] >= a.c.num_pages) continue;
-                ok |= 1u << k;
-                if (!EXACT && piece * 8 >= D) continue;
-                const uint32_t slot = t - div(t, a.c.page) * a.c.page.d;
-                kx[k] = load_once(k_head + page[k] * a.c.ks[0] + slot * a.c.ks[2] + piece * 8);
-                vx[k] = load_once(v_head + page[k] * a.c.vs[0] + slot * a.c.vs[2] + piece * 8);
+                if (!(valid >> row & 1) || (!EXACT && piece * 8 >= D)) continue;
+                kx[k] = *(const u32x4 *)(k_head + off_k[n & 3][row] + piece * 8);
+                vx[k] = *(const u32x4 *)(v_head + off_v[n & 3][row] + piece * 8);
             }
         };
 
-        uint32_t t0 = unit0 * T;
-        pages_at(t0);
-        fetch(t0);
-        pages_at(t0 + T);
         __syncthreads();        // the piece of work before, and the sums of blocks, have been read
+        const uint32_t turn = (wave - tile0) & 3;      // of the first four tiles this one is this wave's
+        uint32_t page = page_at(tile0 + turn);
+        if (turn < 2) {
+            place(tile0 + turn, page);
+            page = page_at(tile0 + turn + 4);
+        }
         if (unit0 == 0 && tid < members) {
             const uint32_t shares = whole ? 1 : cut.owner(u + units - 1) - blockIdx.x + 1;
             ((u32x4 *)a.notes)[((uint64_t)(first + member0 + tid) * kvh + h) * a.parts + part] =
                 u32x4{blockIdx.x, shares * 2 + (u != u_begin), tid * a.group, 0};
         }
-        for (int buf = 0; t0 < end; t0 += T, buf ^= 1) {
+        __syncthreads();
+        fetch(tile0);
+        for (uint32_t n = tile0; n < tile_end; ++n) {
+            u32x4 *const now_k = s_k[n & 1], *const now_v = s_v[n & 1];
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const uint32_t row = row_of(k), piece = piece_of(k);
-                s_k[buf][spot(row, piece)] = kx[k];
-                s_v[buf][spot(row, piece)] = vx[k];
-                if (piece == 0) s_ok[buf][row] = ok >> k & 1;
+                now_k[put[k]] = kx[k];
+                now_v[put[k]] = vx[k];
+            }
+            if (((n + 2) & 3) == wave) {
+                place(n + 2, page);
+                page = page_at(n + 6);
             }
             __syncthreads();
-            if (t0 + T < end) {
-                fetch(t0 + T);
-                pages_at(t0 + 2 * T);
-            }
+            if (n + 1 < tile_end) fetch(n + 1);
             if (wave * 32 >= rows) continue;
             f32x4 x[2][ST];
 #pragma unroll
@@ -291,21 +319,19 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 x[0][s] = x[1][s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    const u32x4 y = s_k[buf][spot(s * 16 + c16, j * 4 + g)];
+                    const u32x4 y = now_k[k_at[j] + s * 16 * PR];
                     x[0][s] = mfma<BF16>(y, q[0][j], x[0][s]);
                     x[1][s] = mfma<BF16>(y, q[1][j], x[1][s]);
                 }
             }
-            uint32_t valid = 0x01010101u;
-#pragma unroll
-            for (int s = 0; s < ST; ++s) valid &= *(const uint32_t *)&s_ok[buf][s * 16 + g * 4];
-            const bool some = __any(valid != 0x01010101u);
-            if (some) {
+            const uint64_t valid = valid_of(n);
+            if (~valid << (64 - T)) {       // the last tile's end, or a page number outside the pool
+                const uint64_t mine = valid >> (g * 4);
 #pragma unroll
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (!s_ok[buf][s * 16 + g * 4 + i]) x[0][s][i] = x[1][s][i] = -INFINITY;
+                        if (!(mine >> (s * 16 + i) & 1)) x[0][s][i] = x[1][s][i] = -INFINITY;
             }
             u32x4 p[2][ST / 2];
 #pragma unroll
@@ -315,26 +341,23 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][s][i]);
-                // (a scale of 0 makes no number of the -inf of a tile without tokens: fmaxf leaves that out)
-                const float m_new = fmaxf(m[t], row_reduce<true>(top) * a.scale2 - kLift);
-                const float use = m_new == -INFINITY ? 0.f : m_new;
-                if (__any(m_new > m[t])) {
-                    const float r = __builtin_amdgcn_exp2f(m[t] - use);
+                top = row_reduce<true>(top) * a.scale2 - kLift;
+                // The sums are rescaled only where weights would pass 2^(kLift + kSlack):
+                // rarely, after a run's first tiles.
+                if (__any(top > m[t] + kSlack)) {
+                    const float m_new = fmaxf(m[t], top), r = __builtin_amdgcn_exp2f(m[t] - (m_new == -INFINITY ? 0.f : m_new));
                     l[t] *= r;
 #pragma unroll
                     for (int j = 0; j < VC; ++j) o[t][j] *= r;
                     m[t] = m_new;
                 }
+                const float use = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
-                        float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], a.scale2, -use));
-                        float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], a.scale2, -use));
-                        if (some) {
-                            if (!s_ok[buf][s * 16 + g * 4 + i]) p0 = 0.f;
-                            if (!s_ok[buf][s * 16 + g * 4 + i + 1]) p1 = 0.f;
-                        }
+                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], a.scale2, -use));
+                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], a.scale2, -use));
                         l[t] += p0 + p1;
                         p[t][s >> 1][(s & 1) * 2 + i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
                     }
@@ -346,7 +369,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 for (int w0 = 0; w0 < P16; ++w0) {
                     u32x4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = s_v[buf][spot(s * 32 + (i >> 2) * 16 + g * 4 + (i & 3), w0 * 16 + c16)];
+                    for (int i = 0; i < 8; ++i) v[i] = now_v[v_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR + w0 * 16];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
 #pragma unroll
@@ -363,7 +386,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                     u32x2 v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = ((const u32x2 *)&s_v[buf][spot(s * 32 + (i >> 2) * 16 + g * 4 + (i & 3), P16 * 16 + (c16 >> 1))])[c16 & 1];
+                        v[i] = ((const u32x2 *)now_v)[v8_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR * 2];
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -583,7 +606,9 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     a.members = P.members;
     a.parts = P.parts;
     a.rows = P.rows;
+    // a scale of 0 makes no order of logits: every sequence on its own
     a.scale2 = (Q.scale < 0 ? -Q.scale : Q.scale) * kLog2e;
+    if (a.scale2 == 0.f) a.groups = 0;
     a.negate = Q.scale < 0 ? 0x80008000u : 0;
     a.runs = P.runs;
     a.by_runs = make_div(P.runs);

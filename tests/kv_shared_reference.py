@@ -70,11 +70,11 @@ def attend(m, scale=None, hidden=()):
                 ep = 2 * ex + 4 * F32 + 2 * sums
                 lse_tol[h] = ex + 4 * F32 + sums + 2 * F32 * lse[h].abs()
                 # The weights of tokens in common are rounded to the type, half a step each; in fp16, where they are
-                # held times 2^15, no weight is held below the step 2^-24, which adds 2^-39 of the largest (at most 1).
+                # held times 2^11, no weight is held below the step 2^-24, which adds 2^-35 of the largest (at most 1).
                 mix = p @ v[:, j].abs()
                 rounded = unit * (p * before) @ v[:, j].abs()
                 if m.dtype is torch.float16:
-                    rounded = rounded + 2.0 ** -39 * v[before, j].abs().sum(0)
+                    rounded = rounded + 2.0 ** -35 * v[before, j].abs().sum(0)
                 out_tol[h] = unit * out[h].abs() + ((ep + WEIGHT[m.dtype]) * mix + rounded) * (1 + unit) ** 2
                 out_tol[h] += torch.finfo(m.dtype).smallest_normal * torch.finfo(m.dtype).eps
         res.append((out, out_tol, lse, lse_tol))
