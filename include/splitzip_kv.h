@@ -216,7 +216,7 @@ typedef struct splitzip_kv_groups {
 size_t splitzip_kv_groups_struct_size(void);
 
 /* As splitzip_kv_attend_workspace_size, for splitzip_kv_attend_shared with up
- * to `groups` groups (0 and 1: the same as more). */
+ * to `groups` groups. */
 size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t groups);
 
 /* What splitzip_kv_attend computes (window ALL, no mass), where K and V of the

@@ -78,9 +78,6 @@ struct AttendArgs {
     uint64_t ms[2], mos[2];
     uint32_t mass_len;
     int32_t *status;
-    // the rest of sequences whose first tokens were attended with others' (REST):
-    const uint32_t *from;         // [batch] the first token of the rest
-    float *whole_o, *whole_ml;    // [batch][heads] of [dim] and [2]: a KV head that was one run's
 };
 
 struct Seen {
@@ -101,23 +98,15 @@ __device__ inline uint32_t units_of(uint32_t n, uint32_t window, uint32_t sinks)
 // The sequences in blocks of 64, one a lane: lengths and running sums of units.
 struct Block64 {
     uint32_t first, len, before, upto;     // first sequence; the lane's length, units before and with it
-    uint32_t from;                         // the lane's first token (REST)
     uint32_t total;                        // units with the block's last
 };
 
-// What is left of a sequence of length n behind its first `from` tokens.
-__device__ inline uint32_t rest_units(uint32_t n, uint32_t from) {
-    return n > from ? (n - from - 1) / kUnit + 1 : 1;
-}
-
-template <bool REST>
 __device__ inline void load_block(const AttendArgs &a, uint32_t first, uint32_t carry, Block64 &k,
                                   int32_t *status) {
     const uint32_t lane = threadIdx.x & 63, b = first + lane;
     k.first = first;
     k.len = b < a.c.batch ? seq_len(a.c, b, status) : 0;
-    k.from = REST && b < a.c.batch ? a.from[b] : 0;
-    const uint32_t units = b >= a.c.batch ? 0 : REST ? rest_units(k.len, k.from) : units_of(k.len, a.window, a.sinks);
+    const uint32_t units = b < a.c.batch ? units_of(k.len, a.window, a.sinks) : 0;
     const uint32_t sum = wave_scan(units);
     k.before = carry + sum - units;
     k.upto = carry + sum;
@@ -202,23 +191,37 @@ __device__ inline float row_reduce(float x) {
     return MAX ? fmaxf(z0, z1) : z0 + z1;
 }
 
-// DP: head_dim rounded up to a multiple of 64.  NT: blocks of 16 query rows a
-// workgroup takes.  EXACT: head_dim is DP.  (Bounded to 168 registers, for a
-// third workgroup on a compute unit, dim 128 spills: 30 us become 36.)
-// REST: of every sequence the tokens behind the first from[b]; all outputs are
-// shares.
-template <bool BF16, int DP, int NT, bool EXACT, bool REST = false>
-__global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
+// What attend_tokens keeps in LDS.  The query rows stay in registers, or here
+// where those would spill.
+template <int DP, int NT>
+struct AttendLds {
+    static constexpr bool kQueries = NT * (DP / 32) >= 12;
+    static constexpr int LQ = DP + 8;
+    __align__(16) uint16_t q[kQueries ? NT * 16 * LQ : 8];
+    uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
+    __align__(16) float o[kWaves][16][DP + 4];
+    float m[kWaves][NT * 16], l[kWaves][NT * 16], top[16], sum[16];
+};
+
+// A workgroup's work on one KV head's tokens for up to 16 NT query rows: the
+// visible numbers from unit0 * kUnit to v_end of the table row.
+//   query_at(row)                address of a query row
+//   meanwhile()                  called while the first K and V are on their way
+//   logits(row, v, x[4])         (keep_logits) logits in base 2 of four visible numbers from v on
+//   emit(row, d, o[4], m, l)     four columns from d on of the sum of 2^(x - m) v, not divided by l
+// DP: head_dim rounded up to a multiple of 64.  NT: blocks of 16 query rows.
+// EXACT: head_dim is DP.
+template <bool BF16, int DP, int NT, bool EXACT, typename Query, typename Meanwhile, typename Logits, typename Emit>
+__device__ __forceinline__ void attend_tokens(AttendLds<DP, NT> &lds, const Cache &c, uint32_t h, const int32_t *table, const Seen &seen,
+                                              uint32_t unit0, uint32_t v_end, uint32_t rows, float scale2, int32_t *status,
+                                              Query query_at, Meanwhile meanwhile, bool keep_logits, Logits logits, Emit emit) {
     constexpr int KS = DP / 32;             // steps of the K product
     constexpr int P16 = DP / 128;           // 16-byte pieces of a V row a lane takes: columns 128 i + 8 (lane % 16)
     constexpr int P8 = (DP % 128) / 64;     // and an 8-byte one: 128 P16 + 4 (lane % 16)
     constexpr int VW = 4 * P16 + 2 * P8;    // words of them
     constexpr int VC = 2 * VW;              // columns
-    constexpr int LD = DP + 4;
-    // The query rows stay in registers, or in LDS where those would spill.
-    constexpr bool QLDS = NT * KS >= 12;
-    constexpr int LQ = DP + 8;
-    __shared__ __align__(16) uint16_t s_q[QLDS ? NT * 16 * LQ : 8];
+    constexpr bool QLDS = AttendLds<DP, NT>::kQueries;
+    constexpr int LQ = AttendLds<DP, NT>::LQ;
     // fp16 weights are held times 2^15: their smallest normal step then lies 2^-29
     // below the largest weight instead of 2^-14.
     constexpr float kLift = BF16 ? 0.f : 15.f;
@@ -228,12 +231,310 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
     // the type's smallest step is p, or that step, or 0; the second part then
     // takes the step away again.
     auto at_least = [](float p) { return BF16 ? p : __builtin_amdgcn_fmed3f(p, p * 0x1p102f, 0x1p-24f); };
-    __shared__ uint64_t off_k[kWaves][2][kTile], off_v[kWaves][2][kTile];
-    __shared__ float s_o[kWaves][16][LD];
-    __shared__ float s_m[kWaves][NT * 16], s_l[kWaves][NT * 16], s_top[16], s_sum[16];
-    uint32_t *s_block = (uint32_t *)s_o;      // while the run is looked up, before any output
-    static_assert(sizeof s_o >= 4 * kMaxBlocks, "sums of all blocks");
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t D = EXACT ? DP : c.dim;
+
+    u32x4 q[QLDS ? 1 : NT][QLDS ? 1 : KS];
+    constexpr int kStage = QLDS ? NT * 16 * (DP / 8) / kAttendThreads : 1;
+    u32x4 stage[kStage];
+    if constexpr (QLDS) {
+#pragma unroll
+        for (int k = 0; k < kStage; ++k) {
+            const uint32_t i = tid + k * kAttendThreads, row = i / (DP / 8), d = i % (DP / 8) * 8;
+            stage[k] = u32x4{0, 0, 0, 0};
+            if (row < rows && (EXACT || d < D)) stage[k] = *(const u32x4 *)(query_at(row) + d);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                q[t][j] = u32x4{0, 0, 0, 0};
+                const uint32_t d = j * 32 + g * 8;
+                if (t * 16 + c16 < rows && (EXACT || d < D)) q[t][j] = *(const u32x4 *)(query_at(t * 16 + c16) + d);
+            }
+    }
+    auto query = [&](int t, int j) {
+        if constexpr (QLDS) return *(const u32x4 *)&lds.q[(t * 16 + c16) * LQ + j * 32 + g * 8];
+        else return q[t][j];
+    };
+    f32x4 o[NT][VC];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t] = -INFINITY;
+        l[t] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VC; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // Bases of this lane's pieces; columns behind head_dim (EXACT false)
+    // are read from column 0 and stay unused.
+    const uint16_t *k_lane[EXACT ? 1 : KS], *v_lane[P16 + P8];
+    const uint16_t *k_head = c.k + h * c.ks[1], *v_head = c.v + h * c.vs[1];
+#pragma unroll
+    for (int j = 0; j < (EXACT ? 1 : KS); ++j) {
+        const uint32_t d = j * 32 + g * 8;
+        k_lane[j] = k_head + (EXACT || d < D ? d : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < P16 + P8; ++i) {
+        const uint32_t d = i < P16 ? i * 128 + c16 * 8 : P16 * 128 + c16 * 4;
+        v_lane[i] = v_head + (EXACT || d < D ? d : 0);
+    }
+
+    // The page number of lane t's token of the wave's tile at v0 (lanes
+    // 32.. repeat 0..31), and from it the places of K and V.
+    auto token = [&](uint32_t v) { return v < seen.sinks ? v : v + seen.shift; };
+    auto page_of = [&](uint32_t v0) {
+        const uint32_t v = v0 + (lane & 31);
+        return v < v_end ? (uint32_t)table[div(token(v), c.page)] : 0xffffffffu;
+    };
+    auto place = [&](uint32_t v0, uint32_t page, int buf) {
+        const uint32_t v = v0 + (lane & 31), t = token(v);
+        const bool in = v < v_end, ok = in && page < c.num_pages;
+        if (in && !ok) report(status, SPLITZIP_KV_BAD_PAGE);
+        const uint32_t p = ok ? page : 0, slot = ok ? t - div(t, c.page) * c.page.d : 0;
+        if (lane < 32) {
+            lds.off_k[wave][buf][lane] = p * c.ks[0] + slot * c.ks[2];
+            lds.off_v[wave][buf][lane] = p * c.vs[0] + slot * c.vs[2];
+        }
+        __builtin_amdgcn_wave_barrier();      // the wave's own LDS: in order without a wait
+        return (uint32_t)__ballot(ok);
+    };
+    // Rows of whole cache lines pass the caches by (32 sequences of 32768 tokens
+    // 642 us, through them 722); others share lines with their neighbours and
+    // go through them (dim 80, 16 x 8192 tokens: 70 us, past them 88).
+    auto load_kv = [](const uint16_t *p) { return EXACT ? load_once(p) : *(const u32x4 *)p; };
+    auto load_kv8 = [](const uint16_t *p) {
+        return EXACT ? __builtin_nontemporal_load((const u32x2 *)p) : *(const u32x2 *)p;
+    };
+    u32x4 kr[2][KS];
+    u32x4 v16[8][P16 ? P16 : 1];
+    u32x2 v8[8];
+    auto word = [&](int i, int w) { return w < 4 * P16 ? v16[i][w / 4][w % 4] : v8[i][w - 4 * P16]; };
+    auto load_k = [&](int buf) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint64_t off = lds.off_k[wave][buf][s * 16 + c16];
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+                kr[s][j] = load_kv(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
+        }
+    };
+    auto load_v = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t off = lds.off_v[wave][buf][(i >> 2) * 16 + g * 4 + (i & 3)];
+#pragma unroll
+            for (int p = 0; p < P16; ++p) v16[i][p] = load_kv(v_lane[p] + off);
+            if constexpr (P8 > 0) v8[i] = load_kv8(v_lane[P16] + off);
+        }
+    };
+
+    uint32_t v0 = unit0 * kUnit + wave * kTile;
+    uint32_t page = 0xffffffffu, valid = 0, valid_next = 0;
+    int buf = 0;
+    if (v0 < v_end) {
+        page = page_of(v0);
+        valid = place(v0, page, 0);
+        load_k(0);
+        load_v(0);
+        page = page_of(v0 + kUnit);
+    }
+    if constexpr (QLDS) {      // K and V are on their way; the row tile before has been read (its last barriers)
+#pragma unroll
+        for (int k = 0; k < kStage; ++k) {
+            const uint32_t i = tid + k * kAttendThreads;
+            *(u32x4 *)&lds.q[i / (DP / 8) * LQ + i % (DP / 8) * 8] = stage[k];
+        }
+        __syncthreads();
+    }
+    meanwhile();
+    for (; v0 < v_end; v0 += kUnit) {
+        const bool more = v0 + kUnit < v_end;
+        if (more) {
+            valid_next = place(v0 + kUnit, page, buf ^ 1);
+            page = page_of(v0 + 2 * kUnit);
+        }
+        if (!EXACT) {
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+                if (j * 32 + g * 8 >= D) kr[0][j] = kr[1][j] = u32x4{0, 0, 0, 0};
+        }
+        f32x4 x[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            x[t][0] = x[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                const u32x4 y = query(t, j);
+                x[t][0] = mfma<BF16>(kr[0][j], y, x[t][0]);
+                x[t][1] = mfma<BF16>(kr[1][j], y, x[t][1]);
+            }
+        }
+        if (more) load_k(buf ^ 1);
+
+        u32x4 hi[NT], lo[NT], rest[BF16 ? NT : 1];
+        const uint32_t mine = (valid >> (g * 4) & 15u) | (valid >> (16 + g * 4) & 15u) << 4;     // of its 8 tokens
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float y[8], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = x[t][i >> 2][i & 3] * scale2;
+                if (valid != 0xffffffffu && !(mine >> i & 1)) y[i] = -INFINITY;
+                top = fmaxf(top, y[i]);
+            }
+            if (keep_logits && t * 16 + c16 < rows) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    logits(t * 16 + c16, v0 + s * 16 + g * 4, f32x4{y[4 * s], y[4 * s + 1], y[4 * s + 2], y[4 * s + 3]});
+            }
+            const float m_new = fmaxf(m[t], row_reduce<true>(top) - kLift);
+            const float use = m_new == -INFINITY ? 0.f : m_new;
+            if (__any(m_new > m[t])) {
+                const float r = __builtin_amdgcn_exp2f(m[t] - use);
+                l[t] *= r;
+#pragma unroll
+                for (int j = 0; j < VC; ++j) o[t][j] *= r;
+                m[t] = m_new;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                // The weight as a sum of 16-bit numbers, as many as hold the
+                // bits that 32 have: three of 8 in bf16, two of 11 in fp16.
+                // One alone would add an error as large as the output's own
+                // rounding, two in bf16 one of 2^-16, which moved 0.1 % of the
+                // outputs by a step.  The further products are hidden behind
+                // the loads (second 0 to 3 %, third 0 to 1; with 32 and 64
+                // rows a KV head 62.3 us become 65.4 and 79.8 85.1).
+                const float p0 = __builtin_amdgcn_exp2f(y[i] - use), p1 = __builtin_amdgcn_exp2f(y[i + 1] - use);
+                l[t] += p0 + p1;
+                float r0, r1;
+                hi[t][i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
+                unpack2<BF16>(hi[t][i / 2], r0, r1);
+                lo[t][i / 2] = pack2<BF16>(p0 - r0, p1 - r1);
+                if constexpr (BF16) {
+                    float s0, s1;
+                    unpack2<BF16>(lo[t][i / 2], s0, s1);
+                    rest[t][i / 2] = pack2<BF16>(p0 - r0 - s0, p1 - r1 - s1);
+                }
+            }
+        }
+        if (valid != 0xffffffffu) {
+            // weight 0 does not silence an infinity or a NaN
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(mine >> i & 1)) {
+#pragma unroll
+                    for (int p = 0; p < P16; ++p) v16[i][p] = u32x4{0, 0, 0, 0};
+                    if constexpr (P8 > 0) v8[i] = u32x2{0, 0};
+                }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+                // An infinity in V counts once, with the first part: times
+                // another that is 0 or negative it would make a NaN.
+                u32x4 col, fin;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    col[i] = __builtin_amdgcn_perm(word(2 * i + 1, w), word(2 * i, w), odd ? 0x07060302u : 0x05040100u);
+                    fin[i] = finite2<BF16>(col[i]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    o[t][2 * w + odd] = mfma<BF16>(col, hi[t], o[t][2 * w + odd]);
+                    o[t][2 * w + odd] = mfma<BF16>(fin, lo[t], o[t][2 * w + odd]);
+                    if constexpr (BF16) o[t][2 * w + odd] = mfma<BF16>(fin, rest[t], o[t][2 * w + odd]);
+                }
+            }
+        if (more) load_v(buf ^ 1);
+        buf ^= 1;
+        valid = valid_next;
+    }
+
+    // The waves' shares joined: common maximum, rescaled sums.
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        l[t] = row_reduce<false>(l[t]);
+        if (lane < 16) {
+            lds.m[wave][t * 16 + lane] = m[t];
+            lds.l[wave][t * 16 + lane] = l[t];
+        }
+    }
+    __syncthreads();
+    for (int t = 0; t < NT && t * 16 < (int)rows; ++t) {
+        // a lane's row c16: the waves' maximum and sum
+        float M = -INFINITY, L = 0.f, mw[kWaves], lw[kWaves];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            mw[w] = lds.m[w][t * 16 + c16];
+            lw[w] = lds.l[w][t * 16 + c16];
+            M = fmaxf(M, mw[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) L += mw[w] == -INFINITY ? lw[w] : lw[w] * __builtin_amdgcn_exp2f(mw[w] - M);
+        if (tid < 16) {
+            lds.top[tid] = M;
+            lds.sum[tid] = L;
+        }
+        // o[t] is indexed by a constant: one of the NT blocks is taken
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt)
+            if (tt == t) {
+                const float r = m[tt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[tt] - M);
+#pragma unroll
+                for (int p = 0; p < P16 + P8; ++p) {
+                    const int wide = p < P16 ? 8 : 4;      // columns of the piece
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < wide; j += 4) {
+                            const int at_col = p * 8 + j;
+                            f32x4 y;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = o[tt][at_col + e][i] * r;
+                            *(f32x4 *)&lds.o[wave][c16][p * 128 + (g * 4 + i) * wide + j] = y;
+                        }
+                }
+            }
+        __syncthreads();
+        constexpr int kItems = 16 * (DP / 4) / kAttendThreads;
+        f32x4 y[kItems];
+        float top[kItems], sum[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
+            top[k] = lds.top[row];
+            sum[k] = lds.sum[row];
+            y[k] = *(const f32x4 *)&lds.o[0][row][d];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) y[k] += *(const f32x4 *)&lds.o[w][row][d];
+        }
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
+            const uint32_t gr = t * 16 + row;
+            if (gr >= rows || d >= D) continue;
+            emit(gr, d, y[k], top[k], sum[k]);
+        }
+        __syncthreads();
+    }
+}
+
+// (Bounded to 168 registers, for a third workgroup on a compute unit, dim 128
+// spills: 30 us become 36.)
+template <bool BF16, int DP, int NT, bool EXACT>
+__global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
+    __shared__ AttendLds<DP, NT> lds;
+    uint32_t *s_block = (uint32_t *)lds.o;      // while the run is looked up, before any output
+    static_assert(sizeof lds.o >= 4 * kMaxBlocks, "sums of all blocks");
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim;
     const uint32_t pairs = a.c.kv_heads * a.row_tiles;     // of a sequence
@@ -247,7 +548,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
         const uint32_t blocks = (a.c.batch + 63) / 64;
         uint32_t total = 0;
         if (blocks == 1) {
-            load_block<REST>(a, 0, 0, blk, status0);
+            load_block(a, 0, 0, blk, status0);
             total = blk.total;
         } else {
             // Every wave sums some blocks, then all of them look at the sums
@@ -255,8 +556,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             // where every wave and every join read all of the lengths).
             for (uint32_t i = wave; i < blocks; i += kWaves) {
                 const uint32_t b = i * 64 + lane;
-                const uint32_t sum = wave_scan(b >= a.c.batch ? 0 : REST ? rest_units(seq_len(a.c, b, status0), a.from[b])
-                                                                     : units_of(seq_len(a.c, b, status0), a.window, a.sinks));
+                const uint32_t sum = wave_scan(b < a.c.batch ? units_of(seq_len(a.c, b, status0), a.window, a.sinks) : 0);
                 if (lane == 63) s_block[i] = sum;
             }
             __syncthreads();
@@ -280,22 +580,21 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
                 }
                 carry = __builtin_amdgcn_readlane(upto, 63);
             }
-            load_block<REST>(a, first, carry, blk, nullptr);
+            load_block(a, first, carry, blk, nullptr);
         }
         const uint64_t past = __ballot(blk.upto * pairs > u_begin);
         at = past ? (uint32_t)__builtin_ctzll(past) : 64;      // the sequence's lane
     }
 
     for (uint32_t u = u_begin; u < u_end;) {
-        uint32_t b, n, units, pair, unit0 = 0, count, from = 0;
+        uint32_t b, n, units, pair, unit0 = 0, count;
         if (a.runs) {
             while (at >= 64) {
-                load_block<REST>(a, blk.first + 64, blk.total, blk, nullptr);
+                load_block(a, blk.first + 64, blk.total, blk, nullptr);
                 at -= 64;
             }
             b = blk.first + at;
             n = __builtin_amdgcn_readlane(blk.len, at);
-            if (REST) from = __builtin_amdgcn_readlane(blk.from, at);
             const uint32_t before = __builtin_amdgcn_readlane(blk.before, at), rel = u - before * pairs;
             units = __builtin_amdgcn_readlane(blk.upto, at) - before;
             pair = rel / units;
@@ -306,330 +605,45 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
             b = div(blockIdx.x, a.by_pairs);
             pair = blockIdx.x - b * pairs;
             n = __builtin_amdgcn_readfirstlane(seq_len(a.c, b, pair == 0 && wave == 0 ? a.status : nullptr));
-            if (REST) from = __builtin_amdgcn_readfirstlane(a.from[b]);
-            count = units = REST ? rest_units(n, from) : units_of(n, a.window, a.sinks);
+            count = units = units_of(n, a.window, a.sinks);
         }
         const bool whole = count == units;
         const uint32_t h = div(pair, a.by_row_tiles), row0 = (pair - h * a.row_tiles) * a.rows;     // rows of the group
         const uint32_t rows = min(a.rows, a.group - row0), head0 = h * a.group + row0;
-        const Seen seen = REST ? Seen{0, from, n > from ? n - from : 0} : seen_of(n, a.window, a.sinks);
+        const Seen seen = seen_of(n, a.window, a.sinks);
         const uint32_t v_end = min(seen.count, (unit0 + count) * kUnit);
         const int32_t *table = a.c.table + b * a.c.table_stride;
 
-        u32x4 q[QLDS ? 1 : NT][QLDS ? 1 : KS];
-        constexpr int kStage = QLDS ? NT * 16 * (DP / 8) / kAttendThreads : 1;
-        u32x4 stage[kStage];
-        if constexpr (QLDS) {
-#pragma unroll
-            for (int k = 0; k < kStage; ++k) {
-                const uint32_t i = tid + k * kAttendThreads, row = i / (DP / 8), d = i % (DP / 8) * 8;
-                stage[k] = u32x4{0, 0, 0, 0};
-                if (row < rows && (EXACT || d < D)) stage[k] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + row) * a.qs[1] + d);
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    q[t][j] = u32x4{0, 0, 0, 0};
-                    const uint32_t d = j * 32 + g * 8;
-                    if (t * 16 + c16 < rows && (EXACT || d < D))
-                        q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + (head0 + t * 16 + c16) * a.qs[1] + d);
-                }
-        }
-        auto query = [&](int t, int j) {
-            if constexpr (QLDS) return *(const u32x4 *)&s_q[(t * 16 + c16) * LQ + j * 32 + g * 8];
-            else return q[t][j];
-        };
-        f32x4 o[NT][VC];
-        float m[NT], l[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            m[t] = -INFINITY;
-            l[t] = 0.f;
-#pragma unroll
-            for (int j = 0; j < VC; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-
-        // Bases of this lane's pieces; columns behind head_dim (EXACT false)
-        // are read from column 0 and stay unused.
-        const uint16_t *k_lane[EXACT ? 1 : KS], *v_lane[P16 + P8];
-        const uint16_t *k_head = a.c.k + h * a.c.ks[1], *v_head = a.c.v + h * a.c.vs[1];
-#pragma unroll
-        for (int j = 0; j < (EXACT ? 1 : KS); ++j) {
-            const uint32_t d = j * 32 + g * 8;
-            k_lane[j] = k_head + (EXACT || d < D ? d : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < P16 + P8; ++i) {
-            const uint32_t d = i < P16 ? i * 128 + c16 * 8 : P16 * 128 + c16 * 4;
-            v_lane[i] = v_head + (EXACT || d < D ? d : 0);
-        }
-
-        // The page number of lane t's token of the wave's tile at v0 (lanes
-        // 32.. repeat 0..31), and from it the places of K and V.
-        auto token = [&](uint32_t v) { return v < seen.sinks ? v : v + seen.shift; };
-        auto page_of = [&](uint32_t v0) {
-            const uint32_t v = v0 + (lane & 31);
-            return v < v_end ? (uint32_t)table[div(token(v), a.c.page)] : 0xffffffffu;
-        };
-        auto place = [&](uint32_t v0, uint32_t page, int buf) {
-            const uint32_t v = v0 + (lane & 31), t = token(v);
-            const bool in = v < v_end, ok = in && page < a.c.num_pages;
-            if (in && !ok) report(a.status, SPLITZIP_KV_BAD_PAGE);
-            const uint32_t p = ok ? page : 0, slot = ok ? t - div(t, a.c.page) * a.c.page.d : 0;
-            if (lane < 32) {
-                off_k[wave][buf][lane] = p * a.c.ks[0] + slot * a.c.ks[2];
-                off_v[wave][buf][lane] = p * a.c.vs[0] + slot * a.c.vs[2];
-            }
-            __builtin_amdgcn_wave_barrier();      // the wave's own LDS: in order without a wait
-            return (uint32_t)__ballot(ok);
-        };
-        // Rows of whole cache lines pass the caches by (32 sequences of 32768 tokens
-        // 642 us, through them 722); others share lines with their neighbours and
-        // go through them (dim 80, 16 x 8192 tokens: 70 us, past them 88).
-        auto load_kv = [](const uint16_t *p) { return EXACT ? load_once(p) : *(const u32x4 *)p; };
-        auto load_kv8 = [](const uint16_t *p) {
-            return EXACT ? __builtin_nontemporal_load((const u32x2 *)p) : *(const u32x2 *)p;
-        };
-        u32x4 kr[2][KS];
-        u32x4 v16[8][P16 ? P16 : 1];
-        u32x2 v8[8];
-        auto word = [&](int i, int w) { return w < 4 * P16 ? v16[i][w / 4][w % 4] : v8[i][w - 4 * P16]; };
-        auto load_k = [&](int buf) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const uint64_t off = off_k[wave][buf][s * 16 + c16];
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-                    kr[s][j] = load_kv(EXACT ? k_lane[0] + off + j * 32 : k_lane[j] + off);
-            }
-        };
-        auto load_v = [&](int buf) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t off = off_v[wave][buf][(i >> 2) * 16 + g * 4 + (i & 3)];
-#pragma unroll
-                for (int p = 0; p < P16; ++p) v16[i][p] = load_kv(v_lane[p] + off);
-                if constexpr (P8 > 0) v8[i] = load_kv8(v_lane[P16] + off);
-            }
-        };
-
-        uint32_t v0 = unit0 * kUnit + wave * kTile;
-        uint32_t page = 0xffffffffu, valid = 0, valid_next = 0;
-        int buf = 0;
-        if (v0 < v_end) {
-            page = page_of(v0);
-            valid = place(v0, page, 0);
-            load_k(0);
-            load_v(0);
-            page = page_of(v0 + kUnit);
-        }
-        if constexpr (QLDS) {      // K and V are on their way; the row tile before has been read (its last barriers)
-#pragma unroll
-            for (int k = 0; k < kStage; ++k) {
-                const uint32_t i = tid + k * kAttendThreads;
-                *(u32x4 *)&s_q[i / (DP / 8) * LQ + i % (DP / 8) * 8] = stage[k];
-            }
-            __syncthreads();
-        }
-        if (a.runs && unit0 == 0 && tid == 0) {      // here its divisions are waited for by nothing
-            const uint32_t shares = whole ? 1 : cut.owner(u + units - 1) - blockIdx.x + 1;
-            ((u32x2 *)a.splits)[(uint64_t)b * pairs + pair] = u32x2{blockIdx.x, shares * 2 + (u != u_begin)};
-        }
-        for (; v0 < v_end; v0 += kUnit) {
-            const bool more = v0 + kUnit < v_end;
-            if (more) {
-                valid_next = place(v0 + kUnit, page, buf ^ 1);
-                page = page_of(v0 + 2 * kUnit);
-            }
-            if (!EXACT) {
-#pragma unroll
-                for (int j = 0; j < KS; ++j)
-                    if (j * 32 + g * 8 >= D) kr[0][j] = kr[1][j] = u32x4{0, 0, 0, 0};
-            }
-            f32x4 x[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                x[t][0] = x[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    const u32x4 y = query(t, j);
-                    x[t][0] = mfma<BF16>(kr[0][j], y, x[t][0]);
-                    x[t][1] = mfma<BF16>(kr[1][j], y, x[t][1]);
-                }
-            }
-            if (more) load_k(buf ^ 1);
-
-            u32x4 hi[NT], lo[NT], rest[BF16 ? NT : 1];
-            const uint32_t mine = (valid >> (g * 4) & 15u) | (valid >> (16 + g * 4) & 15u) << 4;     // of its 8 tokens
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float y[8], top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = x[t][i >> 2][i & 3] * a.scale2;
-                    if (valid != 0xffffffffu && !(mine >> i & 1)) y[i] = -INFINITY;
-                    top = fmaxf(top, y[i]);
-                }
-                if (a.logits && t * 16 + c16 < rows) {
-                    float *to = a.logits + (b * (uint64_t)a.heads + head0 + t * 16 + c16) * a.logit_stride;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint32_t v = v0 + s * 16 + g * 4;
-                        if (v < a.logit_len) *(f32x4 *)(to + v) = f32x4{y[4 * s], y[4 * s + 1], y[4 * s + 2], y[4 * s + 3]};
-                    }
-                }
-                const float m_new = fmaxf(m[t], row_reduce<true>(top) - kLift);
-                const float use = m_new == -INFINITY ? 0.f : m_new;
-                if (__any(m_new > m[t])) {
-                    const float r = __builtin_amdgcn_exp2f(m[t] - use);
-                    l[t] *= r;
-#pragma unroll
-                    for (int j = 0; j < VC; ++j) o[t][j] *= r;
-                    m[t] = m_new;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    // The weight as a sum of 16-bit numbers, as many as hold the
-                    // bits that 32 have: three of 8 in bf16, two of 11 in fp16.
-                    // One alone would add an error as large as the output's own
-                    // rounding, two in bf16 one of 2^-16, which moved 0.1 % of the
-                    // outputs by a step.  The further products are hidden behind
-                    // the loads (second 0 to 3 %, third 0 to 1; with 32 and 64
-                    // rows a KV head 62.3 us become 65.4 and 79.8 85.1).
-                    const float p0 = __builtin_amdgcn_exp2f(y[i] - use), p1 = __builtin_amdgcn_exp2f(y[i + 1] - use);
-                    l[t] += p0 + p1;
-                    float r0, r1;
-                    hi[t][i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
-                    unpack2<BF16>(hi[t][i / 2], r0, r1);
-                    lo[t][i / 2] = pack2<BF16>(p0 - r0, p1 - r1);
-                    if constexpr (BF16) {
-                        float s0, s1;
-                        unpack2<BF16>(lo[t][i / 2], s0, s1);
-                        rest[t][i / 2] = pack2<BF16>(p0 - r0 - s0, p1 - r1 - s1);
-                    }
-                }
-            }
-            if (valid != 0xffffffffu) {
-                // weight 0 does not silence an infinity or a NaN
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!(mine >> i & 1)) {
-#pragma unroll
-                        for (int p = 0; p < P16; ++p) v16[i][p] = u32x4{0, 0, 0, 0};
-                        if constexpr (P8 > 0) v8[i] = u32x2{0, 0};
-                    }
-            }
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-#pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    // An infinity in V counts once, with the first part: times
-                    // another that is 0 or negative it would make a NaN.
-                    u32x4 col, fin;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        col[i] = __builtin_amdgcn_perm(word(2 * i + 1, w), word(2 * i, w), odd ? 0x07060302u : 0x05040100u);
-                        fin[i] = finite2<BF16>(col[i]);
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        o[t][2 * w + odd] = mfma<BF16>(col, hi[t], o[t][2 * w + odd]);
-                        o[t][2 * w + odd] = mfma<BF16>(fin, lo[t], o[t][2 * w + odd]);
-                        if constexpr (BF16) o[t][2 * w + odd] = mfma<BF16>(fin, rest[t], o[t][2 * w + odd]);
-                    }
-                }
-            if (more) load_v(buf ^ 1);
-            buf ^= 1;
-            valid = valid_next;
-        }
-
-        // The waves' shares joined: common maximum, rescaled sums.
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            l[t] = row_reduce<false>(l[t]);
-            if (lane < 16) {
-                s_m[wave][t * 16 + lane] = m[t];
-                s_l[wave][t * 16 + lane] = l[t];
-            }
-        }
-        __syncthreads();
         const uint32_t slot = blockIdx.x * 2 + (u != u_begin);
-        for (int t = 0; t < NT && t * 16 < (int)rows; ++t) {
-            // a lane's row c16: the waves' maximum and sum
-            float M = -INFINITY, L = 0.f, mw[kWaves], lw[kWaves];
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                mw[w] = s_m[w][t * 16 + c16];
-                lw[w] = s_l[w][t * 16 + c16];
-                M = fmaxf(M, mw[w]);
-            }
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) L += mw[w] == -INFINITY ? lw[w] : lw[w] * __builtin_amdgcn_exp2f(mw[w] - M);
-            if (tid < 16) {
-                s_top[tid] = M;
-                s_sum[tid] = L;
-            }
-            // o[t] is indexed by a constant: one of the NT blocks is taken
-#pragma unroll
-            for (int tt = 0; tt < NT; ++tt)
-                if (tt == t) {
-                    const float r = m[tt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[tt] - M);
-#pragma unroll
-                    for (int p = 0; p < P16 + P8; ++p) {
-                        const int wide = p < P16 ? 8 : 4;      // columns of the piece
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < wide; j += 4) {
-                                const int at_col = p * 8 + j;
-                                f32x4 y;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) y[e] = o[tt][at_col + e][i] * r;
-                                *(f32x4 *)&s_o[wave][c16][p * 128 + (g * 4 + i) * wide + j] = y;
-                            }
-                    }
+        attend_tokens<BF16, DP, NT, EXACT>(
+            lds, a.c, h, table, seen, unit0, v_end, rows, a.scale2, a.status,
+            [&](uint32_t row) { return a.q + b * a.qs[0] + (head0 + row) * a.qs[1]; },
+            [&] {
+                if (a.runs && unit0 == 0 && tid == 0) {      // here its divisions are waited for by nothing
+                    const uint32_t shares = whole ? 1 : cut.owner(u + units - 1) - blockIdx.x + 1;
+                    ((u32x2 *)a.splits)[(uint64_t)b * pairs + pair] = u32x2{blockIdx.x, shares * 2 + (u != u_begin)};
                 }
-            __syncthreads();
-            constexpr int kItems = 16 * (DP / 4) / kAttendThreads;
-            f32x4 y[kItems];
-            float top[kItems], sum[kItems];
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
-                top[k] = s_top[row];
-                sum[k] = s_sum[row];
-                y[k] = *(const f32x4 *)&s_o[0][row][d];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w) y[k] += *(const f32x4 *)&s_o[w][row][d];
-            }
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                const uint32_t item = tid + k * kAttendThreads, row = item / (DP / 4), d = item % (DP / 4) * 4;
-                const uint32_t gr = t * 16 + row;
-                if (gr >= rows || d >= D) continue;
-                if (REST && whole) {
-                    const uint64_t at_row = b * (uint64_t)a.heads + head0 + gr;
-                    *(f32x4 *)(a.whole_o + at_row * D + d) = y[k];
-                    if (d == 0) *(f32x2 *)(a.whole_ml + at_row * 2) = f32x2{top[k], sum[k]};
-                } else if (whole) {
-                    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
-                    u32x2 z{pack2<BF16>(y[k][0] * inv, y[k][1] * inv), pack2<BF16>(y[k][2] * inv, y[k][3] * inv)};
-                    *(u32x2 *)(a.out + b * a.os[0] + (head0 + gr) * a.os[1] + d) = z;
+            },
+            a.logits != nullptr,
+            [&](uint32_t row, uint32_t v, f32x4 x) {
+                float *to = a.logits + (b * (uint64_t)a.heads + head0 + row) * a.logit_stride;
+                if (v < a.logit_len) *(f32x4 *)(to + v) = x;
+            },
+            [&](uint32_t row, uint32_t d, f32x4 y, float top, float sum) {
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
+                    *(u32x2 *)(a.out + b * a.os[0] + (head0 + row) * a.os[1] + d) = z;
                     if (d == 0) {
-                        const float e = sum[k] == 0.f ? -INFINITY : top[k] + log2f(sum[k]);
-                        if (a.lse) a.lse[b * (uint64_t)a.heads + head0 + gr] = e * kLn2;
-                        if (a.lse2) a.lse2[b * (uint64_t)a.heads + head0 + gr] = e;
+                        const float e = sum == 0.f ? -INFINITY : top + log2f(sum);
+                        if (a.lse) a.lse[b * (uint64_t)a.heads + head0 + row] = e * kLn2;
+                        if (a.lse2) a.lse2[b * (uint64_t)a.heads + head0 + row] = e;
                     }
                 } else {
-                    *(f32x4 *)(a.share_o + ((uint64_t)slot * a.rows + gr) * D + d) = y[k];
-                    if (d == 0) *(f32x2 *)(a.share_ml + ((uint64_t)slot * a.rows + gr) * 2) = f32x2{top[k], sum[k]};
+                    *(f32x4 *)(a.share_o + ((uint64_t)slot * a.rows + row) * D + d) = y;
+                    if (d == 0) *(f32x2 *)(a.share_ml + ((uint64_t)slot * a.rows + row) * 2) = f32x2{top, sum};
                 }
-            }
-            __syncthreads();
-        }
+            });
         u += a.runs ? count : 1;
         if (pair == pairs - 1 && unit0 + count == units) ++at;
     }
@@ -891,28 +905,28 @@ inline uint32_t lay_out(AttendArgs &a, const AttendPlan &P, uint64_t seen) {
     return a.runs ? a.runs : (uint32_t)tiles;
 }
 
-template <bool BF16, bool REST, int DP, int NT>
+template <bool BF16, int DP, int NT>
 void launch_attend(const AttendArgs &a, uint32_t grid, hipStream_t s) {
-    if (a.c.dim == DP) k_attend<BF16, DP, NT, true, REST><<<grid, kAttendThreads, 0, s>>>(a);
-    else k_attend<BF16, DP, NT, false, REST><<<grid, kAttendThreads, 0, s>>>(a);
+    if (a.c.dim == DP) k_attend<BF16, DP, NT, true><<<grid, kAttendThreads, 0, s>>>(a);
+    else k_attend<BF16, DP, NT, false><<<grid, kAttendThreads, 0, s>>>(a);
 }
 
-template <bool BF16, bool REST = false>
+template <bool BF16>
 void launch_attend(const AttendArgs &a, uint32_t blocks, uint32_t grid, hipStream_t s) {
     const uint32_t d = (a.c.dim + 63) / 64;
     if (blocks == 1) {
-        if (d == 1) launch_attend<BF16, REST, 64, 1>(a, grid, s);
-        else if (d == 2) launch_attend<BF16, REST, 128, 1>(a, grid, s);
-        else if (d == 3) launch_attend<BF16, REST, 192, 1>(a, grid, s);
-        else launch_attend<BF16, REST, 256, 1>(a, grid, s);
+        if (d == 1) launch_attend<BF16, 64, 1>(a, grid, s);
+        else if (d == 2) launch_attend<BF16, 128, 1>(a, grid, s);
+        else if (d == 3) launch_attend<BF16, 192, 1>(a, grid, s);
+        else launch_attend<BF16, 256, 1>(a, grid, s);
     } else if (blocks == 4) {
-        if (d == 1) launch_attend<BF16, REST, 64, 4>(a, grid, s);
-        else launch_attend<BF16, REST, 128, 4>(a, grid, s);
+        if (d == 1) launch_attend<BF16, 64, 4>(a, grid, s);
+        else launch_attend<BF16, 128, 4>(a, grid, s);
     } else {
-        if (d == 1) launch_attend<BF16, REST, 64, 2>(a, grid, s);
-        else if (d == 2) launch_attend<BF16, REST, 128, 2>(a, grid, s);
-        else if (d == 3) launch_attend<BF16, REST, 192, 2>(a, grid, s);
-        else launch_attend<BF16, REST, 256, 2>(a, grid, s);
+        if (d == 1) launch_attend<BF16, 64, 2>(a, grid, s);
+        else if (d == 2) launch_attend<BF16, 128, 2>(a, grid, s);
+        else if (d == 3) launch_attend<BF16, 192, 2>(a, grid, s);
+        else launch_attend<BF16, 256, 2>(a, grid, s);
     }
 }
 

@@ -2,12 +2,14 @@
 // of a group have their first tokens in common: HIP kernels and the C ABI of
 // splitzip_kv_attend_shared.
 //
-//   k_shared       the tokens in common, for the query rows of a whole group
-//   k_attend REST  (kv_attend.h) every sequence's other tokens
+//   k_both    the tokens in common, for the query rows of a group, and every
+//             sequence's other tokens, where query rows are few
+//   k_shared  the tokens in common where they are many (k_both then has the
+//             other tokens alone)
 //   k_join_shared  the shares of both joined
 //
-// With x = scale q k over a part of the tokens, a share is m >= max x (in base
-// 2), l = sum 2^(x - m) and o = sum 2^(x - m) v; shares join as
+// With x = scale q k over a part of the tokens, a share is m (near max x, in
+// base 2), l = sum 2^(x - m) and o = sum 2^(x - m) v; shares join as
 // M = max m, out = sum o 2^(m - M) / sum l 2^(m - M).
 
 #include <type_traits>
@@ -17,12 +19,26 @@
 
 namespace {
 
-constexpr uint32_t kRows = 128;        // query rows a workgroup takes: 32 a wave
+constexpr uint32_t kRows = 128;        // query rows a workgroup of k_shared takes: 32 a wave
 constexpr int kSharedThreads = 256;
 constexpr uint32_t kSharedRuns = 512;
+constexpr uint32_t kGroupsHere = 2048; // groups that k_both holds in LDS
 
 // Tokens a tile of K or V has, 16 KB of it or less.
 constexpr int tile_tokens(int dp) { return dp <= 128 ? 64 : 32; }
+
+// How query rows are put together: sequences a row tile has, and row tiles a
+// sequence's query heads of a KV head are cut into (one of the two is 1).
+struct Tiling {
+    uint32_t members, parts, rows;     // rows: of a full row tile
+};
+
+// Where the shares of a sequence's rows of a KV head lie, for the first row of
+// the part: share 0 at row first, share j at row rest + j * 2 rows; whether the
+// sequence has tokens in common with others (in the note of its other tokens).
+struct Note {
+    uint32_t first, rest, n, common;
+};
 
 struct SharedArgs {
     Cache c;
@@ -30,24 +46,16 @@ struct SharedArgs {
     uint64_t qs[2];
     const int32_t *cu, *shared;
     uint32_t groups, heads, group;     // group: query heads of a KV head
-    uint32_t members, parts;           // sequences a row tile has; row tiles a sequence's heads are cut into (one of them is 1)
-    uint32_t rows;                     // rows of a full row tile
-    float scale2;                      // |scale| log2(e)
-    uint32_t negate;                   // 0x80008000 where the scale is negative
+    Tiling of, alone;                  // of groups, of sequences alone (members 1)
+    float scale2;                      // scale * log2(e)
     uint32_t runs;
     Div by_runs, by_group;
-    uint32_t *from;                    // [batch] tokens that were attended for the group
-    uint32_t *notes;                   // [batch][kv_heads][parts][4]: see Note
-    float *slot_o, *slot_ml;           // [runs][2] shares of [rows][dim] and [rows][2]
-    float *whole_o, *whole_ml;         // [batch][heads] of [dim] and [2]: row tiles that were one run's
+    uint32_t *from;                    // [batch] tokens that k_shared attended for the group; NULL: k_both attends them
+    Note *of_notes, *alone_notes;      // [batch][kv_heads][of.parts], [alone.parts]
+    float *o, *ml;                     // rows of [dim] and [2]: shares
+    uint32_t slots, slot_rows;         // the launch's first row of [runs][2][slot_rows] for row tiles that several runs have
+    uint32_t of_whole, alone_whole;    // first rows of [batch][heads]: row tiles that one run has
     int32_t *status;
-};
-
-// Where a sequence's rows of a KV head are: runs first .. first + n - 1 have
-// shares of them, at `row` of the row tile, the first as its second share if it
-// is late; with n = 1 they are in whole_o.
-struct Note {
-    uint32_t first, n2_late, row, reserved;
 };
 
 // A group's sequences, and how many tokens they have in common.
@@ -75,23 +83,235 @@ struct Block64Groups {
     uint32_t units, tiles, before, upto, total;
 };
 
-template <int T>
-__device__ inline void group_units(const SharedArgs &a, const Group &g, uint32_t &units, uint32_t &tiles) {
-    units = g.len ? (g.len - 1) / T + 1 : 0;
-    tiles = ((g.size + a.members - 1) / a.members) * a.parts;
-}
-
-template <int T>
-__device__ inline void load_groups(const SharedArgs &a, uint32_t base, uint32_t carry, Block64Groups &k, int32_t *status) {
-    const uint32_t g = base + (threadIdx.x & 63);
+template <int UNIT>
+__device__ inline void scan_groups(const SharedArgs &a, uint32_t base, uint32_t carry, Group group, Block64Groups &k) {
     k.base = base;
-    k.group = g < a.groups ? group_of(a, g, status) : Group{0, 0, 0};
-    group_units<T>(a, k.group, k.units, k.tiles);
+    k.group = group;
+    k.units = group.len ? (group.len - 1) / UNIT + 1 : 0;
+    k.tiles = ((group.size + a.of.members - 1) / a.of.members) * a.of.parts;
     const uint32_t n = k.units * k.tiles, sum = wave_scan(n);
     k.before = carry + sum - n;
     k.upto = carry + sum;
     k.total = __builtin_amdgcn_readlane(k.upto, 63);
 }
+
+template <int UNIT>
+__device__ inline void load_groups(const SharedArgs &a, uint32_t base, uint32_t carry, Block64Groups &k, int32_t *status) {
+    const uint32_t g = base + (threadIdx.x & 63);
+    scan_groups<UNIT>(a, base, carry, g < a.groups ? group_of(a, g, status) : Group{0, 0, 0}, k);
+}
+
+// One row tile's work on one KV head: some units of its tokens.
+struct Piece {
+    uint32_t first, len, from;       // the sequence whose table row is read, its tokens from .. len - 1
+    uint32_t h, unit0, count, units; // KV head; units of those tokens here, and all of them
+    uint32_t row0, rows;             // rows of the row tile: query heads row0 .. of the sequences from first on, in turn
+    uint32_t part;
+};
+
+// The piece of a group at unit u of the groups' work, from the block that
+// has it.
+__device__ inline Piece group_piece(const SharedArgs &a, const Block64Groups &blk, uint32_t at, uint32_t u, uint32_t u_end) {
+    auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
+    const uint32_t size = lane_of(blk.group.size), tiles = lane_of(blk.tiles);
+    Piece p{lane_of(blk.group.first), lane_of(blk.group.len), 0, 0, 0, 0, lane_of(blk.units), 0, 0, 0};
+    const uint32_t rel = u - lane_of(blk.before) * a.c.kv_heads, pair = rel / p.units;
+    p.unit0 = rel - pair * p.units;
+    p.count = min(p.units - p.unit0, u_end - u);
+    p.h = pair / tiles;
+    const uint32_t tile = pair - p.h * tiles, member0 = tile / a.of.parts * a.of.members;
+    p.part = tile % a.of.parts;
+    p.row0 = member0 * a.group + p.part * a.of.rows;
+    p.rows = a.of.parts == 1 ? min(a.of.members, size - member0) * a.group : min(a.of.rows, a.group - p.part * a.of.rows);
+    return p;
+}
+
+// Sequence and query head of a row.
+__device__ inline void locate_row(const SharedArgs &a, const Piece &p, uint32_t row, uint32_t &b, uint32_t &head) {
+    const uint32_t i = p.row0 + row, m = div(i, a.by_group);
+    b = p.first + m;
+    head = p.h * a.group + i - m * a.group;
+}
+
+// The run that begins a row tile tells the join where its shares will be.
+__device__ inline void note_shares(const SharedArgs &a, const Piece &p, const Cut &cut, uint32_t u, bool late, bool of_group,
+                                   bool common) {
+    const uint32_t members = of_group && a.of.parts == 1 ? p.rows / a.group : 1;
+    if (p.unit0 || threadIdx.x >= members) return;
+    const uint32_t n = p.count == p.units ? 1 : cut.owner(u + p.units - 1) - blockIdx.x + 1;
+    const uint32_t row = threadIdx.x * a.group;      // the member's first
+    uint32_t b, head;
+    locate_row(a, p, row, b, head);
+    const uint32_t rest = a.slots + blockIdx.x * 2 * a.slot_rows + row;
+    const uint32_t first = n > 1 ? rest + (late ? a.slot_rows : 0) : (of_group ? a.of_whole : a.alone_whole) + b * a.heads + head;
+    const uint32_t parts = of_group ? a.of.parts : a.alone.parts;
+    u32x4 *notes = (u32x4 *)(of_group ? a.of_notes : a.alone_notes);
+    notes[((uint64_t)b * a.c.kv_heads + p.h) * parts + p.part] = u32x4{first, rest, n, common};
+}
+
+// The row of a share's arrays that a row of the piece has.
+__device__ inline uint64_t share_row(const SharedArgs &a, const Piece &p, uint32_t row, bool late, bool of_group) {
+    if (p.count != p.units) return a.slots + (uint64_t)(blockIdx.x * 2 + late) * a.slot_rows + row;
+    uint32_t b, head;
+    locate_row(a, p, row, b, head);
+    return (of_group ? a.of_whole : a.alone_whole) + (uint64_t)b * a.heads + head;
+}
+
+// ---------------------------------------------------------------------------
+// few query rows
+// ---------------------------------------------------------------------------
+
+struct Block64Rest {
+    uint32_t base, len, from, units, before, upto, total;
+};
+
+// Groups' tokens in common and sequences' other tokens in units of kUnit, all
+// of them cut into equal runs.  Every workgroup looks all groups and lengths
+// over to find its run; which of the groups a sequence belongs to is looked up
+// in LDS.
+template <bool BF16, int DP, int NT, bool EXACT>
+__global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
+    __shared__ AttendLds<DP, NT> lds;
+    __shared__ uint32_t s_block[kMaxBlocks];
+    __shared__ int32_t s_cu[kGroupsHere + 1];
+    __shared__ uint32_t s_len[kGroupsHere];
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t D = EXACT ? DP : a.c.dim, kvh = a.c.kv_heads;
+    int32_t *status0 = blockIdx.x == 0 ? a.status : nullptr;
+    const uint32_t groups = a.from ? 0 : a.groups;       // that this launch has the tokens of
+
+    Block64Groups gblk{};
+    auto block_of_groups = [&](uint32_t base, uint32_t carry) {
+        const uint32_t g = base + lane;
+        Group x{0, 0, 0};
+        if (g < groups) x = Group{(uint32_t)s_cu[g], (uint32_t)(s_cu[g + 1] - s_cu[g]), s_len[g]};
+        scan_groups<kUnit>(a, base, carry, x, gblk);
+    };
+    uint32_t group_units = 0;
+    if (groups) {
+        for (uint32_t g = tid; g < groups; g += kAttendThreads) {
+            const Group x = group_of(a, g, status0);
+            s_cu[g] = a.cu[g];
+            s_len[g] = x.len;
+            if (g == groups - 1) s_cu[groups] = a.cu[groups];
+        }
+        __syncthreads();
+        for (uint32_t base = 0; base < groups; base += 64) {
+            block_of_groups(base, group_units);
+            group_units = gblk.total;
+        }
+        if (groups > 64) block_of_groups(0, 0);
+        group_units *= kvh;
+    }
+
+    Block64Rest blk{};
+    auto block_of_rest = [&](uint32_t base, uint32_t carry, int32_t *status) {
+        const uint32_t b = base + lane;
+        blk.base = base;
+        blk.len = b < a.c.batch ? seq_len(a.c, b, status) : 0;
+        blk.from = 0;
+        if (a.from) {
+            if (b < a.c.batch) blk.from = min(a.from[b], blk.len);
+        } else {
+            uint32_t lo = 0, hi = groups;        // the last group that begins at b or before
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) >> 1;
+                if (s_cu[mid] <= (int32_t)b) lo = mid + 1; else hi = mid;
+            }
+            if (lo && (int32_t)b < s_cu[lo] && s_len[lo - 1] <= blk.len) blk.from = s_len[lo - 1];
+        }
+        // an empty rest is one unit's work, so that every sequence has a share
+        blk.units = b < a.c.batch ? (blk.len > blk.from ? (blk.len - blk.from - 1) / kUnit + 1 : 1) : 0;
+        const uint32_t sum = wave_scan(blk.units);
+        blk.before = carry + sum - blk.units;
+        blk.upto = carry + sum;
+        blk.total = __builtin_amdgcn_readlane(blk.upto, 63);
+    };
+    const uint32_t blocks = (a.c.batch + 63) / 64, pairs = kvh * a.alone.parts;
+    uint32_t rest_units = 0;
+    if (blocks == 1) {
+        block_of_rest(0, 0, status0);
+        rest_units = blk.total;
+    } else {
+        for (uint32_t i = wave; i < blocks; i += kWaves) {
+            block_of_rest(i * 64, 0, status0);
+            if (lane == 63) s_block[i] = blk.total;
+        }
+        __syncthreads();
+        for (uint32_t f = 0; f < blocks; f += 64)
+            rest_units += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
+    }
+    const Cut cut = cut_of(group_units + rest_units * pairs, a.by_runs);
+    if (blockIdx.x >= cut.runs) return;
+    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = cut.begin(blockIdx.x + 1);
+    bool found = blocks == 1;       // blk is the block of the rest that the run is in, or one before it
+
+    for (uint32_t u = u_begin; u < u_end;) {
+        const bool of_group = u < group_units, late = u != u_begin;
+        Piece p;
+        uint64_t past;
+        if (of_group) {
+            while (!(past = __ballot(gblk.upto * kvh > u))) {
+                if (gblk.base + 64 >= groups) return;
+                block_of_groups(gblk.base + 64, gblk.total);
+            }
+            p = group_piece(a, gblk, (uint32_t)__builtin_ctzll(past), u, u_end);
+        } else {
+            const uint32_t v = u - group_units;
+            if (!found) {
+                uint32_t first = 0, carry = 0;
+                for (uint32_t f = 0; f < blocks; f += 64) {
+                    const uint32_t sum = f + lane < blocks ? s_block[f + lane] : 0, upto = carry + wave_scan(sum);
+                    if ((past = __ballot(upto * pairs > v))) {
+                        const uint32_t i = (uint32_t)__builtin_ctzll(past);
+                        first = (f + i) * 64;
+                        carry = __builtin_amdgcn_readlane(upto - sum, i);
+                        break;
+                    }
+                    carry = __builtin_amdgcn_readlane(upto, 63);
+                }
+                block_of_rest(first, carry, nullptr);
+                found = true;
+            }
+            while (!(past = __ballot(blk.upto * pairs > v))) {
+                if (blk.base + 64 >= a.c.batch) return;      // lengths that another stream changes meanwhile
+                block_of_rest(blk.base + 64, blk.total, nullptr);
+            }
+            const uint32_t at = (uint32_t)__builtin_ctzll(past);
+            auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
+            p = Piece{blk.base + at, lane_of(blk.len), lane_of(blk.from), 0, 0, 0, lane_of(blk.units), 0, 0, 0};
+            const uint32_t rel = v - lane_of(blk.before) * pairs, pair = rel / p.units;
+            p.unit0 = rel - pair * p.units;
+            p.count = min(p.units - p.unit0, u_end - u);
+            p.h = pair / a.alone.parts;
+            p.part = pair - p.h * a.alone.parts;
+            p.row0 = p.part * a.alone.rows;
+            p.rows = min(a.alone.rows, a.group - p.row0);
+        }
+        if (p.h >= kvh) return;
+        const Seen seen{0, p.from, p.len - p.from};
+        attend_tokens<BF16, DP, NT, EXACT>(
+            lds, a.c, p.h, a.c.table + p.first * a.c.table_stride, seen, p.unit0, min(seen.count, (p.unit0 + p.count) * kUnit), p.rows,
+            a.scale2, a.status,
+            [&](uint32_t row) {
+                uint32_t b, head;
+                locate_row(a, p, row, b, head);
+                return a.q + b * a.qs[0] + head * a.qs[1];
+            },
+            [&] { note_shares(a, p, cut, u, late, of_group, p.from != 0); }, false, [](uint32_t, uint32_t, f32x4) {},
+            [&](uint32_t row, uint32_t d, f32x4 y, float top, float sum) {
+                const uint64_t at = share_row(a, p, row, late, of_group);
+                *(f32x4 *)(a.o + at * D + d) = y;
+                if (d == 0) *(f32x2 *)(a.ml + at * 2) = f32x2{top, sum};
+            });
+        u += p.count;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// many query rows
+// ---------------------------------------------------------------------------
 
 // The work -- all row tiles of all groups in tiles of T tokens, for every KV
 // head -- is cut into equal runs, one a workgroup.  A workgroup's four waves
@@ -128,6 +348,9 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim, kvh = a.c.kv_heads;
+    // Logits are compared before they are scaled: a negative scale is the queries'.
+    const uint32_t negate = a.scale2 < 0.f ? 0x80008000u : 0;
+    const float scale2 = fabsf(a.scale2);
     // This lane's places in a tile: where it puts its pieces, and what it reads
     // of the first 16 rows (further ones are a constant away).
     uint32_t put[NP], k_at[KS], v_at[4], v8_at[4];
@@ -201,37 +424,23 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
             if (blk.base + 64 >= a.groups) return;      // cu or lengths that change meanwhile
             load_groups<T>(a, blk.base + 64, blk.total, blk, nullptr);
         }
-        const uint32_t at = (uint32_t)__builtin_ctzll(past);
-        const uint32_t first = __builtin_amdgcn_readlane(blk.group.first, at), size = __builtin_amdgcn_readlane(blk.group.size, at),
-                       len = __builtin_amdgcn_readlane(blk.group.len, at), units = __builtin_amdgcn_readlane(blk.units, at),
-                       tiles = __builtin_amdgcn_readlane(blk.tiles, at), rel = u - __builtin_amdgcn_readlane(blk.before, at) * kvh;
-        const uint32_t pair = rel / units, unit0 = rel - pair * units, count = min(units - unit0, u_end - u);
-        const uint32_t h = pair / tiles, tile = pair - h * tiles;
-        if (h >= kvh) return;
-        const bool whole = count == units;
-        const uint32_t member0 = tile / a.parts * a.members, part = tile % a.parts;
-        const uint32_t members = min(a.members, size - member0);
-        const uint32_t rows = a.parts == 1 ? members * a.group : min(a.rows, a.group - part * a.rows);
-        const uint32_t end = min(len, (unit0 + count) * T);
-        const int32_t *table = a.c.table + first * a.c.table_stride;
-        // member and query head of a row
-        auto locate_row = [&](uint32_t r, uint32_t &b, uint32_t &head) {
-            const uint32_t i = part * a.rows + r, m = div(i, a.by_group);
-            b = first + member0 + m;
-            head = h * a.group + i - m * a.group;
-        };
+        const Piece p = group_piece(a, blk, (uint32_t)__builtin_ctzll(past), u, u_end);
+        if (p.h >= kvh) return;
+        const bool late = u != u_begin;
+        const uint32_t rows = p.rows, end = min(p.len, (p.unit0 + p.count) * T);
+        const int32_t *table = a.c.table + p.first * a.c.table_stride;
 
         u32x4 q[2][KS];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint32_t r = wave * 32 + t * 16 + c16;
             uint32_t b = 0, head = 0;
-            if (r < rows) locate_row(r, b, head);
+            if (r < rows) locate_row(a, p, r, b, head);
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
                 const uint32_t d = j * 32 + g * 8;
                 q[t][j] = u32x4{0, 0, 0, 0};
-                if (r < rows && (EXACT || d < D)) q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + head * a.qs[1] + d) ^ a.negate;
+                if (r < rows && (EXACT || d < D)) q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + head * a.qs[1] + d) ^ negate;
             }
         }
         f32x4 o[2][VC];
@@ -247,11 +456,11 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
         // Staging: this thread's pieces of a tile.  A row's place is found by one
         // lane, two tiles ahead (the waves take turns), from a page number loaded
         // a tile before; the pieces' threads take it from LDS.
-        const uint16_t *k_head = a.c.k + h * a.c.ks[1], *v_head = a.c.v + h * a.c.vs[1];
+        const uint16_t *k_head = a.c.k + p.h * a.c.ks[1], *v_head = a.c.v + p.h * a.c.vs[1];
         u32x4 kx[NP], vx[NP];
         auto row_of = [&](int k) { return (tid + k * kSharedThreads) / PR; };
         auto piece_of = [&](int k) { return (tid + k * kSharedThreads) % PR; };
-        const uint32_t tile0 = unit0, tile_end = (end - 1) / T + 1;
+        const uint32_t tile0 = p.unit0, tile_end = (end - 1) / T + 1;
         auto page_at = [&](uint32_t n) {
             const uint32_t t = n * T + lane;
             return lane < T && t < end ? (uint32_t)table[div(t, a.c.page)] : 0xffffffffu;
@@ -292,11 +501,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
             place(tile0 + turn, page);
             page = page_at(tile0 + turn + 4);
         }
-        if (unit0 == 0 && tid < members) {
-            const uint32_t shares = whole ? 1 : cut.owner(u + units - 1) - blockIdx.x + 1;
-            ((u32x4 *)a.notes)[((uint64_t)(first + member0 + tid) * kvh + h) * a.parts + part] =
-                u32x4{blockIdx.x, shares * 2 + (u != u_begin), tid * a.group, 0};
-        }
+        note_shares(a, p, cut, u, late, true, true);
         __syncthreads();
         fetch(tile0);
         for (uint32_t n = tile0; n < tile_end; ++n) {
@@ -333,7 +538,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                     for (int i = 0; i < 4; ++i)
                         if (!(mine >> (s * 16 + i) & 1)) x[0][s][i] = x[1][s][i] = -INFINITY;
             }
-            u32x4 p[2][ST / 2];
+            u32x4 w16[2][ST / 2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 float top = -INFINITY;
@@ -341,7 +546,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][s][i]);
-                top = row_reduce<true>(top) * a.scale2 - kLift;
+                top = row_reduce<true>(top) * scale2 - kLift;
                 // The sums are rescaled only where weights would pass 2^(kLift + kSlack):
                 // rarely, after a run's first tiles.
                 if (__any(top > m[t] + kSlack)) {
@@ -356,10 +561,10 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 for (int s = 0; s < ST; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
-                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], a.scale2, -use));
-                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], a.scale2, -use));
+                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], scale2, -use));
+                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], scale2, -use));
                         l[t] += p0 + p1;
-                        p[t][s >> 1][(s & 1) * 2 + i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
+                        w16[t][s >> 1][(s & 1) * 2 + i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
                     }
             }
             // 32 tokens a time: the lane's 8 tokens' pieces, halves of words exchanged
@@ -378,8 +583,8 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 col[i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], odd ? 0x07060302u : 0x05040100u);
-                            o[0][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, p[0][s], o[0][w0 * 8 + 2 * w + odd]);
-                            o[1][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, p[1][s], o[1][w0 * 8 + 2 * w + odd]);
+                            o[0][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[0][s], o[0][w0 * 8 + 2 * w + odd]);
+                            o[1][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[1][s], o[1][w0 * 8 + 2 * w + odd]);
                         }
                 }
                 if constexpr (P8 > 0) {
@@ -395,24 +600,21 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 col[i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], odd ? 0x07060302u : 0x05040100u);
-                            o[0][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, p[0][s], o[0][P16 * 8 + 2 * w + odd]);
-                            o[1][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, p[1][s], o[1][P16 * 8 + 2 * w + odd]);
+                            o[0][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[0][s], o[0][P16 * 8 + 2 * w + odd]);
+                            o[1][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[1][s], o[1][P16 * 8 + 2 * w + odd]);
                         }
                 }
             }
         }
 
-        const uint32_t slot = blockIdx.x * 2 + (u != u_begin);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             l[t] = row_reduce<false>(l[t]);
             const uint32_t r = wave * 32 + t * 16 + c16;
             if (r >= rows) continue;
-            uint32_t b, head;
-            locate_row(r, b, head);
-            const uint64_t row = whole ? b * (uint64_t)a.heads + head : (uint64_t)slot * a.rows + r;
-            float *to = (whole ? a.whole_o : a.slot_o) + row * D;
-            if (g == 0) *(f32x2 *)((whole ? a.whole_ml : a.slot_ml) + row * 2) = f32x2{m[t], l[t]};
+            const uint64_t row = share_row(a, p, r, late, true);
+            float *to = a.o + row * D;
+            if (g == 0) *(f32x2 *)(a.ml + row * 2) = f32x2{m[t], l[t]};
 #pragma unroll
             for (int w0 = 0; w0 < P16 + P8; ++w0) {
                 const int wide = w0 < P16 ? 8 : 4;       // columns of a piece
@@ -428,90 +630,90 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                     }
             }
         }
-        u += count;
+        u += p.count;
     }
 }
 
-constexpr uint32_t kMaxShares = kSharedRuns + 1024;      // of a query head: runs of both kernels
+// ---------------------------------------------------------------------------
+// join
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kMaxShares = kSharedRuns + 1024;      // of a query head: runs of both launches
+constexpr int kAhead = 12;                               // shares a thread loads before their weights are known
 
 struct JoinArgs {
     SharedArgs s;
-    AttendArgs r;          // the rest
+    uint16_t *out;
+    uint64_t os[2];
+    float *lse;
+    uint32_t rows, of_step, alone_step;      // rows there are; rows from a share to the next
 };
 
-// One workgroup per query head of a sequence.
+// One workgroup per query head of a sequence: its shares, rescaled to their
+// common maximum.  A chain of two loads (where they are; maxima, sums and
+// outputs together); every wave works the weights out for itself instead of
+// waiting for another.
 template <bool BF16>
-__global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs ja) {
+__global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
     __shared__ float s_w[kJoinThreads / 64][kMaxShares];
     __shared__ f32x4 s_o[kJoinThreads];
-    const SharedArgs &a = ja.s;
-    const AttendArgs &r = ja.r;
+    const SharedArgs &a = j.s;
     const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, b = blockIdx.y, head = blockIdx.x, dim = a.c.dim;
-    const uint32_t h = head / a.group, in_group = head - h * a.group, part = in_group / a.rows;
-    const uint64_t whole = b * (uint64_t)a.heads + head;
-    uint32_t first = 0, n0 = 0, row = 0, late = 0;
-    if (a.from[b]) {
-        const u32x4 note = ((const u32x4 *)a.notes)[((uint64_t)b * a.c.kv_heads + h) * a.parts + part];
-        // within the workspace also where arguments that changed meanwhile left it unwritten
-        first = min(note[0], a.runs - 1), n0 = min(note[1] >> 1, a.runs - first), late = note[1] & 1;
-        row = min(note[2] + in_group - part * a.rows, a.rows - 1);
-    }
-    uint32_t rest_first = 0, n1 = 1, rest_row = 0, rest_late = 0;
-    if (r.runs) {
-        const Shares sh(r, b, h, in_group);
-        rest_first = sh.first, n1 = sh.n, rest_row = sh.row, rest_late = sh.late;
-    }
-    const uint32_t n = n0 + n1;
-    // rows of a share, and whose array they are in
-    auto place = [&](uint32_t j, const float *&o, const float *&ml) {
-        uint64_t at = whole;
-        if (j < n0) {
-            if (n0 > 1) at = (uint64_t)((first + j) * 2 + (j == 0 ? late : 0)) * a.rows + row;
-            o = n0 > 1 ? a.slot_o : a.whole_o;
-            ml = n0 > 1 ? a.slot_ml : a.whole_ml;
-        } else {
-            j -= n0;
-            if (n1 > 1) at = (uint64_t)((rest_first + j) * 2 + (j == 0 ? rest_late : 0)) * r.rows + rest_row;
-            o = n1 > 1 ? r.share_o : r.whole_o;
-            ml = n1 > 1 ? r.share_ml : r.whole_ml;
-        }
-        o += at * dim;
-        ml += at * 2;
+    const uint32_t h = head / a.group, in_group = head - h * a.group;
+    const uint32_t of_part = in_group / a.of.rows, alone_part = in_group / a.alone.rows;
+    u32x4 of = ((const u32x4 *)a.of_notes)[((uint64_t)b * a.c.kv_heads + h) * a.of.parts + of_part];
+    const u32x4 alone = ((const u32x4 *)a.alone_notes)[((uint64_t)b * a.c.kv_heads + h) * a.alone.parts + alone_part];
+    // (bounded, where arguments that changed meanwhile left notes unwritten)
+    const uint32_t n0 = alone[3] ? min(of[2], kMaxShares / 2) : 0, n = n0 + min(alone[2], kMaxShares / 2);
+    const uint32_t of_row = in_group - of_part * a.of.rows, alone_row = in_group - alone_part * a.alone.rows;
+    auto row_of = [&](uint32_t i) {
+        const uint32_t k = i < n0 ? i : i - n0, step = i < n0 ? j.of_step : j.alone_step;
+        const uint32_t at = k ? (i < n0 ? of[1] : alone[1]) + k * step : i < n0 ? of[0] : alone[0];
+        return (uint64_t)min(at + (i < n0 ? of_row : alone_row), j.rows - 1);
     };
-    float top = -INFINITY, sum = 0.f;
-    for (uint32_t j = lane; j < n; j += 64) {
-        const float *o, *ml;
-        place(j, o, ml);
-        top = fmaxf(top, ml[0]);
+    const uint32_t pieces = dim / 4, ways = kJoinThreads / pieces;      // 4-column pieces of a row; shares summed side by side
+    const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
+    f32x4 y[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const uint32_t k = way + i * ways;
+        y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (way < ways && k < n) y[i] = *(const f32x4 *)(a.o + row_of(k) * dim + d);
     }
+    f32x2 ml{-INFINITY, 0.f};
+    if (lane < n) ml = *(const f32x2 *)(a.ml + row_of(lane) * 2);
+    float top = ml[0];
+    for (uint32_t k = lane + 64; k < n; k += 64) top = fmaxf(top, a.ml[row_of(k) * 2]);
     top = wave_reduce<true>(top);
-    for (uint32_t j = lane; j < n; j += 64) {
-        const float *o, *ml;
-        place(j, o, ml);
-        // a share with m = -inf saw no finite logit: its sum is 0, or NaN, which stays
-        const float w = ml[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[0] - top);
-        s_w[wave][j] = w;
-        sum += ml[1] * w;
+    // a share with m = -inf saw no finite logit: its sum is 0, or NaN, which stays
+    auto weight = [&](float m) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
+    float w = weight(ml[0]), sum = ml[1] * w;
+    if (lane < n) s_w[wave][lane] = w;
+    for (uint32_t k = lane + 64; k < n; k += 64) {
+        const f32x2 more = *(const f32x2 *)(a.ml + row_of(k) * 2);
+        w = weight(more[0]);
+        s_w[wave][k] = w;
+        sum += more[1] * w;
     }
     sum = wave_reduce<false>(sum);
     __builtin_amdgcn_wave_barrier();
-    const uint32_t pieces = dim / 4, ways = kJoinThreads / pieces;
-    const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
-    f32x4 y{0.f, 0.f, 0.f, 0.f};
-    if (way < ways)
-        for (uint32_t j = way; j < n; j += ways) {
-            const float *o, *ml;
-            place(j, o, ml);
-            y += *(const f32x4 *)(o + d) * s_w[wave][j];
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    if (way < ways) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t k = way + i * ways;
+            if (k < n) o += y[i] * s_w[wave][k];
         }
-    s_o[tid] = y;
+        for (uint32_t k = way + kAhead * ways; k < n; k += ways) o += *(const f32x4 *)(a.o + row_of(k) * dim + d) * s_w[wave][k];
+    }
+    s_o[tid] = o;
     __syncthreads();
     if (tid < pieces) {
-        for (uint32_t w = 1; w < ways; ++w) y += s_o[w * pieces + tid];
+        for (uint32_t k = 1; k < ways; ++k) o += s_o[k * pieces + tid];
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        u32x2 z{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv)};
-        *(u32x2 *)(r.out + b * r.os[0] + head * r.os[1] + d) = z;
-        if (tid == 0 && r.lse) r.lse[whole] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
+        u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
+        *(u32x2 *)(j.out + b * j.os[0] + head * j.os[1] + d) = z;
+        if (tid == 0 && j.lse) j.lse[b * (uint64_t)a.heads + head] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
     }
 }
 
@@ -520,37 +722,86 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs ja) {
 // ---------------------------------------------------------------------------
 
 struct SharedPlan {
-    AttendPlan rest;
-    uint32_t members, parts, rows, runs;
-    size_t from_at, notes_at, slot_at, slot_ml_at, whole_at, whole_ml_at, rest_whole_at, rest_whole_ml_at, rest_at, bytes;
+    uint32_t group, blocks, both_runs, shared_runs;     // blocks of 16 rows in k_both; shared_runs 0: no k_shared
+    Tiling of, alone;
+    uint32_t of_slots, of_whole, both_slots, alone_whole, rows, slot_rows;
+    size_t from_at, of_notes_at, alone_notes_at, ml_at, o_at, bytes;
 };
 
-bool shared_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups, SharedPlan &p) {
-    if (groups > SPLITZIP_KV_MAX_BATCH || !attend_plan(c, heads, 0, p.rest)) return false;
-    const uint32_t group = p.rest.group;
-    p.members = group <= kRows ? kRows / group : 1;
-    p.parts = (group - 1) / kRows + 1;
-    p.rows = p.parts == 1 ? p.members * group : (group - 1) / p.parts + 1;
+Tiling tiling(uint32_t group, uint32_t most) {
+    Tiling t{};
+    t.members = group <= most ? most / group : 1;
+    t.parts = (group - 1) / most + 1;
+    t.rows = t.parts == 1 ? t.members * group : (group - 1) / t.parts + 1;
+    return t;
+}
+
+// many: with k_shared; most: query rows a workgroup of k_both takes.
+bool lay_out(const splitzip_kv_cache *c, uint32_t heads, bool many, uint32_t most, SharedPlan &p) {
+    const uint32_t group = heads / c->kv_heads, batch = c->batch;
+    p.group = group;
+    p.blocks = most / 16;
+    p.alone = tiling(group, most);
+    p.alone.members = 1;
+    p.alone.rows = p.alone.parts == 1 ? group : p.alone.rows;
+    p.of = tiling(group, many ? kRows : most);
     const uint64_t all = (uint64_t)c->max_pages * c->page_size;
     const uint32_t tokens = tile_tokens((c->head_dim + 63) / 64 * 64);
-    const uint64_t units = (all / tokens + 1) * c->batch * p.parts * c->kv_heads;
-    if (units >> 31) return false;
-    // a group has two sequences at least
-    const uint64_t most = groups ? units : 0, runs = c->head_dim <= 192 ? kSharedRuns : kSharedRuns / 2;
-    p.runs = (uint32_t)(most < runs ? most : runs);
-    if (p.runs < 1) p.runs = 1;
-    const size_t row = (size_t)c->head_dim * 4, per = (size_t)c->batch * heads, slots = (size_t)p.runs * 2 * p.rows;
+    const uint64_t tiles = (uint64_t)batch * p.of.parts * c->kv_heads;      // of groups, at most
+    const uint64_t both = (all / kUnit + 1) * ((many ? 0 : tiles) + (uint64_t)batch * p.alone.parts * c->kv_heads);
+    const uint64_t shared = many ? (all / tokens + 1) * tiles : 0;
+    if (both >> 31 || shared >> 31) return false;
+    const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim <= 192 ? kSharedRuns : kSharedRuns / 2;
+    p.both_runs = both < runs ? (uint32_t)both : runs;
+    p.shared_runs = shared < more ? (uint32_t)shared : more;
+    p.slot_rows = p.of.rows > p.alone.rows ? p.of.rows : p.alone.rows;
+    if (many) p.slot_rows = p.alone.rows;
+    const uint64_t per = (uint64_t)batch * heads, of_slots = (uint64_t)p.shared_runs * 2 * p.of.rows,
+                   both_slots = (uint64_t)p.both_runs * 2 * p.slot_rows, rows = of_slots + both_slots + 2 * per;
+    if (rows >> 31) return false;
+    p.of_slots = 0;
+    p.of_whole = (uint32_t)of_slots;
+    p.both_slots = p.of_whole + (uint32_t)per;
+    p.alone_whole = p.both_slots + (uint32_t)both_slots;
+    p.rows = (uint32_t)rows;
     p.from_at = 0;
-    p.notes_at = up16((size_t)c->batch * 4);
-    p.slot_at = p.notes_at + (size_t)c->batch * c->kv_heads * p.parts * sizeof(Note);
-    p.slot_ml_at = p.slot_at + slots * row;
-    p.whole_at = up16(p.slot_ml_at + slots * 8);
-    p.whole_ml_at = p.whole_at + per * row;
-    p.rest_whole_at = up16(p.whole_ml_at + per * 8);
-    p.rest_whole_ml_at = p.rest_whole_at + per * row;
-    p.rest_at = up16(p.rest_whole_ml_at + per * 8);
-    p.bytes = p.rest_at + p.rest.bytes;
+    p.of_notes_at = up16((size_t)batch * 4);
+    p.alone_notes_at = p.of_notes_at + (size_t)batch * c->kv_heads * p.of.parts * sizeof(Note);
+    p.ml_at = p.alone_notes_at + (size_t)batch * c->kv_heads * p.alone.parts * sizeof(Note);
+    p.o_at = up16(p.ml_at + rows * 8);
+    p.bytes = p.o_at + rows * c->head_dim * 4;
+    if (p.bytes < 16) p.bytes = 16;
     return true;
+}
+
+bool shape_fits(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups) {
+    return groups <= SPLITZIP_KV_MAX_BATCH && heads && heads <= SPLITZIP_KV_MAX_HEADS && heads % c->kv_heads == 0;
+}
+
+// By the query rows of a group of average size; the sizes are on the device.
+bool shared_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups, SharedPlan &p) {
+    if (!shape_fits(c, heads, groups)) return false;
+    const uint32_t group = heads / c->kv_heads;
+    const uint64_t average = groups ? (uint64_t)c->batch * group / groups : 0;
+    const bool many = groups && (average > 32 || groups > kGroupsHere);
+    return lay_out(c, heads, many, group <= 16 && (many || average <= 16) ? 16 : 32, p);
+}
+
+template <bool BF16>
+void launch_both(const SharedArgs &a, uint32_t blocks, hipStream_t s) {
+    auto go = [&](auto dp, auto nt) {
+        constexpr int DP = decltype(dp)::value, NT = decltype(nt)::value;
+        if (a.c.dim == DP) k_both<BF16, DP, NT, true><<<a.runs, kAttendThreads, 0, s>>>(a);
+        else k_both<BF16, DP, NT, false><<<a.runs, kAttendThreads, 0, s>>>(a);
+    };
+    auto with = [&](auto dp) {
+        if (blocks == 1) go(dp, std::integral_constant<int, 1>{});
+        else go(dp, std::integral_constant<int, 2>{});
+    };
+    if (a.c.dim <= 64) with(std::integral_constant<int, 64>{});
+    else if (a.c.dim <= 128) with(std::integral_constant<int, 128>{});
+    else if (a.c.dim <= 192) with(std::integral_constant<int, 192>{});
+    else with(std::integral_constant<int, 256>{});
 }
 
 template <bool BF16>
@@ -573,9 +824,14 @@ extern "C" {
 size_t splitzip_kv_groups_struct_size(void) { return sizeof(splitzip_kv_groups); }
 
 size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t groups) {
-    SharedPlan p;
-    if (!shape_ok(cache) || !shared_plan(cache, heads, groups, p)) return 0;
-    return p.bytes;
+    if (!shape_ok(cache) || !shape_fits(cache, heads, groups)) return 0;
+    size_t bytes = 0;
+    for (int way = 0; way < 4; ++way) {      // a call with fewer groups goes another way
+        SharedPlan p;
+        if (!lay_out(cache, heads, way & 1, way & 2 ? 32 : 16, p)) return 0;
+        if (p.bytes > bytes) bytes = p.bytes;
+    }
+    return bytes;
 }
 
 int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_query *query, const splitzip_kv_groups *groups,
@@ -594,70 +850,55 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     if (!Q.q || !Q.out || !aligned(Q.q, 16) || !aligned(Q.out, 16) || !d_ws || !aligned(d_ws, 16)) return SPLITZIP_ERR_INVALID;
     if (ws_bytes < P.bytes) return SPLITZIP_ERR_WORKSPACE;
     uint8_t *ws = reinterpret_cast<uint8_t *>(d_ws);
-    JoinArgs ja{};
-    SharedArgs &a = ja.s;
+    SharedArgs a{};
     a.c = view(cache);
     a.q = Q.q;
     a.cu = groups->cu;
     a.shared = groups->shared;
     a.groups = groups->groups;
     a.heads = Q.heads;
-    a.group = P.rest.group;
-    a.members = P.members;
-    a.parts = P.parts;
-    a.rows = P.rows;
-    // a scale of 0 makes no order of logits: every sequence on its own
-    a.scale2 = (Q.scale < 0 ? -Q.scale : Q.scale) * kLog2e;
-    if (a.scale2 == 0.f) a.groups = 0;
-    a.negate = Q.scale < 0 ? 0x80008000u : 0;
-    a.runs = P.runs;
-    a.by_runs = make_div(P.runs);
-    a.by_group = make_div(a.group);
-    a.from = reinterpret_cast<uint32_t *>(ws + P.from_at);
-    a.notes = reinterpret_cast<uint32_t *>(ws + P.notes_at);
-    a.slot_o = reinterpret_cast<float *>(ws + P.slot_at);
-    a.slot_ml = reinterpret_cast<float *>(ws + P.slot_ml_at);
-    a.whole_o = reinterpret_cast<float *>(ws + P.whole_at);
-    a.whole_ml = reinterpret_cast<float *>(ws + P.whole_ml_at);
+    a.group = P.group;
+    a.of = P.of;
+    a.alone = P.alone;
+    a.scale2 = Q.scale * kLog2e;
+    a.by_group = make_div(P.group);
+    a.of_notes = reinterpret_cast<Note *>(ws + P.of_notes_at);
+    a.alone_notes = reinterpret_cast<Note *>(ws + P.alone_notes_at);
+    a.ml = reinterpret_cast<float *>(ws + P.ml_at);
+    a.o = reinterpret_cast<float *>(ws + P.o_at);
+    a.of_whole = P.of_whole;
+    a.alone_whole = P.alone_whole;
     a.status = d_status;
-    AttendArgs &r = ja.r;
-    r.c = a.c;
-    r.q = Q.q;
-    r.out = Q.out;
-    r.lse = Q.lse;
-    for (int i = 0; i < 2; ++i) {
-        a.qs[i] = r.qs[i] = Q.q_stride[i];
-        r.os[i] = Q.out_stride[i];
-    }
-    r.heads = Q.heads;
-    r.group = P.rest.group;
-    r.row_tiles = P.rest.row_tiles;
-    r.rows = P.rest.rows;
-    r.window = SPLITZIP_KV_ALL;
-    r.scale2 = Q.scale * kLog2e;
-    r.status = d_status;
-    r.from = a.from;
-    uint8_t *rest = ws + P.rest_at;
-    r.splits = reinterpret_cast<uint32_t *>(rest);
-    r.share_o = reinterpret_cast<float *>(rest + P.rest.o_at);
-    r.share_ml = reinterpret_cast<float *>(rest + P.rest.ml_at);
-    r.whole_o = reinterpret_cast<float *>(ws + P.rest_whole_at);
-    r.whole_ml = reinterpret_cast<float *>(ws + P.rest_whole_ml_at);
-    const uint32_t grid = lay_out(r, P.rest, r.c.max_len);
+    for (int i = 0; i < 2; ++i) a.qs[i] = Q.q_stride[i];
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = cache->dtype == SPLITZIP_KV_BF16;
-    const uint32_t grid_shared = P.runs + (cache->batch - 1) / kSharedThreads + 1;
-    if (bf16) launch_shared<true>(a, grid_shared, s);
-    else launch_shared<false>(a, grid_shared, s);
-    int rc = launched();
+    // a scale of 0 makes no order of logits, which k_shared goes by: every sequence on its own
+    if (P.shared_runs && a.scale2 == 0.f) a.groups = 0;
+    const bool many = P.shared_runs && a.groups;
+    if (many) {
+        a.from = reinterpret_cast<uint32_t *>(ws + P.from_at);
+        a.runs = P.shared_runs;
+        a.by_runs = make_div(a.runs);
+        a.slots = P.of_slots;
+        a.slot_rows = P.of.rows;
+        const uint32_t grid = a.runs + (cache->batch - 1) / kSharedThreads + 1;
+        if (bf16) launch_shared<true>(a, grid, s);
+        else launch_shared<false>(a, grid, s);
+        const int rc = launched();
+        if (rc) return rc;
+    }
+    a.runs = P.both_runs;
+    a.by_runs = make_div(a.runs);
+    a.slots = P.both_slots;
+    a.slot_rows = P.slot_rows;
+    if (bf16) launch_both<true>(a, P.blocks, s);
+    else launch_both<false>(a, P.blocks, s);
+    const int rc = launched();
     if (rc) return rc;
-    if (bf16) launch_attend<true, true>(r, P.rest.blocks, grid, s);
-    else launch_attend<false, true>(r, P.rest.blocks, grid, s);
-    rc = launched();
-    if (rc) return rc;
+    JoinArgs j{a, Q.out, {Q.out_stride[0], Q.out_stride[1]}, Q.lse, P.rows, 2 * (many ? P.of.rows : P.slot_rows), 2 * P.slot_rows};
     const dim3 joins(Q.heads, cache->batch);
-    if (bf16) k_join_shared<true><<<joins, kJoinThreads, 0, s>>>(ja);
-    else k_join_shared<false><<<joins, kJoinThreads, 0, s>>>(ja);
+    if (bf16) k_join_shared<true><<<joins, kJoinThreads, 0, s>>>(j);
+    else k_join_shared<false><<<joins, kJoinThreads, 0, s>>>(j);
     return launched();
 }
 
