@@ -53,9 +53,6 @@ struct PageArgs {
     int32_t *status;
 };
 
-__device__ inline void take_name(const State &s, uint32_t page, int32_t n) {
-    if (atomicAdd(&s.refs[page], n) == 0) atomicSub(&s.free_in[page / kBlock], 1);
-}
 __device__ inline void drop_name(const State &s, uint32_t page, int32_t n) {
     if (atomicSub(&s.refs[page], n) == n) atomicAdd(&s.free_in[page / kBlock], 1);
 }
@@ -83,14 +80,15 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 4;     // pieces a thread has under way
 
 // The workgroup copies the first `slots` slots of a page.
+template <int AHEAD = kCopyAhead>
 __device__ inline void copy_page(const uint16_t *src, uint16_t *dst, const Geometry &g, uint32_t slots) {
     const uint32_t total = g.slot_first ? slots * g.per_slot : g.total;
-    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kCopyThreads * kCopyAhead) {
-        u32x4 x[kCopyAhead];
-        uint64_t to[kCopyAhead];
-        bool ok[kCopyAhead];
+    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kCopyThreads * AHEAD) {
+        u32x4 x[AHEAD];
+        uint64_t to[AHEAD];
+        bool ok[AHEAD];
 #pragma unroll
-        for (int u = 0; u < kCopyAhead; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const uint32_t i = i0 + u * kCopyThreads;
             const uint32_t row = div(i, g.run), piece = i - row * g.run.d;
             const uint32_t r0 = div(row, g.n1), r1 = row - r0 * g.n1.d;
@@ -99,7 +97,7 @@ __device__ inline void copy_page(const uint16_t *src, uint16_t *dst, const Geome
             if (ok[u]) x[u] = load_once(src + r0 * g.s0 + r1 * g.s1 + piece * 8);
         }
 #pragma unroll
-        for (int u = 0; u < kCopyAhead; ++u)
+        for (int u = 0; u < AHEAD; ++u)
             if (ok[u]) store_away(dst + to[u], x[u]);
     }
 }
@@ -149,6 +147,45 @@ __global__ __launch_bounds__(kThreads) void k_free(PageArgs a, uint32_t blocks) 
     }
 }
 
+constexpr uint32_t kSmallPages = 16384, kSmallEntries = 4096;
+constexpr int kSmallThreads = 1024;
+
+// The same by one workgroup, with the counts in LDS (a pool of 64 pages and 4
+// rows of 13 entries: one launch instead of three).
+__global__ __launch_bounds__(kSmallThreads) void k_count(PageArgs a, uint32_t width) {
+    __shared__ int32_t n[kSmallPages];
+    const uint32_t tid = threadIdx.x;
+    for (uint32_t p = tid; p < a.c.num_pages; p += kSmallThreads) n[p] = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < a.c.batch * width; i += kSmallThreads) {
+        const uint32_t b = i / width, at = i - b * width;
+        const uint32_t held = pages_for(a.c, seq_len(a.c, b, at == 0 ? a.status : nullptr));
+        int32_t *entry = a.table + b * a.c.table_stride + at;
+        const uint32_t page = (uint32_t)*entry;
+        if (at < held && page < a.c.num_pages) {
+            atomicAdd(&n[page], 1);
+        } else {
+            if (at < held) report(a.status, SPLITZIP_KV_BAD_PAGE);
+            *entry = -1;
+        }
+    }
+    __syncthreads();
+    for (uint32_t p = tid; p < a.c.num_pages; p += kSmallThreads) {
+        a.s.refs[p] = n[p];
+        a.s.writers[p] = 0;
+        a.s.lowest[p] = 0x7fffffff;
+    }
+    // a wave for every 256 pages
+    for (uint32_t k = tid >> 6; k * kBlock < a.c.num_pages; k += kSmallThreads / 64) {
+        uint32_t is_free = 0;
+        for (uint32_t q = 0; q < kBlock; q += 64) {
+            const uint32_t p = k * kBlock + q + (tid & 63);
+            is_free += __popcll(__ballot(p < a.c.num_pages && n[p] == 0));
+        }
+        if ((tid & 63) == 0) a.s.free_in[k] = is_free;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------
@@ -158,49 +195,66 @@ constexpr int kForkThreads = 1024;
 // A workgroup has some columns of the table for all sequences (the last one
 // the lengths): it reads what the rows will be, and then writes them, so that
 // rows can be copies of each other in any order without a second table.  A
-// thread has U rows of one column, one below the other: beams of one parent
-// are named in one addition.
+// row's pages are named by as many rows as have it as parent, instead of by
+// itself: one addition for all of them, and none where rows change places.  A
+// thread has U rows of one column, one below the other, whose additions to one
+// page are one.  (64 beams of up to 2048 tokens 5.2 us; naming and dropping
+// entry by entry, 15.)
 template <int U>
 __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t width, uint32_t columns) {
+    extern __shared__ uint32_t s_children[];      // [batch / 2 + 1], 16 bits each
+    const uint32_t batch = a.c.batch;
+    for (uint32_t k = threadIdx.x; k < batch / 2 + 1; k += blockDim.x) s_children[k] = 0;
+    __syncthreads();
     const bool is_lens = blockIdx.x == gridDim.x - 1;
+    auto parent_of = [&](uint32_t b) {
+        const int32_t p = a.arg[b];
+        return p >= -1 && p < (int32_t)batch ? p : (int32_t)b;
+    };
+    for (uint32_t b = threadIdx.x; b < batch; b += blockDim.x) {
+        const int32_t p = parent_of(b);
+        if (is_lens && p != a.arg[b]) report(a.status, SPLITZIP_KV_BAD_PARENT);
+        // (a sum of up to 65535 stays within its half)
+        if (p >= 0) atomicAdd(&s_children[p >> 1], p & 1 ? 1u << 16 : 1u);
+    }
     const uint32_t per_row = is_lens ? 1 : columns;       // a power of two
     const uint32_t i = blockIdx.x * columns + (threadIdx.x & (per_row - 1));
     const uint32_t b0 = threadIdx.x / per_row * U;
-    int32_t next[U];
+    const bool mine = is_lens || i < width;
+    int32_t next[U], was[U];
     uint64_t changed = 0;
-    uint32_t page = kNoPage;
-    int32_t names = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const uint32_t b = b0 + u;
-        next[u] = 0;
-        if (b >= a.c.batch || (!is_lens && i >= width)) continue;
-        const int32_t parent = a.arg[b];
-        if (parent < -1 || parent >= (int32_t)a.c.batch) {
-            if (is_lens) report(a.status, SPLITZIP_KV_BAD_PARENT);
-            continue;
-        }
+        was[u] = next[u] = -1;
+        if (!mine || b >= batch) continue;
+        const int32_t parent = parent_of(b);
+        if (!is_lens) was[u] = a.table[b * a.c.table_stride + i];
         if (parent == (int32_t)b) continue;
         changed |= 1ull << u;
-        if (is_lens) {
-            next[u] = parent < 0 ? 0 : a.c.lens[parent];
-            continue;
-        }
-        const int32_t was = a.table[b * a.c.table_stride + i];
-        next[u] = parent < 0 ? -1 : a.table[parent * a.c.table_stride + i];
-        if (was == next[u]) continue;
-        if ((uint32_t)was < a.c.num_pages) drop_name(a.s, was, 1);
-        if ((uint32_t)next[u] < a.c.num_pages) {
-            if ((uint32_t)next[u] != page) {
-                if (names) take_name(a.s, page, names);
-                page = next[u];
-                names = 0;
-            }
-            ++names;
-        }
+        if (is_lens) next[u] = parent < 0 ? 0 : a.c.lens[parent];
+        else if (parent >= 0) next[u] = a.table[parent * a.c.table_stride + i];
     }
-    if (names) take_name(a.s, page, names);
     __syncthreads();
+    if (!is_lens) {
+        int32_t sum = 0, add[U], before[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t b = b0 + u;
+            add[u] = before[u] = 0;
+            if ((uint32_t)was[u] < a.c.num_pages) sum += (int32_t)(s_children[b >> 1] >> (b & 1 ? 16 : 0) & 0xffff) - 1;
+            if (u + 1 < U && was[u + 1] == was[u]) continue;
+            add[u] = sum;
+            sum = 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (add[u]) before[u] = atomicAdd(&a.s.refs[was[u]], add[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (add[u] && before[u] + add[u] == 0) atomicAdd(&a.s.free_in[(uint32_t)was[u] / kBlock], 1);
+            else if (add[u] && before[u] == 0) atomicSub(&a.s.free_in[(uint32_t)was[u] / kBlock], 1);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (changed >> u & 1) {
@@ -213,18 +267,11 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t widt
 // resize
 // ---------------------------------------------------------------------------
 
-// A wave per sequence: its entries behind the new length go, those that are
-// missing below it are counted.  Pages are held from a row's start without a
-// gap, so both are looked for from the border, 64 entries a time.
-__global__ __launch_bounds__(kThreads) void k_want(PageArgs a, uint32_t width) {
-    const uint32_t b = blockIdx.x * (kThreads / 64) + threadIdx.x / 64, lane = threadIdx.x & 63;
-    if (b >= a.c.batch) return;
-    int32_t *row = a.table + b * a.c.table_stride;
-    const uint32_t old_len = seq_len(a.c, b, lane == 0 ? a.status : nullptr);
-    const int32_t asked = a.arg[b];
-    const uint32_t new_len = asked < 0 ? 0 : min((uint32_t)asked, a.c.max_len);
-    if (lane == 0 && (int32_t)new_len != asked) report(a.status, SPLITZIP_KV_BAD_LEN);
-    const uint32_t need = pages_for(a.c, new_len);
+// Pages are held from a row's start without a gap, so what a sequence drops and
+// misses is looked for from the border of its new length.  A wave looks at 64
+// entries a time: drops those behind, and returns the first that is missing.
+__device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32_t need, uint32_t width) {
+    const uint32_t lane = threadIdx.x & 63;
     for (uint32_t i0 = need; i0 < width; i0 += 64) {
         const int32_t page = i0 + lane < width ? row[i0 + lane] : -1;
         if (page >= 0) {
@@ -237,25 +284,44 @@ __global__ __launch_bounds__(kThreads) void k_want(PageArgs a, uint32_t width) {
     while (first) {
         const uint32_t n = min(first, 64u), i = first - n + lane;
         const uint64_t held = __ballot(lane < n && row[i] >= 0);
-        if (held) {
-            first = first - n + 64 - __builtin_clzll(held);
-            break;
-        }
+        if (held) return first - n + 64 - __builtin_clzll(held);
         first -= n;
     }
+    return 0;
+}
+
+// Lengths asked for and old, and the page that is begun and will be written,
+// of which the writers are counted.
+__device__ inline Want want_of(const PageArgs &a, uint32_t b, bool tell) {
+    const uint32_t old_len = seq_len(a.c, b, tell ? a.status : nullptr);
+    const int32_t asked = a.arg[b];
+    const uint32_t new_len = asked < 0 ? 0 : min((uint32_t)asked, a.c.max_len);
+    if (tell && (int32_t)new_len != asked) report(a.status, SPLITZIP_KV_BAD_LEN);
+    const uint32_t need = pages_for(a.c, new_len);
+    return Want{need, need, kNoPage, old_len, new_len, 0, 0, 0};
+}
+__device__ inline void begin_writing(const PageArgs &a, uint32_t b, const int32_t *row, Want &w) {
+    const uint32_t at = div(w.old_len, a.c.page);
+    if (w.new_len <= w.old_len || w.old_len == at * a.c.page.d) return;      // else `at` is below need
+    const uint32_t page = (uint32_t)row[at];
+    if (page < a.c.num_pages) {
+        w.page = page;
+        atomicAdd(&a.s.writers[page], 1);
+        atomicMin(&a.s.lowest[page], (int32_t)b);
+    } else {
+        report(a.status, SPLITZIP_KV_BAD_PAGE);
+    }
+}
+
+// A wave per sequence.
+__global__ __launch_bounds__(kThreads) void k_want(PageArgs a, uint32_t width) {
+    const uint32_t b = blockIdx.x * (kThreads / 64) + threadIdx.x / 64, lane = threadIdx.x & 63;
+    if (b >= a.c.batch) return;
+    int32_t *row = a.table + b * a.c.table_stride;
+    Want w = want_of(a, b, lane == 0);
+    w.first = drop_and_find(a, row, w.need, width);
     if (lane == 0) {
-        Want w{first, need, kNoPage, old_len, new_len, 0, 0, 0};
-        const uint32_t at = div(old_len, a.c.page);
-        if (new_len > old_len && old_len != at * a.c.page.d) {       // then `at` is below need
-            const uint32_t page = (uint32_t)row[at];
-            if (page < a.c.num_pages) {
-                w.page = page;
-                atomicAdd(&a.s.writers[page], 1);
-                atomicMin(&a.s.lowest[page], (int32_t)b);
-            } else {
-                report(a.status, SPLITZIP_KV_BAD_PAGE);
-            }
-        }
+        begin_writing(a, b, row, w);
         a.s.want[b] = w;
     }
 }
@@ -274,35 +340,79 @@ __device__ inline uint32_t group_scan(uint32_t x, uint32_t *part, uint32_t &all)
     return upto + (wave ? __builtin_amdgcn_readlane(waves, wave - 1) : 0);
 }
 
+// Counts that this launch's additions changed: past the caches.
+__device__ inline int32_t latest(const int32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
 // One workgroup: how many pages the sequences want, each its place among them,
-// and the first so many free pages, in order.
-__global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t blocks) {
-    __shared__ uint32_t part[64], s_block[kChooseThreads], s_before[kChooseThreads], s_take[kChooseThreads];
+// and the first so many free pages, in order.  WANT: with what k_want does for
+// up to kChooseThreads sequences, a thread each where a sequence drops or
+// misses a page at most (a step's tokens), else a wave.  (64 sequences with 8
+// drafts each, given back and made room for: 15.6 us, with k_want 20.8 to 25.5.)
+template <bool WANT>
+__global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t width, uint32_t blocks) {
+    __shared__ uint32_t part[64], s_block[kChooseThreads], s_before[kChooseThreads], s_take[kChooseThreads], s_slow;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t total = 0;
+    Want mine{};
+    if (WANT) {
+        if (tid == 0) s_slow = 0;
+        __syncthreads();
+        int32_t *row = a.table + tid * a.c.table_stride;
+        bool slow = false;
+        if (tid < a.c.batch) {
+            mine = want_of(a, tid, true);
+            const uint32_t need = mine.need;
+            const int32_t before2 = need > 1 ? row[need - 2] : 0, before1 = need ? row[need - 1] : 0;
+            const int32_t behind1 = need < width ? row[need] : -1, behind2 = need + 1 < width ? row[need + 1] : -1;
+            slow = behind2 >= 0 || (before1 < 0 && before2 < 0);
+            if (slow) {
+                s_take[atomicAdd(&s_slow, 1u)] = tid;
+            } else {
+                if (before1 < 0) mine.first = need - 1;
+                if (behind1 >= 0) {
+                    if ((uint32_t)behind1 < a.c.num_pages) drop_name(a.s, behind1, 1);
+                    row[need] = -1;
+                }
+            }
+        }
+        __syncthreads();
+        for (uint32_t i = wave; i < s_slow; i += kChooseThreads / 64) {
+            const uint32_t b = s_take[i];
+            const uint32_t need = want_of(a, b, false).need;
+            const uint32_t first = drop_and_find(a, a.table + b * a.c.table_stride, need, width);
+            if (lane == 0) s_before[b] = first;
+        }
+        __syncthreads();
+        if (slow) mine.first = s_before[tid];
+        if (tid < a.c.batch) begin_writing(a, tid, row, mine);
+        wait_vector_memory();      // the additions have been made
+        __syncthreads();
+    }
     for (uint32_t b0 = 0; b0 < a.c.batch; b0 += kChooseThreads) {
         const uint32_t b = b0 + tid;
         uint32_t n = 0, copies = 0;
+        Want w{};
         if (b < a.c.batch) {
-            const Want w = a.s.want[b];
+            w = WANT ? mine : a.s.want[b];
             // the sequences that write a page leave it to the first of them, if no other names it
             if (w.page != kNoPage) {
-                const int32_t refs = a.s.refs[w.page];
-                copies = refs > 1 && !(a.s.writers[w.page] == refs && a.s.lowest[w.page] == (int32_t)b);
+                const int32_t refs = latest(&a.s.refs[w.page]);
+                copies = refs > 1 && !(latest(&a.s.writers[w.page]) == refs && latest(&a.s.lowest[w.page]) == (int32_t)b);
             }
             n = w.need - w.first + copies;
         }
         uint32_t all;
         const uint32_t upto = group_scan(n, part, all);
         if (b < a.c.batch) {
-            a.s.want[b].before = total + upto - n;
-            a.s.want[b].copies = copies;
+            w.before = total + upto - n;
+            w.copies = copies;
+            a.s.want[b] = w;
         }
         total += all;
     }
     uint32_t found = 0;
     for (uint32_t k0 = 0; k0 < blocks && found < total; k0 += kChooseThreads) {
-        const uint32_t n = k0 + tid < blocks ? (uint32_t)a.s.free_in[k0 + tid] : 0;
+        const uint32_t n = k0 + tid < blocks ? (uint32_t)latest(&a.s.free_in[k0 + tid]) : 0;
         uint32_t all, used;
         const uint32_t before = found + group_scan(n, part, all) - n;
         const bool here = n && before < total;
@@ -320,7 +430,7 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
 #pragma unroll
             for (uint32_t q = 0; q < kBlock / 64; ++q) {
                 const uint32_t p = p0 + q * 64 + lane;
-                free4[q] = __ballot(p < a.c.num_pages && a.s.refs[p] == 0);
+                free4[q] = __ballot(p < a.c.num_pages && latest(&a.s.refs[p]) == 0);
             }
             uint32_t done = 0;
 #pragma unroll
@@ -380,8 +490,8 @@ __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, 
     }
     if (!copied) return;
     const uint64_t step = pool & 1 ? page_v : page_k;
-    copy_page(pools.p[pool] + w.page * step, pools.p[pool] + copy * step, pool & 1 ? gv : gk,
-              w.old_len - div(w.old_len, a.c.page) * a.c.page.d);
+    copy_page<8>(pools.p[pool] + w.page * step, pools.p[pool] + copy * step, pool & 1 ? gv : gk,
+                 w.old_len - div(w.old_len, a.c.page) * a.c.page.d);
 }
 
 // ---------------------------------------------------------------------------
@@ -627,6 +737,10 @@ int splitzip_kv_pages_count(const splitzip_kv_pages *pages, int32_t *d_status, v
     if (const int rc = prepare(pages, nullptr, d_status, a)) return rc;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const uint32_t width = pages->cache->max_pages, blocks = blocks_of(a.c.num_pages);
+    if (a.c.num_pages <= kSmallPages && (uint64_t)a.c.batch * width <= kSmallEntries) {
+        k_count<<<1, kSmallThreads, 0, s>>>(a, width);
+        return launched();
+    }
     k_clear<<<grid_for(blocks), kThreads, 0, s>>>(a);
     int rc = launched();
     if (!rc && a.c.batch && width) {
@@ -649,14 +763,18 @@ int splitzip_kv_pages_fork(const splitzip_kv_pages *pages, const int32_t *parent
     if (!parents) return SPLITZIP_ERR_INVALID;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const uint32_t width = pages->cache->max_pages, batch = a.c.batch;
-    // rows a thread: four, and as many more as leave a workgroup at least one column
+    // Rows a thread: four, and as many more as leave a workgroup at least one
+    // column; 16 columns, a cache line, as far as that goes.
     const int u = batch <= 4 * kForkThreads ? 4 : batch <= 16 * kForkThreads ? 16 : 64;
-    uint32_t columns = 64;
-    while (columns > 1 && (batch - 1) / u + 1 > kForkThreads / columns) columns >>= 1;
+    const uint32_t ways = (batch - 1) / u + 1;      // threads a column
+    uint32_t columns = 16;
+    while (columns > 1 && ways > kForkThreads / columns) columns >>= 1;
+    uint32_t threads = ways * columns;
+    threads = threads <= 64 ? 64 : (threads + 63) / 64 * 64;
     const uint32_t grid = (width ? (width - 1) / columns + 1 : 0) + 1;
-    if (u == 4) k_fork<4><<<grid, kForkThreads, 0, s>>>(a, width, columns);
-    else if (u == 16) k_fork<16><<<grid, kForkThreads, 0, s>>>(a, width, columns);
-    else k_fork<64><<<grid, kForkThreads, 0, s>>>(a, width, columns);
+    if (u == 4) k_fork<4><<<grid, threads, (batch / 2 + 1) * 4, s>>>(a, width, columns);
+    else if (u == 16) k_fork<16><<<grid, threads, (batch / 2 + 1) * 4, s>>>(a, width, columns);
+    else k_fork<64><<<grid, threads, (batch / 2 + 1) * 4, s>>>(a, width, columns);
     return launched();
 }
 
@@ -666,12 +784,15 @@ int splitzip_kv_pages_resize(const splitzip_kv_pages *pages, const int32_t *lens
     if (a.c.batch == 0) return SPLITZIP_OK;
     if (!lens) return SPLITZIP_ERR_INVALID;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    k_want<<<(a.c.batch - 1) / (kThreads / 64) + 1, kThreads, 0, s>>>(a, pages->cache->max_pages);
-    int rc = launched();
-    if (rc) return rc;
-    k_choose<<<1, kChooseThreads, 0, s>>>(a, blocks_of(a.c.num_pages));
-    rc = launched();
-    if (rc) return rc;
+    const uint32_t width = pages->cache->max_pages, blocks = blocks_of(a.c.num_pages);
+    if (a.c.batch <= kChooseThreads) {
+        k_choose<true><<<1, kChooseThreads, 0, s>>>(a, width, blocks);
+    } else {
+        k_want<<<(a.c.batch - 1) / (kThreads / 64) + 1, kThreads, 0, s>>>(a, width);
+        if (const int rc = launched()) return rc;
+        k_choose<false><<<1, kChooseThreads, 0, s>>>(a, width, blocks);
+    }
+    if (const int rc = launched()) return rc;
     const splitzip_kv_cache *c = pages->cache;
     const Geometry gk = geometry(c, c, false, true), gv = geometry(c, c, true, true);
     return by_layers(pages, [&](uint32_t l0, uint32_t n) {

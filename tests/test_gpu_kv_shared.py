@@ -55,17 +55,19 @@ def check(m, scale=None, hidden=(), want_status=0):
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("dim", [8, 64, 72, 80, 96, 128, 136, 192, 200, 256])
-@pytest.mark.parametrize("group", [1, 5])
+@pytest.mark.parametrize("group", [1, 5, 20])
 def test_dims(dtype, dim, group):
+    """Few query rows a group, and many."""
     _say("shared dim=%d group=%d %s" % (dim, group, dtype))
     check(H.make([(100, [120, 100, 133]), (40, [41, 300])], 2, dim, 16, dtype, 2 * group, seed=dim + group))
 
 
 @pytest.mark.parametrize("common", [0, 1, 15, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500, 1000])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-def test_tokens_in_common(common, dim):
-    _say("shared tokens=%d dim=%d" % (common, dim))
-    check(H.make([(common, [common + 7, common, common + 70])], 2, dim, 16, BF16, 8, seed=common, layout="nhd"))
+@pytest.mark.parametrize("heads", [8, 48])
+def test_tokens_in_common(common, dim, heads):
+    _say("shared tokens=%d dim=%d heads=%d" % (common, dim, heads))
+    check(H.make([(common, [common + 7, common, common + 70])], 2, dim, 16, BF16, heads, seed=common, layout="nhd"))
 
 
 @pytest.mark.parametrize("group", [1, 2, 3, 16, 33, 63, 64, 65, 100, 127, 128, 129, 130, 200, 257])
@@ -89,29 +91,30 @@ def test_pages(page, layout):
     check(H.make([(150, [160, 150, 151]), (3, [5, 9])], 3, 80, page, BF16, 6, seed=page, layout=layout))
 
 
-@pytest.mark.parametrize("groups", [63, 64, 65, 130, 700])
-def test_many_groups(groups):
-    """Several blocks of groups, runs that have several groups."""
+@pytest.mark.parametrize("groups,heads", [(63, 4), (64, 4), (65, 40), (130, 4), (130, 40), (700, 4), (2049, 2)])
+def test_many_groups(groups, heads):
+    """Several blocks of groups, runs that have several groups; more than one workgroup holds."""
     _say("shared in %d groups" % groups)
     rng = random.Random(groups)
     made = []
     for _ in range(groups):
         common = rng.choice([0, 1, 20, 64, 65, 140])
         made.append((common, [common + rng.randrange(1 if i else 0, 9) for i in range(rng.choice([1, 2, 3]))]))
-    check(H.make(made, 2, 64, 16, BF16, 4, seed=groups))
+    check(H.make(made, 2, 64, 16, BF16, heads, seed=groups))
 
 
-def test_members_of_all_kinds():
+@pytest.mark.parametrize("heads", [8, 40])
+def test_members_of_all_kinds(heads):
     """Ended and short sequences, one that ends where the others go on, a group of one and of none,
     tokens in common beyond the first sequence, sequences in no group."""
     _say("shared: members of all kinds")
-    m = H.make([(100, [110, 0, 40, 100, 99, 101]), (50, [80]), (64, [0, 70, 64]), (300, [200, 210, 200])], 2, 128, 16, BF16, 8, seed=3)
+    m = H.make([(100, [110, 0, 40, 100, 99, 101]), (50, [80]), (64, [0, 70, 64]), (300, [200, 210, 200])], 2, 128, 16, BF16, heads, seed=3)
     check(m)
     m.cu, m.shared = [0, 6, 6, 7, 10, 13], [100, 30, 50, 64, 300]
     check(m)
     m.cu, m.shared = [1, 1], [100]
     check(m)
-    m = H.make([(0, [20, 3]), (64, [100, 70]), (0, [9])], 2, 128, 16, BF16, 8, seed=4)
+    m = H.make([(0, [20, 3]), (64, [100, 70]), (0, [9])], 2, 128, 16, BF16, heads, seed=4)
     m.cu, m.shared = [2, 4], [64]                # sequences before and behind the groups
     check(m)
     m.cu, m.shared = [0], []
@@ -127,9 +130,10 @@ def test_nothing_cached():
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0, 1e-3])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
-def test_scales(scale, dtype):
-    _say("shared scale=%g %s" % (scale, dtype))
-    check(H.make([(100, [120, 100])], 2, 128, 16, dtype, 8, seed=9), scale=scale)
+@pytest.mark.parametrize("heads", [8, 40])
+def test_scales(scale, dtype, heads):
+    _say("shared scale=%g %s heads=%d" % (scale, dtype, heads))
+    check(H.make([(100, [120, 100])], 2, 128, 16, dtype, heads, seed=9), scale=scale)
 
 
 def test_long():
@@ -141,10 +145,11 @@ def test_long():
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("dim", [128, 200])
-def test_bad_pages(dtype, dim):
+@pytest.mark.parametrize("heads", [8, 32])
+def test_bad_pages(dtype, dim, heads):
     """Page numbers outside the pool: their tokens are left out, whatever lies where they point."""
     _say("shared: bad pages %s %d" % (dtype, dim))
-    m = H.make([(100, [120, 100, 130]), (64, [64, 70])], 2, dim, 16, dtype, 8, seed=1)
+    m = H.make([(100, [120, 100, 130]), (64, [64, 70])], 2, dim, 16, dtype, heads, seed=1)
     m.table[0, 2] = m.k.shape[0]
     m.table[3, 0] = -1
     m.table[2, 7] = 1 << 30
@@ -152,7 +157,7 @@ def test_bad_pages(dtype, dim):
     hidden |= {(2, t) for t in range(112, 128)}
     check(m, hidden=hidden, want_status=_abi.KV_BAD_PAGE)
     # none of the tokens in common
-    m = H.make([(32, [40, 32, 33])], 2, dim, 16, dtype, 8, seed=2)
+    m = H.make([(32, [40, 32, 33])], 2, dim, 16, dtype, heads, seed=2)
     m.table[0, :2] = -1
     check(m, hidden={(b, t) for b in range(3) for t in range(32)}, want_status=_abi.KV_BAD_PAGE)
 
@@ -168,10 +173,11 @@ def test_ranges_that_decrease():
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
-def test_infinite_values(dtype):
+@pytest.mark.parametrize("members", [3, 20])
+def test_infinite_values(dtype, members):
     """An infinity in V of a token in common comes out as one, under small weights too; a NaN in K makes its rows NaN."""
     _say("shared: infinities %s" % dtype)
-    m = H.make([(100, [120, 100, 130])], 2, 128, 16, dtype, 8, seed=1)
+    m = H.make([(100, [120, 100, 130] + [101] * (members - 3))], 2, 128, 16, dtype, 8, seed=1)
     page = int(m.table[0, 3])
     m.v[page, 1, 5, 7] = float("inf")
     m.v[page, 0, 2, 9] = float("-inf")
@@ -190,7 +196,7 @@ def test_infinite_values(dtype):
                 out[b, h, column] = o[h, column].to(dtype)
                 small += 1
         close(out[b], o, tol, "out %d" % b)
-    assert 0 < small < 24
+    assert 0 < small < 8 * members
     m.k[page, 0, 4, 3] = float("nan")
     R.to_gpu(m, S)
     out = m.cache.attend_shared(m.gq, ints(m.cu), ints(m.shared), S.KVSharedWorkspace(m.cache, 8, 1))
@@ -254,7 +260,7 @@ def same(got, want, what):
 
 def test_streams_and_graphs():
     _say("shared: two streams, two graphs")
-    steps = [Step(1, [(300, [310, 300, 333]), (40, [50, 41])]), Step(2, [(1000, [1100] * 9)])]
+    steps = [Step(1, [(300, [310, 300, 333]), (40, [50, 41])]), Step(2, [(1000, [1100] * 30)])]
     streams = [torch.cuda.Stream() for _ in steps]
     graphs = []
     for s in steps:
