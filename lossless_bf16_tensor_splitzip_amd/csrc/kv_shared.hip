@@ -19,12 +19,13 @@
 
 namespace {
 
-constexpr uint32_t kRows = 128;        // query rows a workgroup of k_shared takes: 32 a wave
+constexpr int kNT = 2;
+constexpr uint32_t kRows = 64 * kNT;   // query rows a workgroup of k_shared takes
 constexpr int kSharedThreads = 256;
 constexpr uint32_t kSharedRuns = 512;
 constexpr uint32_t kGroupsHere = 2048; // groups that k_both holds in LDS
 
-// Tokens a tile of K or V has, 16 KB of it or less.
+// Tokens that k_shared's workgroups take at a time: 16 KB of K and of V, or less.
 constexpr int tile_tokens(int dp) { return dp <= 128 ? 64 : 32; }
 
 // How query rows are put together: sequences a row tile has, and row tiles a
@@ -313,6 +314,34 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
 // many query rows
 // ---------------------------------------------------------------------------
 
+// 16 or 4 bytes a lane from memory into LDS, the lanes' one after another from
+// `to` on, without registers.  The compiler does not know of these: what waits
+// for them is written out (until_loads), and the loop that has them under way
+// has no other loads from memory.  (M0 holds the place in LDS, and is read one
+// state after it is written.)
+__device__ inline uint32_t lds_place(const void *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+__device__ inline void load_to_lds16(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+__device__ inline void load_to_lds4(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+}
+__device__ inline void until_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
+// Until all waves of the workgroup are here and their LDS stores have been
+// made; loads from memory stay under way.
+__device__ inline void meet() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // The work -- all row tiles of all groups in tiles of T tokens, for every KV
 // head -- is cut into equal runs, one a workgroup.  A workgroup's four waves
 // have 32 query rows each and meet the same tokens, which are staged in LDS:
@@ -324,14 +353,13 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
 // as much again.  The error, half a step of the type for each weight, is as
 // large as that of rounding the output where V has no mean (1.4 times that
 // error together), and smaller where it has.
-template <bool BF16, int DP, bool EXACT>
-__global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(SharedArgs a) {
-    constexpr int T = tile_tokens(DP);
+template <bool BF16, int DP, int NT, bool EXACT>
+__global__ __launch_bounds__(kSharedThreads, NT * DP <= 256 ? 2 : 1) void k_shared(SharedArgs a) {
+    constexpr int T = tile_tokens(DP), ST = T / 16;
     constexpr int KS = DP / 32;              // steps of the K product
     constexpr int P16 = DP / 128, P8 = (DP % 128) / 64, VC = DP / 16;      // as in k_attend
     constexpr int PR = DP / 8;               // 16-byte pieces of a row
     constexpr int NP = T * PR / kSharedThreads;      // pieces a thread stages of K, of V
-    constexpr int ST = T / 16;
     // fp16 weights are held times 2^11, up to 2^4 above what the maximum of before
     // allows: no more than 2^15, and steps of 2^-35 of the largest or less.
     constexpr float kSlack = 4.f, kLift = BF16 ? 0.f : 11.f;
@@ -341,8 +369,10 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
     auto spot = [](uint32_t row, uint32_t piece) {
         return row * PR + (DP % 128 == 0 ? piece ^ (row & 15) : piece ^ (row >> 1 & 7));
     };
-    __shared__ u32x4 s_k[2][T * PR], s_v[2][T * PR];
-    __shared__ uint64_t off_k[4][T], off_v[4][T], s_valid[4];      // of tiles, in turn
+    __shared__ u32x4 s_k[2][T * PR], s_v[2][T * PR];      // two tiles, in turn
+    __shared__ uint64_t off_k[4][T], off_v[4][T];         // of four tiles: rows' places, bytes
+    __shared__ uint64_t s_valid[4];                       // which of their tokens are there
+    __shared__ uint32_t s_page[4][64];                    // page numbers
     uint32_t *s_block = (uint32_t *)s_k;
     static_assert(sizeof s_k >= 4 * kMaxBlocks, "sums of all blocks");
     const uint32_t tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
@@ -351,11 +381,9 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
     // Logits are compared before they are scaled: a negative scale is the queries'.
     const uint32_t negate = a.scale2 < 0.f ? 0x80008000u : 0;
     const float scale2 = fabsf(a.scale2);
-    // This lane's places in a tile: where it puts its pieces, and what it reads
-    // of the first 16 rows (further ones are a constant away).
-    uint32_t put[NP], k_at[KS], v_at[4], v8_at[4];
-#pragma unroll
-    for (int k = 0; k < NP; ++k) put[k] = spot((tid + k * kSharedThreads) / PR, (tid + k * kSharedThreads) % PR);
+    // This lane's places in a tile, of the first 16 rows (further ones are a
+    // constant away).
+    uint32_t k_at[KS], v_at[4], v8_at[4];
 #pragma unroll
     for (int j = 0; j < KS; ++j) k_at[j] = spot(c16, j * 4 + g);
 #pragma unroll
@@ -418,6 +446,11 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
         load_groups<T>(a, first, carry, blk, nullptr);
     }
 
+    if (!EXACT) {       // columns behind head_dim
+        __syncthreads();
+        for (uint32_t i = tid; i < 2 * T * PR; i += kSharedThreads) s_k[0][i] = s_v[0][i] = u32x4{0, 0, 0, 0};
+    }
+
     for (uint32_t u = u_begin; u < u_end;) {
         uint64_t past;
         while (!(past = __ballot(blk.upto * kvh > u))) {
@@ -430,10 +463,10 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
         const uint32_t rows = p.rows, end = min(p.len, (p.unit0 + p.count) * T);
         const int32_t *table = a.c.table + p.first * a.c.table_stride;
 
-        u32x4 q[2][KS];
+        u32x4 q[NT][KS];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t r = wave * 32 + t * 16 + c16;
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t r = (wave * NT + t) * 16 + c16;
             uint32_t b = 0, head = 0;
             if (r < rows) locate_row(a, p, r, b, head);
 #pragma unroll
@@ -443,174 +476,185 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 192 ? 2 : 1) void k_shared(Sh
                 if (r < rows && (EXACT || d < D)) q[t][j] = *(const u32x4 *)(a.q + b * a.qs[0] + head * a.qs[1] + d) ^ negate;
             }
         }
-        f32x4 o[2][VC];
-        float m[2], l[2];
+        f32x4 o[NT][VC];
+        float m[NT], l[NT];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t) {
             m[t] = -INFINITY;
             l[t] = 0.f;
 #pragma unroll
             for (int j = 0; j < VC; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        // Staging: this thread's pieces of a tile.  A row's place is found by one
-        // lane, two tiles ahead (the waves take turns), from a page number loaded
-        // a tile before; the pieces' threads take it from LDS.
-        const uint16_t *k_head = a.c.k + p.h * a.c.ks[1], *v_head = a.c.v + p.h * a.c.vs[1];
-        u32x4 kx[NP], vx[NP];
-        auto row_of = [&](int k) { return (tid + k * kSharedThreads) / PR; };
-        auto piece_of = [&](int k) { return (tid + k * kSharedThreads) % PR; };
+        // Tile n's K and V are loaded a tile ahead.  A row's place is found by one
+        // lane, three tiles ahead (the waves take turns), from a page number loaded
+        // a tile before, and taken to the registers of the threads that load the
+        // row's pieces a tile later.
+        const uint8_t *k_head = (const uint8_t *)(a.c.k + p.h * a.c.ks[1]), *v_head = (const uint8_t *)(a.c.v + p.h * a.c.vs[1]);
         const uint32_t tile0 = p.unit0, tile_end = (end - 1) / T + 1;
-        auto page_at = [&](uint32_t n) {
+        auto load_pages = [&](uint32_t n) {
             const uint32_t t = n * T + lane;
-            return lane < T && t < end ? (uint32_t)table[div(t, a.c.page)] : 0xffffffffu;
+            const uint32_t to = lds_place(s_page[n & 3]);
+            if (lane < T && t < end) load_to_lds4(table + div(t, a.c.page), to);
         };
-        auto place = [&](uint32_t n, uint32_t page) {
-            const uint32_t t = n * T + lane;
+        auto place = [&](uint32_t n) {
+            const uint32_t t = n * T + lane, page = s_page[n & 3][lane];
             const bool in = lane < T && t < end, ok = in && page < a.c.num_pages;
             if (in && !ok) report(a.status, SPLITZIP_KV_BAD_PAGE);
             const uint32_t slot = t - div(t, a.c.page) * a.c.page.d;
-            if (lane < T) {
-                off_k[n & 3][lane] = ok ? page * a.c.ks[0] + slot * a.c.ks[2] : 0;
-                off_v[n & 3][lane] = ok ? page * a.c.vs[0] + slot * a.c.vs[2] : 0;
+            if (lane < T) {      // a token that is not there: the pool's first, stored over with zeros
+                off_k[n & 3][lane] = ok ? 2 * (page * a.c.ks[0] + slot * a.c.ks[2]) : 0;
+                off_v[n & 3][lane] = ok ? 2 * (page * a.c.vs[0] + slot * a.c.vs[2]) : 0;
             }
             const uint64_t mask = __ballot(ok);
             if (lane == 0) s_valid[n & 3] = mask;
         };
-        auto valid_of = [&](uint32_t n) {
-            const uint64_t x = s_valid[n & 3];
+        auto missing_of = [&](uint32_t n) {      // its tokens that are not there
+            const uint64_t x = ~s_valid[n & 3] << (64 - T) >> (64 - T);
             return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
                    (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
         };
-        auto fetch = [&](uint32_t n) {
-            const uint64_t valid = valid_of(n);
+        // Piece k of this thread: its place in the tile is tid + 256 k, and what belongs there.
+        auto row_of = [&](int k) { return (tid + k * kSharedThreads) / PR; };
+        auto piece_of = [&](int k) {
+            const uint32_t row = row_of(k);
+            return spot(row, (tid + k * kSharedThreads) % PR) - row * PR;
+        };
+        auto load_tile = [&](uint32_t n) {
+            const uint32_t to_k = lds_place(s_k[n & 1]) + wave * 1024, to_v = lds_place(s_v[n & 1]) + wave * 1024;
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const uint32_t row = row_of(k), piece = piece_of(k);
-                kx[k] = vx[k] = u32x4{0, 0, 0, 0};
-                if (!(valid >> row & 1) || (!EXACT && piece * 8 >= D)) continue;
-                kx[k] = *(const u32x4 *)(k_head + off_k[n & 3][row] + piece * 8);
-                vx[k] = *(const u32x4 *)(v_head + off_v[n & 3][row] + piece * 8);
+                const uint32_t piece = piece_of(k);
+                if (!EXACT && piece * 8 >= D) continue;      // zeros since the start
+                load_to_lds16(k_head + off_k[n & 3][row_of(k)] + piece * 16, to_k + k * kSharedThreads * 16);
+                load_to_lds16(v_head + off_v[n & 3][row_of(k)] + piece * 16, to_v + k * kSharedThreads * 16);
             }
         };
+        auto clear_rows = [&](uint32_t n, uint64_t missing) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                if (missing >> row_of(k) & 1) s_k[n & 1][tid + k * kSharedThreads] = s_v[n & 1][tid + k * kSharedThreads] = u32x4{0, 0, 0, 0};
+        };
+        const bool active = wave * (16 * NT) < rows;
 
         __syncthreads();        // the piece of work before, and the sums of blocks, have been read
-        const uint32_t turn = (wave - tile0) & 3;      // of the first four tiles this one is this wave's
-        uint32_t page = page_at(tile0 + turn);
-        if (turn < 2) {
-            place(tile0 + turn, page);
-            page = page_at(tile0 + turn + 4);
-        }
+        load_pages(tile0 + wave);
         note_shares(a, p, cut, u, late, true, true);
-        __syncthreads();
-        fetch(tile0);
+        until_loads();
+        if (wave < 3) place(tile0 + wave);
+        meet();
+        uint64_t missing = missing_of(tile0);
+        load_tile(tile0);
         for (uint32_t n = tile0; n < tile_end; ++n) {
-            u32x4 *const now_k = s_k[n & 1], *const now_v = s_v[n & 1];
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                now_k[put[k]] = kx[k];
-                now_v[put[k]] = vx[k];
+            until_loads();
+            if (missing) clear_rows(n, missing);
+            meet();
+            if (n + 1 < tile_end) load_tile(n + 1);
+            if (((n - tile0) & 3) == wave) {
+                if (n + 3 < tile_end) place(n + 3);
+                if (n + 4 < tile_end) load_pages(n + 4);
             }
-            if (((n + 2) & 3) == wave) {
-                place(n + 2, page);
-                page = page_at(n + 6);
-            }
-            __syncthreads();
-            if (n + 1 < tile_end) fetch(n + 1);
-            if (wave * 32 >= rows) continue;
-            f32x4 x[2][ST];
+            const uint64_t here = missing;
+            if (active) {
+                const u32x4 *const now_k = s_k[n & 1], *const now_v = s_v[n & 1];
+                f32x4 x[NT][ST];
 #pragma unroll
-            for (int s = 0; s < ST; ++s) {
-                x[0][s] = x[1][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < ST; ++s) {
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    const u32x4 y = now_k[k_at[j] + s * 16 * PR];
-                    x[0][s] = mfma<BF16>(y, q[0][j], x[0][s]);
-                    x[1][s] = mfma<BF16>(y, q[1][j], x[1][s]);
+                    for (int t = 0; t < NT; ++t) x[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        const u32x4 y = now_k[k_at[j] + s * 16 * PR];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) x[t][s] = mfma<BF16>(y, q[t][j], x[t][s]);
+                    }
                 }
-            }
-            const uint64_t valid = valid_of(n);
-            if (~valid << (64 - T)) {       // the last tile's end, or a page number outside the pool
-                const uint64_t mine = valid >> (g * 4);
+                if (here) {       // the last tile's end, or a page number outside the pool
+                    const uint64_t mine = here >> (g * 4);
 #pragma unroll
-                for (int s = 0; s < ST; ++s)
+                    for (int s = 0; s < ST; ++s)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!(mine >> (s * 16 + i) & 1)) x[0][s][i] = x[1][s][i] = -INFINITY;
-            }
-            u32x4 w16[2][ST / 2];
+                        for (int i = 0; i < 4; ++i)
+                            if (mine >> (s * 16 + i) & 1)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int s = 0; s < ST; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][s][i]);
-                top = row_reduce<true>(top) * scale2 - kLift;
+                                for (int t = 0; t < NT; ++t) x[t][s][i] = -INFINITY;
+                }
                 // The sums are rescaled only where weights would pass 2^(kLift + kSlack):
                 // rarely, after a run's first tiles.
-                if (__any(top > m[t] + kSlack)) {
-                    const float m_new = fmaxf(m[t], top), r = __builtin_amdgcn_exp2f(m[t] - (m_new == -INFINITY ? 0.f : m_new));
-                    l[t] *= r;
+                float top[NT];
+                bool far = false;
 #pragma unroll
-                    for (int j = 0; j < VC; ++j) o[t][j] *= r;
-                    m[t] = m_new;
+                for (int t = 0; t < NT; ++t) {
+                    top[t] = -INFINITY;
+#pragma unroll
+                    for (int s = 0; s < ST; ++s)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[t] = fmaxf(top[t], x[t][s][i]);
+                    far = far || top[t] * scale2 > m[t] + (kLift + kSlack);
                 }
-                const float use = m[t] == -INFINITY ? 0.f : m[t];
+                if (__any(far)) {
 #pragma unroll
-                for (int s = 0; s < ST; ++s)
+                    for (int t = 0; t < NT; ++t) {
+                        const float m_new = fmaxf(m[t], row_reduce<true>(top[t]) * scale2 - kLift);
+                        const float r = __builtin_amdgcn_exp2f(m[t] - (m_new == -INFINITY ? 0.f : m_new));
+                        l[t] *= r;
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], scale2, -use));
-                        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], scale2, -use));
-                        l[t] += p0 + p1;
-                        w16[t][s >> 1][(s & 1) * 2 + i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
+                        for (int j = 0; j < VC; ++j) o[t][j] *= r;
+                        m[t] = m_new;
                     }
-            }
-            // 32 tokens a time: the lane's 8 tokens' pieces, halves of words exchanged
+                }
+                u32x4 w[NT][ST / 2];
 #pragma unroll
-            for (int s = 0; s < ST / 2; ++s) {
+                for (int t = 0; t < NT; ++t) {
+                    const float use = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
-                for (int w0 = 0; w0 < P16; ++w0) {
-                    u32x4 v[8];
+                    for (int s = 0; s < ST; ++s)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = now_v[v_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR + w0 * 16];
+                        for (int i = 0; i < 4; i += 2) {
+                            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i], scale2, -use));
+                            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][s][i + 1], scale2, -use));
+                            l[t] += p0 + p1;
+                            w[t][s >> 1][(s & 1) * 2 + i / 2] = pack2<BF16>(at_least(p0), at_least(p1));
+                        }
+                }
+                // 32 tokens a time: the lane's 8 tokens' pieces, halves of words exchanged
+                auto add_columns = [&](int s, int c0, const auto &v, int words) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
+                    for (int k = 0; k < words; ++k)
 #pragma unroll
                         for (int odd = 0; odd < 2; ++odd) {
                             u32x4 col;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                col[i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], odd ? 0x07060302u : 0x05040100u);
-                            o[0][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[0][s], o[0][w0 * 8 + 2 * w + odd]);
-                            o[1][w0 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[1][s], o[1][w0 * 8 + 2 * w + odd]);
+                                col[i] = __builtin_amdgcn_perm(v[2 * i + 1][k], v[2 * i][k], odd ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) o[t][c0 + 2 * k + odd] = mfma<BF16>(col, w[t][s], o[t][c0 + 2 * k + odd]);
                         }
-                }
-                if constexpr (P8 > 0) {
-                    u32x2 v[8];
+                };
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = ((const u32x2 *)now_v)[v8_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR * 2];
+                for (int s = 0; s < ST / 2; ++s) {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w)
+                    for (int w0 = 0; w0 < P16; ++w0) {
+                        u32x4 v[8];
 #pragma unroll
-                        for (int odd = 0; odd < 2; ++odd) {
-                            u32x4 col;
+                        for (int i = 0; i < 8; ++i) v[i] = now_v[v_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR + w0 * 16];
+                        add_columns(s, w0 * 8, v, 4);
+                    }
+                    if constexpr (P8 > 0) {
+                        u32x2 v[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                col[i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], odd ? 0x07060302u : 0x05040100u);
-                            o[0][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[0][s], o[0][P16 * 8 + 2 * w + odd]);
-                            o[1][P16 * 8 + 2 * w + odd] = mfma<BF16>(col, w16[1][s], o[1][P16 * 8 + 2 * w + odd]);
-                        }
+                        for (int i = 0; i < 8; ++i) v[i] = ((const u32x2 *)now_v)[v8_at[i & 3] + (s * 32 + (i >> 2) * 16) * PR * 2];
+                        add_columns(s, P16 * 8, v, 2);
+                    }
                 }
             }
+            missing = missing_of(n + 1);
         }
 
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NT; ++t) {
             l[t] = row_reduce<false>(l[t]);
-            const uint32_t r = wave * 32 + t * 16 + c16;
+            const uint32_t r = (wave * NT + t) * 16 + c16;
             if (r >= rows) continue;
             const uint64_t row = share_row(a, p, r, late, true);
             float *to = a.o + row * D;
@@ -746,12 +790,11 @@ bool lay_out(const splitzip_kv_cache *c, uint32_t heads, bool many, uint32_t mos
     p.alone.rows = p.alone.parts == 1 ? group : p.alone.rows;
     p.of = tiling(group, many ? kRows : most);
     const uint64_t all = (uint64_t)c->max_pages * c->page_size;
-    const uint32_t tokens = tile_tokens((c->head_dim + 63) / 64 * 64);
     const uint64_t tiles = (uint64_t)batch * p.of.parts * c->kv_heads;      // of groups, at most
     const uint64_t both = (all / kUnit + 1) * ((many ? 0 : tiles) + (uint64_t)batch * p.alone.parts * c->kv_heads);
-    const uint64_t shared = many ? (all / tokens + 1) * tiles : 0;
+    const uint64_t shared = many ? (all / tile_tokens((int)c->head_dim) + 1) * tiles : 0;
     if (both >> 31 || shared >> 31) return false;
-    const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim <= 192 ? kSharedRuns : kSharedRuns / 2;
+    const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim * kNT <= 256 ? kSharedRuns : kSharedRuns / 2;
     p.both_runs = both < runs ? (uint32_t)both : runs;
     p.shared_runs = shared < more ? (uint32_t)shared : more;
     p.slot_rows = p.of.rows > p.alone.rows ? p.of.rows : p.alone.rows;
@@ -808,8 +851,8 @@ template <bool BF16>
 void launch_shared(const SharedArgs &a, uint32_t grid, hipStream_t s) {
     auto go = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
-        if (a.c.dim == DP) k_shared<BF16, DP, true><<<grid, kSharedThreads, 0, s>>>(a);
-        else k_shared<BF16, DP, false><<<grid, kSharedThreads, 0, s>>>(a);
+        if (a.c.dim == DP) k_shared<BF16, DP, kNT, true><<<grid, kSharedThreads, 0, s>>>(a);
+        else k_shared<BF16, DP, kNT, false><<<grid, kSharedThreads, 0, s>>>(a);
     };
     if (a.c.dim <= 64) go(std::integral_constant<int, 64>{});
     else if (a.c.dim <= 128) go(std::integral_constant<int, 128>{});
