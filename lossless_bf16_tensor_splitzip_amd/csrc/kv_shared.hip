@@ -19,8 +19,17 @@
 
 namespace {
 
+constexpr int kSharedWaves = 4, kSharedThreads = 64 * kSharedWaves;
+constexpr uint32_t kRows = 32 * kSharedWaves;      // query rows a workgroup of k_shared takes
+// Runs of k_shared: as many as are resident.  One writes up to 128 rows of
+// shares of every row tile that it has part of, which few tokens do not repay
+// (8 KV heads of 128, 128 query rows each, us with runs of at least 1, 2, 4 and 8
+// tiles: 1024 tokens 26, 25, 27 and 33, 4096 39, 33, 32 and 36, 12000 48, 49, 40
+// and 44).
 constexpr uint32_t kSharedRuns = 512;
 constexpr uint32_t kGroupsHere = 2048; // groups that k_both holds in LDS
+
+constexpr uint32_t kLeast = 4;         // tiles of a run, at least
 
 // Tokens that k_shared's workgroups take at a time: 16 KB of K and of V, or less.
 constexpr int tile_tokens(int dp) { return dp <= 128 ? 64 : 32; }
@@ -350,15 +359,14 @@ __device__ inline void meet() {
 // as much again.  The error, half a step of the type for each weight, is as
 // large as that of rounding the output where V has no mean (1.4 times that
 // error together), and smaller where it has.
-template <bool BF16, int DP, int W, bool EXACT>
-__global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs a) {
+template <bool BF16, int DP, bool EXACT>
+__global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(SharedArgs a) {
     constexpr int NT = 2;                    // blocks of 16 query rows a wave has
-    constexpr int kThreads = 64 * W;
     constexpr int T = tile_tokens(DP), ST = T / 16;
     constexpr int KS = DP / 32;              // steps of the K product
     constexpr int P16 = DP / 128, P8 = (DP % 128) / 64, VC = DP / 16;      // as in k_attend
     constexpr int PR = DP / 8;               // 16-byte pieces of a row
-    constexpr int NP = T * PR / kThreads;      // pieces a thread stages of K, of V
+    constexpr int NP = T * PR / kSharedThreads;      // pieces a thread stages of K, of V
     // fp16 weights are held times 2^11, up to 2^4 above what the maximum of before
     // allows: no more than 2^15, and steps of 2^-35 of the largest or less.
     constexpr float kSlack = 4.f, kLift = BF16 ? 0.f : 11.f;
@@ -392,7 +400,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
     }
 
     if (blockIdx.x >= a.runs) {      // what every sequence has in common with its group
-        const uint32_t b = (blockIdx.x - a.runs) * kThreads + tid;
+        const uint32_t b = (blockIdx.x - a.runs) * kSharedThreads + tid;
         if (b >= a.c.batch) return;
         uint32_t lo = 0, hi = a.groups;      // the last group that begins at b or before
         while (lo < hi) {
@@ -417,7 +425,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
         load_groups<T>(a, 0, 0, blk, status0);
         total = blk.total;
     } else {
-        for (uint32_t i = wave; i < blocks; i += W) {
+        for (uint32_t i = wave; i < blocks; i += kSharedWaves) {
             Block64Groups one;
             load_groups<T>(a, i * 64, 0, one, status0);
             if (lane == 63) s_block[i] = one.total;
@@ -426,9 +434,10 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
         for (uint32_t f = 0; f < blocks; f += 64)
             total += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
     }
-    const Cut cut = cut_of(total * kvh, a.by_runs);
+    const uint32_t units = total * kvh;
+    const Cut cut = units < kLeast * a.runs ? Cut{units, (units + kLeast - 1) / kLeast, kLeast, 0} : cut_of(units, a.by_runs);
     if (blockIdx.x >= cut.runs) return;
-    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = cut.begin(blockIdx.x + 1);
+    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = min(units, cut.begin(blockIdx.x + 1));
     if (blocks > 1) {
         uint32_t first = 0, carry = 0;
         for (uint32_t f = 0; f < blocks; f += 64) {
@@ -447,7 +456,7 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
 
     if (!EXACT) {       // columns behind head_dim
         __syncthreads();
-        for (uint32_t i = tid; i < 2 * T * PR; i += kThreads) s_k[0][i] = s_v[0][i] = u32x4{0, 0, 0, 0};
+        for (uint32_t i = tid; i < 2 * T * PR; i += kSharedThreads) s_k[0][i] = s_v[0][i] = u32x4{0, 0, 0, 0};
     }
 
     for (uint32_t u = u_begin; u < u_end;) {
@@ -514,10 +523,10 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
                    (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
         };
         // Piece k of this thread: its place in the tile is tid + 256 k, and what belongs there.
-        auto row_of = [&](int k) { return (tid + k * kThreads) / PR; };
+        auto row_of = [&](int k) { return (tid + k * kSharedThreads) / PR; };
         auto piece_of = [&](int k) {
             const uint32_t row = row_of(k);
-            return spot(row, (tid + k * kThreads) % PR) - row * PR;
+            return spot(row, (tid + k * kSharedThreads) % PR) - row * PR;
         };
         auto load_tile = [&](uint32_t n) {
             const uint32_t to_k = lds_place(s_k[n & 1]) + wave * 1024, to_v = lds_place(s_v[n & 1]) + wave * 1024;
@@ -531,19 +540,19 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
             for (int k = 0; k < NP; ++k) {
                 const uint32_t piece = piece_of(k);
                 if (!EXACT && piece * 8 >= D) continue;      // zeros since the start
-                load_to_lds16(k_head + from_k[k] + piece * 16, to_k + k * kThreads * 16);
-                load_to_lds16(v_head + from_v[k] + piece * 16, to_v + k * kThreads * 16);
+                load_to_lds16(k_head + from_k[k] + piece * 16, to_k + k * kSharedThreads * 16);
+                load_to_lds16(v_head + from_v[k] + piece * 16, to_v + k * kSharedThreads * 16);
             }
         };
         auto clear_rows = [&](uint32_t n, uint64_t missing) {
 #pragma unroll
             for (int k = 0; k < NP; ++k)
-                if (missing >> row_of(k) & 1) s_k[n & 1][tid + k * kThreads] = s_v[n & 1][tid + k * kThreads] = u32x4{0, 0, 0, 0};
+                if (missing >> row_of(k) & 1) s_k[n & 1][tid + k * kSharedThreads] = s_v[n & 1][tid + k * kSharedThreads] = u32x4{0, 0, 0, 0};
         };
         const bool active = wave * (16 * NT) < rows;
 
         __syncthreads();        // the piece of work before, and the sums of blocks, have been read
-        if (wave < 4) load_pages(tile0 + wave);
+        load_pages(tile0 + wave);
         note_shares(a, p, cut, u, late, true, true);
         until_loads();
         if (wave < 3) place(tile0 + wave);
@@ -555,8 +564,8 @@ __global__ __launch_bounds__(64 * W, DP <= 128 ? 2 : 1) void k_shared(SharedArgs
             if (missing) clear_rows(n, missing);
             meet();
             if (n + 1 < tile_end) load_tile(n + 1);
-            if (((n - tile0) & (W - 1)) == wave && n + 3 < tile_end) place(n + 3);
-            if (((n - tile0 + 1) & (W - 1)) == wave && n + 4 < tile_end) load_pages(n + 4);
+            if (((n - tile0) & (kSharedWaves - 1)) == wave && n + 3 < tile_end) place(n + 3);
+            if (((n - tile0 + 1) & (kSharedWaves - 1)) == wave && n + 4 < tile_end) load_pages(n + 4);
             const uint64_t here = missing;
             if (active) {
                 const u32x4 *const now_k = s_k[n & 1], *const now_v = s_v[n & 1];
@@ -769,7 +778,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
 // ---------------------------------------------------------------------------
 
 struct SharedPlan {
-    uint32_t group, blocks, many, both_runs, shared_runs;     // blocks of 16 rows in k_both; query rows of k_shared, or 0
+    uint32_t group, blocks, both_runs, shared_runs;     // blocks of 16 rows in k_both; shared_runs 0: no k_shared
     Tiling of, alone;
     uint32_t of_slots, of_whole, both_slots, alone_whole, rows, slot_rows;
     size_t from_at, of_notes_at, alone_notes_at, ml_at, o_at, bytes;
@@ -783,23 +792,21 @@ Tiling tiling(uint32_t group, uint32_t most) {
     return t;
 }
 
-// many: query rows a workgroup of k_shared takes (0: without it); most: of
-// k_both.
-bool lay_out(const splitzip_kv_cache *c, uint32_t heads, uint32_t many, uint32_t most, SharedPlan &p) {
+// many: with k_shared; most: query rows a workgroup of k_both takes.
+bool lay_out(const splitzip_kv_cache *c, uint32_t heads, bool many, uint32_t most, SharedPlan &p) {
     const uint32_t group = heads / c->kv_heads, batch = c->batch;
     p.group = group;
-    p.many = many;
     p.blocks = most / 16;
     p.alone = tiling(group, most);
     p.alone.members = 1;
     p.alone.rows = p.alone.parts == 1 ? group : p.alone.rows;
-    p.of = tiling(group, many ? many : most);
+    p.of = tiling(group, many ? kRows : most);
     const uint64_t all = (uint64_t)c->max_pages * c->page_size;
     const uint64_t tiles = (uint64_t)batch * p.of.parts * c->kv_heads;      // of groups, at most
     const uint64_t both = (all / kUnit + 1) * ((many ? 0 : tiles) + (uint64_t)batch * p.alone.parts * c->kv_heads);
     const uint64_t shared = many ? (all / tile_tokens((int)c->head_dim) + 1) * tiles : 0;
     if (both >> 31 || shared >> 31) return false;
-    const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim <= 128 && many == 128 ? kSharedRuns : kSharedRuns / 2;
+    const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim <= 128 ? kSharedRuns : kSharedRuns / 2;
     p.both_runs = both < runs ? (uint32_t)both : runs;
     p.shared_runs = shared < more ? (uint32_t)shared : more;
     p.slot_rows = p.of.rows > p.alone.rows ? p.of.rows : p.alone.rows;
@@ -826,12 +833,22 @@ bool shape_fits(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups) {
     return groups <= SPLITZIP_KV_MAX_BATCH && heads && heads <= SPLITZIP_KV_MAX_HEADS && heads % c->kv_heads == 0;
 }
 
-// By the query rows of a group of average size; the sizes are on the device.
+// Which kernel has the tokens in common.  k_both reads them again for every 32
+// query rows, k_shared for every 128, with another launch and larger shares.  By
+// what k_both would read, with groups of average size and of all tokens that the
+// table holds (sizes and lengths are on the device).  One group, us, k_both and
+// k_shared: 8 KV heads of 128, 32 query rows a KV head, 4096 tokens (17 MB) 18
+// and 25, 32768 (134 MB) 52 and 41; 64 rows, 4096 (34 MB) 25 and 28; 128 rows,
+// 1024 (17 MB) 21 and 27, 4096 (67 MB) 36 and 32; 512 rows, 512 (34 MB) 50 and
+// 48, 32768 (2.1 GB) 723 and 120.  2 KV heads of 256: 256 rows, 4096 (67 MB) 39
+// and 45; 512 rows, 4096 (134 MB) 49 and 51; 1024 rows, 4096 (268 MB) 97 and 60;
+// 64 rows, 32768 (134 MB) 51 and 54; 128 rows (268 MB) 85 and 62.
 bool shared_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups, SharedPlan &p) {
     if (!shape_fits(c, heads, groups)) return false;
     const uint32_t group = heads / c->kv_heads;
     const uint64_t average = groups ? (uint64_t)c->batch * group / groups : 0;
-    const uint32_t many = !groups || (average <= 32 && groups <= kGroupsHere) ? 0 : average > 128 && c->head_dim <= 128 ? 256 : 128;
+    const double read = 4.0 * c->max_pages * c->page_size * c->kv_heads * c->head_dim * groups * (double)((average + 31) / 32);
+    const bool many = groups > kGroupsHere || (average > 16 && read > (c->head_dim <= 128 ? 56e6 : 160e6));
     return lay_out(c, heads, many, group <= 16 && (many || average <= 16) ? 16 : 32, p);
 }
 
@@ -853,21 +870,17 @@ void launch_both(const SharedArgs &a, uint32_t blocks, hipStream_t s) {
 }
 
 template <bool BF16>
-void launch_shared(const SharedArgs &a, uint32_t rows, hipStream_t s) {
-    const uint32_t infos = (a.c.batch - 1) / (2 * rows) + 1;      // 2 rows threads each
-    auto go = [&](auto dp, auto w) {
-        constexpr int DP = decltype(dp)::value, W = decltype(w)::value;
-        if (a.c.dim == DP) k_shared<BF16, DP, W, true><<<a.runs + infos, 64 * W, 0, s>>>(a);
-        else k_shared<BF16, DP, W, false><<<a.runs + infos, 64 * W, 0, s>>>(a);
+void launch_shared(const SharedArgs &a, hipStream_t s) {
+    const uint32_t grid = a.runs + (a.c.batch - 1) / kSharedThreads + 1;
+    auto go = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        if (a.c.dim == DP) k_shared<BF16, DP, true><<<grid, kSharedThreads, 0, s>>>(a);
+        else k_shared<BF16, DP, false><<<grid, kSharedThreads, 0, s>>>(a);
     };
-    auto with = [&](auto dp) {
-        if (rows == 256) go(dp, std::integral_constant<int, 8>{});
-        else go(dp, std::integral_constant<int, 4>{});
-    };
-    if (a.c.dim <= 64) with(std::integral_constant<int, 64>{});
-    else if (a.c.dim <= 128) with(std::integral_constant<int, 128>{});
-    else if (a.c.dim <= 192) go(std::integral_constant<int, 192>{}, std::integral_constant<int, 4>{});
-    else go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    if (a.c.dim <= 64) go(std::integral_constant<int, 64>{});
+    else if (a.c.dim <= 128) go(std::integral_constant<int, 128>{});
+    else if (a.c.dim <= 192) go(std::integral_constant<int, 192>{});
+    else go(std::integral_constant<int, 256>{});
 }
 
 }  // namespace
@@ -879,9 +892,9 @@ size_t splitzip_kv_groups_struct_size(void) { return sizeof(splitzip_kv_groups);
 size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t groups) {
     if (!shape_ok(cache) || !shape_fits(cache, heads, groups)) return 0;
     size_t bytes = 0;
-    for (uint32_t way = 0; way < 6; ++way) {      // a call with fewer groups goes another way
+    for (int way = 0; way < 4; ++way) {      // a call with fewer groups goes another way
         SharedPlan p;
-        if (!lay_out(cache, heads, way / 2 * 128, way & 1 ? 32 : 16, p)) return 0;
+        if (!lay_out(cache, heads, way & 1, way & 2 ? 32 : 16, p)) return 0;
         if (p.bytes > bytes) bytes = p.bytes;
     }
     return bytes;
@@ -934,8 +947,8 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
         a.by_runs = make_div(a.runs);
         a.slots = P.of_slots;
         a.slot_rows = P.of.rows;
-        if (bf16) launch_shared<true>(a, P.many, s);
-        else launch_shared<false>(a, P.many, s);
+        if (bf16) launch_shared<true>(a, s);
+        else launch_shared<false>(a, s);
         const int rc = launched();
         if (rc) return rc;
     }
