@@ -54,8 +54,9 @@ def parse():
                          "at 2^16, 2^18, ..., 2^30 elements and print them as one JSON line")
     ap.add_argument("--kv", metavar="CASE", nargs="?", const="all",
                     help="instead of the benchmark, time the key-value cache operators on the cases "
-                         "of perf/operators.py (or the one named) and on forms that they leave "
-                         "out (forms: only those), and print them as one JSON line")
+                         "of perf/operators.py and perf/more_operators.py (or the one named) and "
+                         "on forms that they leave out (forms: only those), and print them as "
+                         "one JSON line")
     ap.add_argument("--probes", action="store_true",
                     help="instead of the benchmark, run the probes of the part's costs that the "
                          "design rests on (reference-stream library) and print them as one JSON line")
@@ -386,16 +387,18 @@ def single_call_sizes(S, W, dev, stream):
 
 
 def kv_operators(only=None):
-    """The key-value cache operators on the cases of perf/operators.py: us a
-    pass of the kernels and of the plain forms (elementary torch operations),
-    GB/s by the bytes an operator cannot do without, and that floor's time at
-    the rate of a 2 GiB device-to-device copy of the same run.  Passes take
-    turns over three states of different inputs; median of five rounds."""
+    """The key-value cache operators on the cases of perf/operators.py and
+    perf/more_operators.py: us a pass of the kernels and of the plain forms
+    (elementary torch operations), GB/s by the bytes an operator cannot do
+    without, and the floor, the time of those bytes at the rate of a 2 GiB
+    device-to-device copy or of its products at that of a bf16 product of
+    8192^3, whichever is longer, both of the same run.  Passes take turns over
+    three states of different inputs; median of five rounds."""
     import statistics
 
     import torch
 
-    from perf import operators as P
+    from perf import more_operators, operators
 
     def timed(fn, passes):
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -412,8 +415,13 @@ def kv_operators(only=None):
     timed(copy, 3)
     rate = 2 * src.numel() / statistics.median(timed(copy, 5) for _ in range(5)) / 1e3
     del src, dst
-    out = {"copy_GBps": round(rate, 0)}
-    for case in P.listed():
+    a, b = (torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    product = lambda k: a @ b             # noqa: E731
+    timed(product, 3)
+    flops = 2 * 8192 ** 3 / statistics.median(timed(product, 5) for _ in range(5)) / 1e6
+    del a, b
+    out = {"copy_GBps": round(rate, 0), "product_TFLOPs": round(flops, 0)}
+    for P, case in [(P, case) for P in (operators, more_operators) for case in P.listed()]:
         if only and case["name"] != only:
             continue
         P.own = True
@@ -425,13 +433,14 @@ def kv_operators(only=None):
             run = lambda k: P.run(states[k % 3])      # noqa: E731
             timed(run, 6)
             us[side] = statistics.median(timed(run, passes) for _ in range(5 if P.own else 3))
-        nbytes = P.work(case)["bytes"]
+        work = P.work(case)
+        nbytes = work["bytes"]
         out[case["name"]] = {"us": round(us["kernel"], 2), "plain_us": round(us["plain"], 1),
-                             "floor_us": round(nbytes / rate / 1e3, 2),
+                             "floor_us": round(max(nbytes / rate / 1e3, work["flops"] / flops / 1e6), 2),
                              "GBps": round(nbytes / us["kernel"] / 1e3, 0)}
         del states
     if only in (None, "forms"):
-        out["forms"] = kv_forms(P, timed, rate)
+        out["forms"] = kv_forms(operators, timed, rate)
     return out
 
 
