@@ -695,6 +695,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(Sh
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kMaxShares = kSharedRuns + 1024;      // of a query head: runs of both launches
+constexpr uint32_t kJoinWaves = kJoinThreads / 64;
 constexpr int kAhead = 12;                               // shares a thread loads before their weights are known
 
 struct JoinArgs {
@@ -703,73 +704,145 @@ struct JoinArgs {
     uint64_t os[2];
     float *lse;
     uint32_t rows, of_step, alone_step;      // rows there are; rows from a share to the next
+    uint32_t per;                            // query heads a workgroup has: kJoinWaves, or 1
 };
 
-// One workgroup per query head of a sequence: its shares, rescaled to their
-// common maximum.  A chain of two loads (where they are; maxima, sums and
-// outputs together); every wave works the weights out for itself instead of
-// waiting for another.
-template <bool BF16>
-__global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
-    __shared__ float s_w[kJoinThreads / 64][kMaxShares];
-    __shared__ f32x4 s_o[kJoinThreads];
-    const SharedArgs &a = j.s;
-    const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, b = blockIdx.y, head = blockIdx.x, dim = a.c.dim;
-    const uint32_t h = head / a.group, in_group = head - h * a.group;
-    const uint32_t of_part = in_group / a.of.rows, alone_part = in_group / a.alone.rows;
-    u32x4 of = ((const u32x4 *)a.of_notes)[((uint64_t)b * a.c.kv_heads + h) * a.of.parts + of_part];
-    const u32x4 alone = ((const u32x4 *)a.alone_notes)[((uint64_t)b * a.c.kv_heads + h) * a.alone.parts + alone_part];
-    // (bounded, where arguments that changed meanwhile left notes unwritten)
-    const uint32_t n0 = alone[3] ? min(of[2], kMaxShares / 2) : 0, n = n0 + min(alone[2], kMaxShares / 2);
-    const uint32_t of_row = in_group - of_part * a.of.rows, alone_row = in_group - alone_part * a.alone.rows;
-    auto row_of = [&](uint32_t i) {
-        const uint32_t k = i < n0 ? i : i - n0, step = i < n0 ? j.of_step : j.alone_step;
-        const uint32_t at = k ? (i < n0 ? of[1] : alone[1]) + k * step : i < n0 ? of[0] : alone[0];
-        return (uint64_t)min(at + (i < n0 ? of_row : alone_row), j.rows - 1);
-    };
-    const uint32_t pieces = dim / 4, ways = kJoinThreads / pieces;      // 4-column pieces of a row; shares summed side by side
-    const uint32_t way = tid / pieces, d = (tid - way * pieces) * 4;
-    f32x4 y[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        const uint32_t k = way + i * ways;
-        y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (way < ways && k < n) y[i] = *(const f32x4 *)(a.o + row_of(k) * dim + d);
+// Where a query head's shares are: n0 of its group's tokens, the others of its own.
+struct HeadShares {
+    uint32_t n0, n, of_first, of_rest, of_step, alone_first, alone_rest, alone_step, last;
+
+    __device__ HeadShares(const JoinArgs &j, uint32_t b, uint32_t head) {
+        const SharedArgs &a = j.s;
+        const uint32_t h = head / a.group, in_group = head - h * a.group;
+        const uint32_t of_part = in_group / a.of.rows, alone_part = in_group / a.alone.rows;
+        const uint64_t pair = (uint64_t)b * a.c.kv_heads + h;
+        const u32x4 of = ((const u32x4 *)a.of_notes)[pair * a.of.parts + of_part];
+        const u32x4 alone = ((const u32x4 *)a.alone_notes)[pair * a.alone.parts + alone_part];
+        // (bounded, where arguments that changed meanwhile left notes unwritten)
+        n0 = alone[3] ? min(of[2], kMaxShares / 2) : 0;
+        n = n0 + min(alone[2], kMaxShares / 2);
+        const uint32_t of_row = in_group - of_part * a.of.rows, alone_row = in_group - alone_part * a.alone.rows;
+        of_first = of[0] + of_row, of_rest = of[1] + of_row, of_step = j.of_step;
+        alone_first = alone[0] + alone_row, alone_rest = alone[1] + alone_row, alone_step = j.alone_step;
+        last = j.rows - 1;
     }
+    __device__ uint64_t row(uint32_t i) const {
+        const bool of = i < n0;
+        const uint32_t k = of ? i : i - n0;
+        return min(k ? (of ? of_rest + k * of_step : alone_rest + k * alone_step) : of ? of_first : alone_first, last);
+    }
+};
+
+// The weights of n shares into w, and the joined sum, by a wave.
+__device__ inline void weigh(const float *shares_ml, const HeadShares &sh, float *w, float &top, float &sum) {
+    const uint32_t lane = threadIdx.x & 63;
     f32x2 ml{-INFINITY, 0.f};
-    if (lane < n) ml = *(const f32x2 *)(a.ml + row_of(lane) * 2);
-    float top = ml[0];
-    for (uint32_t k = lane + 64; k < n; k += 64) top = fmaxf(top, a.ml[row_of(k) * 2]);
+    if (lane < sh.n) ml = *(const f32x2 *)(shares_ml + sh.row(lane) * 2);
+    top = ml[0];
+    for (uint32_t k = lane + 64; k < sh.n; k += 64) top = fmaxf(top, shares_ml[sh.row(k) * 2]);
     top = wave_reduce<true>(top);
     // a share with m = -inf saw no finite logit: its sum is 0, or NaN, which stays
     auto weight = [&](float m) { return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top); };
-    float w = weight(ml[0]), sum = ml[1] * w;
-    if (lane < n) s_w[wave][lane] = w;
-    for (uint32_t k = lane + 64; k < n; k += 64) {
-        const f32x2 more = *(const f32x2 *)(a.ml + row_of(k) * 2);
-        w = weight(more[0]);
-        s_w[wave][k] = w;
-        sum += more[1] * w;
+    const float v = weight(ml[0]);
+    sum = ml[1] * v;
+    if (lane < sh.n) w[lane] = v;
+    for (uint32_t k = lane + 64; k < sh.n; k += 64) {
+        const f32x2 more = *(const f32x2 *)(shares_ml + sh.row(k) * 2);
+        const float u = weight(more[0]);
+        w[k] = u;
+        sum += more[1] * u;
     }
     sum = wave_reduce<false>(sum);
-    __builtin_amdgcn_wave_barrier();
-    f32x4 o{0.f, 0.f, 0.f, 0.f};
-    if (way < ways) {
+}
+
+template <bool BF16>
+__device__ inline void write_head(const JoinArgs &j, uint32_t b, uint32_t head, uint32_t d, f32x4 o, float top, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
+    *(u32x2 *)(j.out + b * j.os[0] + head * j.os[1] + d) = z;
+    if (d == 0 && j.lse) j.lse[b * (uint64_t)j.s.heads + head] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
+}
+
+// A wave per query head of a sequence: its shares, rescaled to their common
+// maximum.  A chain of two loads: where they are; maxima, sums and outputs
+// together.  Heads of more shares than a wave loads at once are all four waves',
+// one after another; where heads are few a workgroup has one.  (96 x 32 heads
+// of 64 columns with 2 to 4 shares 5.1 us, a workgroup each 9.6; 12 x 24 of 256
+// with 13 and more, a workgroup each 5.2, four a workgroup 12.9.)
+template <bool BF16>
+__global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
+    __shared__ float s_w[kMaxShares];
+    __shared__ f32x4 s_o[kJoinThreads];
+    __shared__ float s_top, s_sum;
+    __shared__ bool s_many[kJoinWaves];
+    const SharedArgs &a = j.s;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, b = blockIdx.y, dim = a.c.dim;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t pieces = dim / 4;      // 4-column pieces of a row
+    // shares summed side by side, and those that a thread loads before their weights are known
+    auto load = [&](const HeadShares &sh, uint32_t t, uint32_t ways, f32x4 (&y)[kAhead]) {
+        const uint32_t way = t / pieces, d = (t - way * pieces) * 4;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const uint32_t k = way + i * ways;
-            if (k < n) o += y[i] * s_w[wave][k];
+            y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (way < ways && k < sh.n) y[i] = *(const f32x4 *)(a.o + sh.row(k) * dim + d);
         }
-        for (uint32_t k = way + kAhead * ways; k < n; k += ways) o += *(const f32x4 *)(a.o + row_of(k) * dim + d) * s_w[wave][k];
+    };
+    auto add = [&](const HeadShares &sh, uint32_t t, uint32_t ways, const f32x4 (&y)[kAhead], const float *w) {
+        const uint32_t way = t / pieces, d = (t - way * pieces) * 4;
+        f32x4 o{0.f, 0.f, 0.f, 0.f};
+        if (way >= ways) return o;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (way + i * ways < sh.n) o += y[i] * w[way + i * ways];
+        for (uint32_t k = way + kAhead * ways; k < sh.n; k += ways) o += *(const f32x4 *)(a.o + sh.row(k) * dim + d) * w[k];
+        return o;
+    };
+    f32x4 y[kAhead];
+    float top, sum;
+    const uint32_t mine = blockIdx.x * kJoinWaves + wave, ways = 64 / pieces;
+    bool many = j.per == 1 && wave == 0;
+    if (j.per != 1 && mine < a.heads) {
+        const HeadShares sh(j, b, mine);
+        many = sh.n > min(ways * kAhead, 64u);
+        if (!many) {
+            float *w = s_w + wave * 64;
+            load(sh, lane, ways, y);
+            weigh(a.ml, sh, w, top, sum);
+            __builtin_amdgcn_wave_barrier();
+            f32x4 o = add(sh, lane, ways, y, w);
+            s_o[tid] = o;
+            __builtin_amdgcn_wave_barrier();
+            if (lane < pieces) {
+                for (uint32_t k = 1; k < ways; ++k) o += s_o[wave * 64 + k * pieces + lane];
+                write_head<BF16>(j, b, mine, lane * 4, o, top, sum);
+            }
+        }
     }
-    s_o[tid] = o;
+    if (lane == 0) s_many[wave] = many;
     __syncthreads();
-    if (tid < pieces) {
-        for (uint32_t k = 1; k < ways; ++k) o += s_o[k * pieces + tid];
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
-        *(u32x2 *)(j.out + b * j.os[0] + head * j.os[1] + d) = z;
-        if (tid == 0 && j.lse) j.lse[b * (uint64_t)a.heads + head] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
+    for (uint32_t i = 0; i < kJoinWaves; ++i) {
+        if (!s_many[i]) continue;
+        const uint32_t head = blockIdx.x * j.per + i, all = kJoinThreads / pieces;
+        const HeadShares sh(j, b, head);
+        load(sh, tid, all, y);
+        if (wave == 0) {
+            weigh(a.ml, sh, s_w, top, sum);
+            if (lane == 0) {
+                s_top = top;
+                s_sum = sum;
+            }
+        }
+        __syncthreads();
+        f32x4 o = add(sh, tid, all, y, s_w);
+        s_o[tid] = o;
+        __syncthreads();
+        if (tid < pieces) {
+            for (uint32_t k = 1; k < all; ++k) o += s_o[k * pieces + tid];
+            write_head<BF16>(j, b, head, tid * 4, o, s_top, s_sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -960,8 +1033,9 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     else launch_both<false>(a, P.blocks, s);
     const int rc = launched();
     if (rc) return rc;
-    JoinArgs j{a, Q.out, {Q.out_stride[0], Q.out_stride[1]}, Q.lse, P.rows, 2 * (many ? P.of.rows : P.slot_rows), 2 * P.slot_rows};
-    const dim3 joins(Q.heads, cache->batch);
+    JoinArgs j{a, Q.out, {Q.out_stride[0], Q.out_stride[1]}, Q.lse, P.rows, 2 * (many ? P.of.rows : P.slot_rows), 2 * P.slot_rows,
+               (uint64_t)Q.heads * cache->batch >= 1024 ? kJoinWaves : 1};
+    const dim3 joins((Q.heads - 1) / j.per + 1, cache->batch);
     if (bf16) k_join_shared<true><<<joins, kJoinThreads, 0, s>>>(j);
     else k_join_shared<false><<<joins, kJoinThreads, 0, s>>>(j);
     return launched();
