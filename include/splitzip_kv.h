@@ -277,9 +277,10 @@ int splitzip_kv_pages_fork(const splitzip_kv_pages *pages, const int32_t *parent
  * are copied in every layer (of the sequences that all grow in one page that
  * no other names the first keeps it).  The pages given are the free ones in
  * ascending order.  When they run out a sequence's length becomes what its
- * pages hold, or stays as it was if its copy could not be had
- * (SPLITZIP_KV_NO_PAGE).  The tokens from the old length on are the caller's
- * to append. */
+ * pages hold, or stays as it was if its copy could not be had, or if it would
+ * have kept a page that another still reads because that one's copy could not
+ * be had (SPLITZIP_KV_NO_PAGE).  The tokens from the old length on are the
+ * caller's to append. */
 int splitzip_kv_pages_resize(const splitzip_kv_pages *pages, const int32_t *lens, int32_t *d_status, void *stream);
 
 /* Compact: with n pages in use, the pages in use from n on move to the free

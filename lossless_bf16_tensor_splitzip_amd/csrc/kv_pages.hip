@@ -41,7 +41,7 @@ struct State {
     uint32_t *list;           // [pages] free pages, ascending
     uint32_t *from;           // [pages] pages to be moved, from the top
     uint32_t *rank;           // [pages] a moved page's place in from
-    uint32_t *words;          // 0: pages in use; 1: moves; 2: pages given
+    uint32_t *words;          // 0: pages in use; 1: moves; 2: pages given; 3: pages wanted
     Want *want;               // [batch]
 };
 
@@ -443,7 +443,10 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
         found += all;
         __syncthreads();
     }
-    if (tid == 0) a.s.words[2] = min(found, total);
+    if (tid == 0) {
+        a.s.words[2] = min(found, total);
+        a.s.words[3] = total;
+    }
 }
 
 // (A state that was written to may name anything: a page number is compared
@@ -460,13 +463,27 @@ __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, 
     copied = copied && copy < a.c.num_pages;
     if (pool == 0 && first_launch) {
         int32_t *row = a.table + b * a.c.table_stride;
+        // A sequence that keeps the page it shared must not write it where another
+        // got no page for its copy and still reads it.
+        bool kept = false;
+        if (given < a.s.words[3] && w.page != kNoPage && !w.copies) {
+            for (uint32_t other = tid; other < a.c.batch; other += kCopyThreads) {
+                const Want x = a.s.want[other];
+                kept = kept || (x.page == w.page && x.copies && x.before >= given);
+            }
+            kept = __syncthreads_or(kept);
+        }
         for (uint32_t i = w.first + tid; i < w.need; i += kCopyThreads) {
             const uint32_t rank = w.before + w.copies + (i - w.first);
             if (rank < given) {
                 const uint32_t page = a.s.list[rank];
                 if (page >= a.c.num_pages) continue;
-                row[i] = (int32_t)page;
-                a.s.refs[page] = 1;
+                if (kept) {
+                    atomicAdd(&a.s.free_in[page / kBlock], 1);
+                } else {
+                    row[i] = (int32_t)page;
+                    a.s.refs[page] = 1;
+                }
             }
         }
         if (tid == 0) {
@@ -477,10 +494,10 @@ __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, 
                 row[div(w.old_len, a.c.page)] = (int32_t)copy;
                 a.s.refs[copy] = 1;
                 drop_name(a.s, w.page, 1);
-            } else if (w.copies) {
+            } else if (w.copies || kept) {
                 len = w.old_len;
             }
-            if (got < n || (w.copies && !copied)) report(a.status, SPLITZIP_KV_NO_PAGE);
+            if (got < n || kept || (w.copies && !copied)) report(a.status, SPLITZIP_KV_NO_PAGE);
             a.c.lens[b] = (int32_t)len;
             if (w.page != kNoPage) {
                 a.s.writers[w.page] = 0;

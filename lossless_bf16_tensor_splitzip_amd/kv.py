@@ -427,7 +427,9 @@ class KVCache:
                 self._here(out, "output")
             if out.requires_grad or _forward._current_level >= 0:
                 _no_grad(out, "output")
-        if lse is not None:
+        if lse is not None and not (lse.dtype is torch.float32 and lse.shape == (self.batch, heads) and
+                                    lse.get_device() == index and lse.is_contiguous() and not lse.requires_grad and
+                                    _forward._current_level < 0):
             _plain(lse, torch.float32, 2, "lse")
             if tuple(lse.shape) != (self.batch, heads) or not lse.is_contiguous():
                 raise ValueError("lse must be contiguous [%d, %d]" % (self.batch, heads))

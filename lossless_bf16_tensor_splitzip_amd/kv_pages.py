@@ -86,16 +86,22 @@ class KVPages:
 
     def _ints(self, t: torch.Tensor, n: int, what: str, apart: bool = True) -> int:
         """Address of n int32 on the cache's device, apart from what the calls write."""
+        if not (t.get_device() == self._index and t.dtype is torch.int32 and t.shape == (n,) and t.is_contiguous()):
+            self._check_ints(t, n, what)
+        p = t.data_ptr()
+        if apart and n:
+            end = p + 4 * n
+            (s0, e0), (s1, e1), (s2, e2) = self._written
+            if p < e0 and s0 < end or p < e1 and s1 < end or p < e2 and s2 < end:
+                raise ValueError("the %s share memory with the table, the lengths or the counts" % what)
+        return p
+
+    def _check_ints(self, t: torch.Tensor, n: int, what: str) -> None:
+        """The same for what the quick look is not content with."""
         if not t.is_cuda or t.device != self.device or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or \
                 not t.is_contiguous():
             raise ValueError("the %s must be %d contiguous int32 on %s, got %s %s on %s"
                              % (what, n, self.device, t.dtype, tuple(t.shape), t.device))
-        p = t.data_ptr()
-        if apart and n:
-            for start, end in self._written:
-                if p < end and start < p + 4 * n:
-                    raise ValueError("the %s share memory with the table, the lengths or the counts" % what)
-        return p
 
     def _ready(self) -> None:
         if not self._counted:
@@ -123,9 +129,11 @@ class KVPages:
         cache's own, after an eviction in place).  Pages behind them are freed,
         then sequences that grow are given pages, the lowest free ones in the
         order of sequences; one that grows within a page that others name is
-        given a copy of it (in every layer) first.  The new tokens are the
-        caller's to append.  With no page left a sequence gets as long as its
-        pages hold (KV_NO_PAGE; compare ``lens`` of the cache)."""
+        given a copy of it (in every layer) first; where all that name it grow,
+        the first of them keeps it.  The new tokens are the caller's to append.
+        With no page left a sequence gets as long as its pages hold, and stays
+        as it was where the page it would write in is still another's
+        (KV_NO_PAGE; compare ``lens`` of the cache)."""
         self._ready()
         first = self.caches[0]
         own = lens.data_ptr() == first.args.lens and first.batch > 0

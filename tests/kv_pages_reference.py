@@ -58,7 +58,7 @@ class Pool:
         for b, (row, old, new) in enumerate(zip(self.table, self.lens, lens)):
             if new > old and old % self.page and row[old // self.page] >= 0:
                 begun.setdefault(row[old // self.page], []).append(b)
-        copies = []
+        copies, keeps, missed = [], [], set()
         for b, (row, old, new) in enumerate(zip(self.table, list(self.lens), lens)):
             at, page = old // self.page, None
             if new > old and old % self.page:
@@ -70,9 +70,12 @@ class Pool:
                 if not free:
                     self.status |= NO_PAGE
                     self.lens[b] = old
+                    missed.add(page)
                 else:
                     copies.append((page, free[0], old % self.page))
                     row[at] = free.pop(0)
+            elif page is not None:
+                keeps.append((b, page, old, self.need(old)))
             first = self.need(new)
             while first and row[first - 1] < 0:
                 first -= 1
@@ -82,6 +85,11 @@ class Pool:
                     self.lens[b] = min(self.lens[b], i * self.page)
                     break
                 row[i] = free.pop(0)
+        for b, page, old, held in keeps:      # another still reads the page
+            if page in missed:
+                self.status |= NO_PAGE
+                self.lens[b] = old
+                self.table[b][held:] = [-1] * (len(self.table[b]) - held)
         for source, target, slots in copies:
             self.kv[:, :, target, :, :slots] = self.kv[:, :, source, :, :slots]
 

@@ -190,6 +190,33 @@ def test_who_keeps_a_shared_page():
         m.check((parents, lens))
 
 
+@pytest.mark.parametrize("lens,want", [
+    # pages of 4; 0, 1 and 2 share one with 3, 1 and 2 slots in use; `spare` pages are free
+    ((0, [4, 2, 3]), [3, 1, 2]),          # no copy to be had: nobody may write the page
+    ((1, [4, 2, 3]), [3, 2, 2]),          # one has its own
+    ((2, [4, 2, 3]), [4, 2, 3]),          # the first keeps it
+    ((2, [8, 2, 3]), [3, 2, 2]),          # its own next page leaves one copy: it gets neither page nor length
+    ((3, [8, 2, 3]), [8, 2, 3]),
+    ((0, [4, 1, 0]), [3, 1, 0]),          # 1 reads it: 0 must copy
+    ((0, [4, 0, 0]), [4, 0, 0]),          # nobody else names it
+])
+@pytest.mark.parametrize("far", [0, 1100])
+def test_the_page_that_is_kept_when_pages_run_out(lens, want, far):
+    """The sequence that would keep the page it shares does not write over one that has no copy."""
+    _say("a kept page, %s, %d sequences between" % (lens, far))
+    spare, lens = lens
+    between = [0] * far
+    m = Made([3] + between + [0, 0], 1 + spare, 4, 2, layers=2, kv_heads=2)
+    m.count()
+    m.fork([0] + list(range(1, far + 1)) + [0, 0])
+    m.resize([3] + between + [1, 2])
+    m.check("shared")
+    m.resize([lens[0]] + between + lens[1:])
+    m.check((lens, far))
+    got = m.lens.tolist()
+    assert [got[0]] + got[far + 1:] == want
+
+
 def test_findings():
     """What only the device sees: left out, reported."""
     _say("findings of the page operators")
