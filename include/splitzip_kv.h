@@ -226,8 +226,8 @@ size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_
  * tokens in common attends on its own.  The weights of the tokens in common
  * are rounded to the cache's type once (half a step of it each); all other
  * sums are held as in splitzip_kv_attend.  Ranges that decrease or leave the
- * batch: BAD_ROWS, no tokens in common (where ranges overlap by that, their
- * sequences' outputs mean nothing); shared below 0: BAD_LEN, taken as 0.
+ * batch: BAD_ROWS, no tokens in common (where ranges overlap by that, outputs
+ * mean nothing); shared below 0: BAD_LEN, taken as 0.
  * Errors: INVALID (also a window or mass), WORKSPACE, HIP. */
 int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_query *query,
                               const splitzip_kv_groups *groups, void *d_ws, size_t ws_bytes, int32_t *d_status,

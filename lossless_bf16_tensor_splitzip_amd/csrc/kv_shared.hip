@@ -55,7 +55,7 @@ struct SharedArgs {
     uint32_t groups, heads, group;     // group: query heads of a KV head
     Tiling of, alone;                  // of groups, of sequences alone (members 1)
     float scale2;                      // scale * log2(e)
-    uint32_t runs;
+    uint32_t runs, most;               // most: units of groups that do not overlap, at most
     Div by_runs, by_group;
     uint32_t *from;                    // [batch] tokens that k_shared attended for the group; NULL: k_both attends them
     Note *of_notes, *alone_notes;      // [batch][kv_heads][of.parts], [alone.parts]
@@ -117,11 +117,12 @@ struct Piece {
 };
 
 // The piece of a group at unit u of the groups' work, from the block that
-// has it.
+// has it; of no unit where ranges that overlap made the running sums wrap.
 __device__ inline Piece group_piece(const SharedArgs &a, const Block64Groups &blk, uint32_t at, uint32_t u, uint32_t u_end) {
     auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
     const uint32_t size = lane_of(blk.group.size), tiles = lane_of(blk.tiles);
     Piece p{lane_of(blk.group.first), lane_of(blk.group.len), 0, 0, 0, 0, lane_of(blk.units), 0, 0, 0};
+    if (!p.units || !tiles) return p;
     const uint32_t rel = u - lane_of(blk.before) * a.c.kv_heads, pair = rel / p.units;
     p.unit0 = rel - pair * p.units;
     p.count = min(p.units - p.unit0, u_end - u);
@@ -210,6 +211,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
         }
         if (groups > 64) block_of_groups(0, 0);
         group_units *= kvh;
+        if (group_units > a.most) group_units = 0;      // ranges that overlap
     }
 
     Block64Rest blk{};
@@ -296,7 +298,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
             p.row0 = p.part * a.alone.rows;
             p.rows = min(a.alone.rows, a.group - p.row0);
         }
-        if (p.h >= kvh) return;
+        if (!p.count || p.h >= kvh) return;
         const Seen seen{0, p.from, p.len - p.from};
         attend_tokens<BF16, DP, NT, EXACT>(
             lds, a.c, p.h, a.c.table + p.first * a.c.table_stride, seen, p.unit0, min(seen.count, (p.unit0 + p.count) * kUnit), p.rows,
@@ -435,6 +437,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(Sh
             total += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
     }
     const uint32_t units = total * kvh;
+    if (units > a.most) return;      // ranges that overlap
     const Cut cut = units < kLeast * a.runs ? Cut{units, (units + kLeast - 1) / kLeast, kLeast, 0} : cut_of(units, a.by_runs);
     if (blockIdx.x >= cut.runs) return;
     const uint32_t u_begin = cut.begin(blockIdx.x), u_end = min(units, cut.begin(blockIdx.x + 1));
@@ -466,7 +469,7 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(Sh
             load_groups<T>(a, blk.base + 64, blk.total, blk, nullptr);
         }
         const Piece p = group_piece(a, blk, (uint32_t)__builtin_ctzll(past), u, u_end);
-        if (p.h >= kvh) return;
+        if (!p.count || p.h >= kvh) return;
         const bool late = u != u_begin;
         const uint32_t rows = p.rows, end = min(p.len, (p.unit0 + p.count) * T);
         const int32_t *table = a.c.table + p.first * a.c.table_stride;
@@ -853,6 +856,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
 struct SharedPlan {
     uint32_t group, blocks, both_runs, shared_runs;     // blocks of 16 rows in k_both; shared_runs 0: no k_shared
     Tiling of, alone;
+    uint32_t most;                                      // units of the groups' tokens, at most
     uint32_t of_slots, of_whole, both_slots, alone_whole, rows, slot_rows;
     size_t from_at, of_notes_at, alone_notes_at, ml_at, o_at, bytes;
 };
@@ -876,9 +880,10 @@ bool lay_out(const splitzip_kv_cache *c, uint32_t heads, bool many, uint32_t mos
     p.of = tiling(group, many ? kRows : most);
     const uint64_t all = (uint64_t)c->max_pages * c->page_size;
     const uint64_t tiles = (uint64_t)batch * p.of.parts * c->kv_heads;      // of groups, at most
-    const uint64_t both = (all / kUnit + 1) * ((many ? 0 : tiles) + (uint64_t)batch * p.alone.parts * c->kv_heads);
-    const uint64_t shared = many ? (all / tile_tokens((int)c->head_dim) + 1) * tiles : 0;
-    if (both >> 31 || shared >> 31) return false;
+    const uint64_t units = (all / (many ? tile_tokens((int)c->head_dim) : kUnit) + 1) * tiles, shared = many ? units : 0;
+    const uint64_t both = (all / kUnit + 1) * batch * p.alone.parts * c->kv_heads + (many ? 0 : units);
+    if (both >> 31 || units >> 31) return false;
+    p.most = (uint32_t)units;
     const uint32_t runs = runs_for(c->head_dim, p.blocks), more = c->head_dim <= 128 ? kSharedRuns : kSharedRuns / 2;
     p.both_runs = both < runs ? (uint32_t)both : runs;
     p.shared_runs = shared < more ? (uint32_t)shared : more;
@@ -1000,6 +1005,7 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     a.of = P.of;
     a.alone = P.alone;
     a.scale2 = Q.scale * kLog2e;
+    a.most = P.most;
     a.by_group = make_div(P.group);
     a.of_notes = reinterpret_cast<Note *>(ws + P.of_notes_at);
     a.alone_notes = reinterpret_cast<Note *>(ws + P.alone_notes_at);

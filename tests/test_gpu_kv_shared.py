@@ -193,6 +193,26 @@ def test_ranges_that_decrease():
     check(m, want_status=_abi.KV_BAD_LEN)
 
 
+@pytest.mark.parametrize("length", [64, 2048])
+@pytest.mark.parametrize("groups", [2001, 2049, 65535])
+@pytest.mark.parametrize("heads", [1, 32])
+def test_ranges_that_overlap_many_times(heads, groups, length):
+    """Groups that have all sequences over and over, more work than sums of 32 bits hold: reported, and the call ends."""
+    _say("shared: %d ranges that overlap, %d heads, %d tokens" % (groups, heads, length))
+    batch, page = 2048, 64
+    k = torch.zeros(length // page, 1, page, 64, dtype=BF16, device=DEV)
+    table = torch.arange(length // page, dtype=torch.int32, device=DEV).repeat(batch, 1)
+    cache = S.KVCache(k, torch.ones_like(k), table, torch.full((batch,), length, dtype=torch.int32, device=DEV))
+    q = torch.zeros(batch, heads, 64, dtype=BF16, device=DEV)
+    cu = torch.tensor([0, batch] * (groups // 2 + 1), dtype=torch.int32, device=DEV)
+    assert cu.numel() == groups + 1
+    shared = torch.full((groups,), length, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cache.attend_shared(q, cu, shared, S.KVSharedWorkspace(cache, heads, groups), status=status)
+    torch.cuda.synchronize()
+    assert int(status) == _abi.KV_BAD_ROWS
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("members", [3, 20])
 def test_infinite_values(dtype, members):
