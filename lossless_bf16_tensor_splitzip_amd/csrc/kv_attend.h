@@ -204,16 +204,17 @@ struct AttendLds {
 };
 
 // A workgroup's work on one KV head's tokens for up to 16 NT query rows: the
-// visible numbers from unit0 * kUnit to v_end of the table row.
+// visible numbers from unit0 * kUnit to v_end of a table row.
+//   page_at(t, i)                entry i of the row, of token t
 //   query_at(row)                address of a query row
 //   meanwhile()                  called while the first K and V are on their way
 //   logits(row, v, x[4])         (keep_logits) logits in base 2 of four visible numbers from v on
 //   emit(row, d, o[4], m, l)     four columns from d on of the sum of 2^(x - m) v, not divided by l
 // DP: head_dim rounded up to a multiple of 64.  NT: blocks of 16 query rows.
 // EXACT: head_dim is DP.
-template <bool BF16, int DP, int NT, bool EXACT, typename Query, typename Meanwhile, typename Logits, typename Emit>
-__device__ __forceinline__ void attend_tokens(AttendLds<DP, NT> &lds, const Cache &c, uint32_t h, const int32_t *table, const Seen &seen,
-                                              uint32_t unit0, uint32_t v_end, uint32_t rows, float scale2, int32_t *status,
+template <bool BF16, int DP, int NT, bool EXACT, typename PageAt, typename Query, typename Meanwhile, typename Logits, typename Emit>
+__device__ __forceinline__ void attend_tokens(AttendLds<DP, NT> &lds, const Cache &c, uint32_t h, const Seen &seen, uint32_t unit0,
+                                              uint32_t v_end, uint32_t rows, float scale2, int32_t *status, PageAt page_at,
                                               Query query_at, Meanwhile meanwhile, bool keep_logits, Logits logits, Emit emit) {
     constexpr int KS = DP / 32;             // steps of the K product
     constexpr int P16 = DP / 128;           // 16-byte pieces of a V row a lane takes: columns 128 i + 8 (lane % 16)
@@ -288,8 +289,8 @@ __device__ __forceinline__ void attend_tokens(AttendLds<DP, NT> &lds, const Cach
     // 32.. repeat 0..31), and from it the places of K and V.
     auto token = [&](uint32_t v) { return v < seen.sinks ? v : v + seen.shift; };
     auto page_of = [&](uint32_t v0) {
-        const uint32_t v = v0 + (lane & 31);
-        return v < v_end ? (uint32_t)table[div(token(v), c.page)] : 0xffffffffu;
+        const uint32_t v = v0 + (lane & 31), t = token(v);
+        return v < v_end ? (uint32_t)page_at(t, div(t, c.page)) : 0xffffffffu;
     };
     auto place = [&](uint32_t v0, uint32_t page, int buf) {
         const uint32_t v = v0 + (lane & 31), t = token(v);
@@ -616,7 +617,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_attend(AttendArgs a) {
 
         const uint32_t slot = blockIdx.x * 2 + (u != u_begin);
         attend_tokens<BF16, DP, NT, EXACT>(
-            lds, a.c, h, table, seen, unit0, v_end, rows, a.scale2, a.status,
+            lds, a.c, h, seen, unit0, v_end, rows, a.scale2, a.status, [&](uint32_t, uint32_t i) { return table[i]; },
             [&](uint32_t row) { return a.q + b * a.qs[0] + (head0 + row) * a.qs[1]; },
             [&] {
                 if (a.runs && unit0 == 0 && tid == 0) {      // here its divisions are waited for by nothing
@@ -887,17 +888,21 @@ inline bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mas
     return true;
 }
 
+// Whole, with few units a KV head: no join (5 us), no search for the run's
+// place.  Split/whole in us, KV heads by units (dim 128, batches of equal and
+// of ragged lengths): 64 x 2 11.1/8.5 and 10.5/7.8, 64 x 4 11.5/14.1 and
+// 11.1/13.2, 256 x 4 20.0/16.1 and 13.1/13.6, 256 x 8 30.3/27.3 and 16.1/23.6,
+// 2048 x 4 96/89 and 41/38, 2048 x 32 650/643 and 123/155.
+inline bool whole_heads(uint64_t tiles, uint32_t units) {
+    return tiles < 1u << 24 && (units <= 2 || (units <= 4 && tiles >= 256));      // a grid's limit
+}
+
 // How many runs a launch has, where no sequence sees more than `seen` tokens;
 // its workgroups.
 inline uint32_t lay_out(AttendArgs &a, const AttendPlan &P, uint64_t seen) {
     const uint32_t units = seen ? (uint32_t)((seen - 1) / kUnit + 1) : 1;
-    // Whole, with few units a KV head: no join (5 us), no search for the run's
-    // place.  Split/whole in us, KV heads by units (dim 128, batches of equal and
-    // of ragged lengths): 64 x 2 11.1/8.5 and 10.5/7.8, 64 x 4 11.5/14.1 and
-    // 11.1/13.2, 256 x 4 20.0/16.1 and 13.1/13.6, 256 x 8 30.3/27.3 and 16.1/23.6,
-    // 2048 x 4 96/89 and 41/38, 2048 x 32 650/643 and 123/155.
     const uint64_t tiles = (uint64_t)a.c.batch * a.c.kv_heads * P.row_tiles;
-    const bool whole = tiles < 1u << 24 && (units <= 2 || (units <= 4 && tiles >= 256));      // a grid's limit
+    const bool whole = whole_heads(tiles, units);
     a.runs = whole ? 0 : tiles * units < P.runs ? (uint32_t)(tiles * units) : P.runs;
     a.by_runs = make_div(a.runs ? a.runs : 1);
     a.by_row_tiles = make_div(P.row_tiles);

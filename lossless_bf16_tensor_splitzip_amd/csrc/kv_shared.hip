@@ -3,7 +3,8 @@
 // splitzip_kv_attend_shared.
 //
 //   k_both    the tokens in common, for the query rows of a group, and every
-//             sequence's other tokens, where query rows are few
+//             sequence's other tokens, where query rows are few; or all tokens
+//             of every sequence, where little would be read once instead
 //   k_shared  the tokens in common where they are many (k_both then has the
 //             other tokens alone)
 //   k_join_shared  the shares of both joined
@@ -55,8 +56,11 @@ struct SharedArgs {
     uint32_t groups, heads, group;     // group: query heads of a KV head
     Tiling of, alone;                  // of groups, of sequences alone (members 1)
     float scale2;                      // scale * log2(e)
-    uint32_t runs, most;               // most: units of groups that do not overlap, at most
-    Div by_runs, by_group;
+    uint32_t runs, most;               // runs 0: a workgroup for each sequence's KV head; most: units of groups that do not overlap, at most
+    Div by_runs, by_group, by_pairs;
+    uint16_t *out;                     // rows of the query heads and their lse
+    uint64_t os[2];
+    float *lse;
     uint32_t *from;                    // [batch] tokens that k_shared attended for the group; NULL: k_both attends them
     Note *of_notes, *alone_notes;      // [batch][kv_heads][of.parts], [alone.parts]
     float *o, *ml;                     // rows of [dim] and [2]: shares
@@ -114,6 +118,7 @@ struct Piece {
     uint32_t h, unit0, count, units; // KV head; units of those tokens here, and all of them
     uint32_t row0, rows;             // rows of the row tile: query heads row0 .. of the sequences from first on, in turn
     uint32_t part;
+    uint32_t split, source;          // tokens before split are those of the table row of sequence source
 };
 
 // The piece of a group at unit u of the groups' work, from the block that
@@ -121,7 +126,7 @@ struct Piece {
 __device__ inline Piece group_piece(const SharedArgs &a, const Block64Groups &blk, uint32_t at, uint32_t u, uint32_t u_end) {
     auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
     const uint32_t size = lane_of(blk.group.size), tiles = lane_of(blk.tiles);
-    Piece p{lane_of(blk.group.first), lane_of(blk.group.len), 0, 0, 0, 0, lane_of(blk.units), 0, 0, 0};
+    Piece p{lane_of(blk.group.first), lane_of(blk.group.len), 0, 0, 0, 0, lane_of(blk.units), 0, 0, 0, 0, 0};
     if (!p.units || !tiles) return p;
     const uint32_t rel = u - lane_of(blk.before) * a.c.kv_heads, pair = rel / p.units;
     p.unit0 = rel - pair * p.units;
@@ -170,14 +175,22 @@ __device__ inline uint64_t share_row(const SharedArgs &a, const Piece &p, uint32
 // ---------------------------------------------------------------------------
 
 struct Block64Rest {
-    uint32_t base, len, from, units, before, upto, total;
+    uint32_t base, len, from, first, units, before, upto, total;
 };
+
+template <bool BF16>
+__device__ inline void write_head(const SharedArgs &a, uint32_t b, uint32_t head, uint32_t d, f32x4 o, float top, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
+    *(u32x2 *)(a.out + b * a.os[0] + head * a.os[1] + d) = z;
+    if (d == 0 && a.lse) a.lse[b * (uint64_t)a.heads + head] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
+}
 
 // Groups' tokens in common and sequences' other tokens in units of kUnit, all
 // of them cut into equal runs.  Every workgroup looks all groups and lengths
 // over to find its run; which of the groups a sequence belongs to is looked up
 // in LDS.
-template <bool BF16, int DP, int NT, bool EXACT>
+template <bool BF16, int DP, int NT, bool EXACT, bool APART>
 __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
     __shared__ AttendLds<DP, NT> lds;
     __shared__ uint32_t s_block[kMaxBlocks];
@@ -187,7 +200,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim, kvh = a.c.kv_heads;
     int32_t *status0 = blockIdx.x == 0 ? a.status : nullptr;
-    const uint32_t groups = a.from ? 0 : a.groups;       // that this launch has the tokens of
+    const uint32_t groups = a.from ? 0 : a.groups;       // that are looked up here
 
     Block64Groups gblk{};
     auto block_of_groups = [&](uint32_t base, uint32_t carry) {
@@ -205,11 +218,13 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
             if (g == groups - 1) s_cu[groups] = a.cu[groups];
         }
         __syncthreads();
-        for (uint32_t base = 0; base < groups; base += 64) {
-            block_of_groups(base, group_units);
-            group_units = gblk.total;
+        if (!APART) {
+            for (uint32_t base = 0; base < groups; base += 64) {
+                block_of_groups(base, group_units);
+                group_units = gblk.total;
+            }
+            if (groups > 64) block_of_groups(0, 0);
         }
-        if (groups > 64) block_of_groups(0, 0);
         group_units *= kvh;
         if (group_units > a.most) group_units = 0;      // ranges that overlap
     }
@@ -219,7 +234,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
         const uint32_t b = base + lane;
         blk.base = base;
         blk.len = b < a.c.batch ? seq_len(a.c, b, status) : 0;
-        blk.from = 0;
+        blk.from = blk.first = 0;
         if (a.from) {
             if (b < a.c.batch) blk.from = min(a.from[b], blk.len);
         } else {
@@ -228,39 +243,64 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
                 const uint32_t mid = (lo + hi) >> 1;
                 if (s_cu[mid] <= (int32_t)b) lo = mid + 1; else hi = mid;
             }
-            if (lo && (int32_t)b < s_cu[lo] && s_len[lo - 1] <= blk.len) blk.from = s_len[lo - 1];
+            if (lo && (int32_t)b < s_cu[lo] && s_len[lo - 1] <= blk.len) {
+                blk.from = s_len[lo - 1];
+                blk.first = s_cu[lo - 1];
+            }
         }
+        const uint32_t from = APART ? 0 : blk.from;
         // an empty rest is one unit's work, so that every sequence has a share
-        blk.units = b < a.c.batch ? (blk.len > blk.from ? (blk.len - blk.from - 1) / kUnit + 1 : 1) : 0;
+        blk.units = b < a.c.batch ? (blk.len > from ? (blk.len - from - 1) / kUnit + 1 : 1) : 0;
         const uint32_t sum = wave_scan(blk.units);
         blk.before = carry + sum - blk.units;
         blk.upto = carry + sum;
         blk.total = __builtin_amdgcn_readlane(blk.upto, 63);
     };
     const uint32_t blocks = (a.c.batch + 63) / 64, pairs = kvh * a.alone.parts;
+    const bool whole = APART && !a.runs;
     uint32_t rest_units = 0;
-    if (blocks == 1) {
-        block_of_rest(0, 0, status0);
-        rest_units = blk.total;
-    } else {
-        for (uint32_t i = wave; i < blocks; i += kWaves) {
-            block_of_rest(i * 64, 0, status0);
-            if (lane == 63) s_block[i] = blk.total;
-        }
-        __syncthreads();
-        for (uint32_t f = 0; f < blocks; f += 64)
-            rest_units += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
-    }
-    const Cut cut = cut_of(group_units + rest_units * pairs, a.by_runs);
-    if (blockIdx.x >= cut.runs) return;
-    const uint32_t u_begin = cut.begin(blockIdx.x), u_end = cut.begin(blockIdx.x + 1);
+    auto piece_of_rest = [&](uint32_t at, uint32_t pair) {
+        auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
+        const uint32_t from = lane_of(blk.from);
+        Piece p{blk.base + at, lane_of(blk.len), APART ? 0 : from, 0, 0, 0, lane_of(blk.units), 0, 0, 0, APART ? from : 0, lane_of(blk.first)};
+        p.h = pair / a.alone.parts;
+        p.part = pair - p.h * a.alone.parts;
+        p.row0 = p.part * a.alone.rows;
+        p.rows = min(a.alone.rows, a.group - p.row0);
+        return p;
+    };
+    Cut cut{};
+    uint32_t u_begin = 0, u_end = 1;
     bool found = blocks == 1;       // blk is the block of the rest that the run is in, or one before it
+    if (!whole) {
+        if (blocks == 1) {
+            block_of_rest(0, 0, status0);
+            rest_units = blk.total;
+        } else {
+            for (uint32_t i = wave; i < blocks; i += kWaves) {
+                block_of_rest(i * 64, 0, status0);
+                if (lane == 63) s_block[i] = blk.total;
+            }
+            __syncthreads();
+            for (uint32_t f = 0; f < blocks; f += 64)
+                rest_units += __builtin_amdgcn_readlane(wave_scan(f + lane < blocks ? s_block[f + lane] : 0), 63);
+        }
+        cut = cut_of(group_units + rest_units * pairs, a.by_runs);
+        if (blockIdx.x >= cut.runs) return;
+        u_begin = cut.begin(blockIdx.x);
+        u_end = cut.begin(blockIdx.x + 1);
+    }
 
     for (uint32_t u = u_begin; u < u_end;) {
         const bool of_group = u < group_units, late = u != u_begin;
         Piece p;
         uint64_t past;
-        if (of_group) {
+        if (whole) {
+            const uint32_t b = div(blockIdx.x, a.by_pairs), pair = blockIdx.x - b * pairs;
+            block_of_rest(b & ~63u, 0, pair == 0 ? a.status : nullptr);
+            p = piece_of_rest(b & 63, pair);
+            p.count = p.units;
+        } else if (of_group) {
             while (!(past = __ballot(gblk.upto * kvh > u))) {
                 if (gblk.base + 64 >= groups) return;
                 block_of_groups(gblk.base + 64, gblk.total);
@@ -288,32 +328,38 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
                 block_of_rest(blk.base + 64, blk.total, nullptr);
             }
             const uint32_t at = (uint32_t)__builtin_ctzll(past);
-            auto lane_of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane(x, at); };
-            p = Piece{blk.base + at, lane_of(blk.len), lane_of(blk.from), 0, 0, 0, lane_of(blk.units), 0, 0, 0};
-            const uint32_t rel = v - lane_of(blk.before) * pairs, pair = rel / p.units;
-            p.unit0 = rel - pair * p.units;
-            p.count = min(p.units - p.unit0, u_end - u);
-            p.h = pair / a.alone.parts;
-            p.part = pair - p.h * a.alone.parts;
-            p.row0 = p.part * a.alone.rows;
-            p.rows = min(a.alone.rows, a.group - p.row0);
+            const uint32_t rel = v - (uint32_t)__builtin_amdgcn_readlane(blk.before, at) * pairs;
+            const uint32_t units = __builtin_amdgcn_readlane(blk.units, at), pair = rel / units;
+            p = piece_of_rest(at, pair);
+            p.unit0 = rel - pair * units;
+            p.count = min(units - p.unit0, u_end - u);
         }
         if (!p.count || p.h >= kvh) return;
         const Seen seen{0, p.from, p.len - p.from};
+        const int32_t *own = a.c.table + p.first * a.c.table_stride;
+        const int32_t *common = APART ? a.c.table + p.source * a.c.table_stride : own;
         attend_tokens<BF16, DP, NT, EXACT>(
-            lds, a.c, p.h, a.c.table + p.first * a.c.table_stride, seen, p.unit0, min(seen.count, (p.unit0 + p.count) * kUnit), p.rows,
-            a.scale2, a.status,
+            lds, a.c, p.h, seen, p.unit0, min(seen.count, (p.unit0 + p.count) * kUnit), p.rows, a.scale2, a.status,
+            [&](uint32_t t, uint32_t i) { return (APART && t < p.split ? common : own)[i]; },
             [&](uint32_t row) {
                 uint32_t b, head;
                 locate_row(a, p, row, b, head);
                 return a.q + b * a.qs[0] + head * a.qs[1];
             },
-            [&] { note_shares(a, p, cut, u, late, of_group, p.from != 0); }, false, [](uint32_t, uint32_t, f32x4) {},
+            [&] {
+                if (!whole) note_shares(a, p, cut, u, late, of_group, p.from != 0);
+            },
+            false, [](uint32_t, uint32_t, f32x4) {},
             [&](uint32_t row, uint32_t d, f32x4 y, float top, float sum) {
+                if (whole) {
+                    write_head<BF16>(a, p.first, p.h * a.group + p.row0 + row, d, y, top, sum);
+                    return;
+                }
                 const uint64_t at = share_row(a, p, row, late, of_group);
                 *(f32x4 *)(a.o + at * D + d) = y;
                 if (d == 0) *(f32x2 *)(a.ml + at * 2) = f32x2{top, sum};
             });
+        if (whole) return;
         u += p.count;
     }
 }
@@ -703,9 +749,6 @@ constexpr int kAhead = 12;                               // shares a thread load
 
 struct JoinArgs {
     SharedArgs s;
-    uint16_t *out;
-    uint64_t os[2];
-    float *lse;
     uint32_t rows, of_step, alone_step;      // rows there are; rows from a share to the next
     uint32_t per;                            // query heads a workgroup has: kJoinWaves, or 1
 };
@@ -756,14 +799,6 @@ __device__ inline void weigh(const float *shares_ml, const HeadShares &sh, float
         sum += more[1] * u;
     }
     sum = wave_reduce<false>(sum);
-}
-
-template <bool BF16>
-__device__ inline void write_head(const JoinArgs &j, uint32_t b, uint32_t head, uint32_t d, f32x4 o, float top, float sum) {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    u32x2 z{pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv)};
-    *(u32x2 *)(j.out + b * j.os[0] + head * j.os[1] + d) = z;
-    if (d == 0 && j.lse) j.lse[b * (uint64_t)j.s.heads + head] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kLn2;
 }
 
 // A wave per query head of a sequence: its shares, rescaled to their common
@@ -819,7 +854,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
             __builtin_amdgcn_wave_barrier();
             if (lane < pieces) {
                 for (uint32_t k = 1; k < ways; ++k) o += s_o[wave * 64 + k * pieces + lane];
-                write_head<BF16>(j, b, mine, lane * 4, o, top, sum);
+                write_head<BF16>(a, b, mine, lane * 4, o, top, sum);
             }
         }
     }
@@ -843,7 +878,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
         __syncthreads();
         if (tid < pieces) {
             for (uint32_t k = 1; k < all; ++k) o += s_o[k * pieces + tid];
-            write_head<BF16>(j, b, head, tid * 4, o, s_top, s_sum);
+            write_head<BF16>(a, b, head, tid * 4, o, s_top, s_sum);
         }
         __syncthreads();
     }
@@ -855,6 +890,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
 
 struct SharedPlan {
     uint32_t group, blocks, both_runs, shared_runs;     // blocks of 16 rows in k_both; shared_runs 0: no k_shared
+    bool apart, whole;                                  // k_both has all tokens of every sequence; by a workgroup for each KV head
     Tiling of, alone;
     uint32_t most;                                      // units of the groups' tokens, at most
     uint32_t of_slots, of_whole, both_slots, alone_whole, rows, slot_rows;
@@ -927,15 +963,25 @@ bool shared_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups, Sh
     const uint64_t average = groups ? (uint64_t)c->batch * group / groups : 0;
     const double read = 4.0 * c->max_pages * c->page_size * c->kv_heads * c->head_dim * groups * (double)((average + 31) / 32);
     const bool many = groups > kGroupsHere || (average > 16 && read > (c->head_dim <= 128 ? 56e6 : 160e6));
-    return lay_out(c, heads, many, group <= 16 && (many || average <= 16) ? 16 : 32, p);
+    // Few units a KV head are a workgroup's, without a join.
+    const uint64_t all = (uint64_t)c->max_pages * c->page_size;
+    const bool whole = !many && whole_heads((uint64_t)c->batch * c->kv_heads * ((group - 1) / 32 + 1), all ? (uint32_t)((all - 1) / kUnit + 1) : 1);
+    if (!lay_out(c, heads, many, group <= 16 && (many || whole || average <= 16) ? 16 : 32, p)) return false;
+    p.whole = whole;
+    p.apart = whole || (!many && p.of.members == 1);
+    return true;
 }
 
 template <bool BF16>
-void launch_both(const SharedArgs &a, uint32_t blocks, hipStream_t s) {
+void launch_both(const SharedArgs &a, uint32_t blocks, bool apart, hipStream_t s) {
+    const uint32_t grid = a.runs ? a.runs : a.c.batch * a.c.kv_heads * a.alone.parts;
     auto go = [&](auto dp, auto nt) {
         constexpr int DP = decltype(dp)::value, NT = decltype(nt)::value;
-        if (a.c.dim == DP) k_both<BF16, DP, NT, true><<<a.runs, kAttendThreads, 0, s>>>(a);
-        else k_both<BF16, DP, NT, false><<<a.runs, kAttendThreads, 0, s>>>(a);
+        auto with = [&](auto exact, auto each) {
+            k_both<BF16, DP, NT, decltype(exact)::value, decltype(each)::value><<<grid, kAttendThreads, 0, s>>>(a);
+        };
+        if (a.c.dim == DP) apart ? with(std::true_type{}, std::true_type{}) : with(std::true_type{}, std::false_type{});
+        else apart ? with(std::false_type{}, std::true_type{}) : with(std::false_type{}, std::false_type{});
     };
     auto with = [&](auto dp) {
         if (blocks == 1) go(dp, std::integral_constant<int, 1>{});
@@ -1004,6 +1050,9 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     a.group = P.group;
     a.of = P.of;
     a.alone = P.alone;
+    a.by_pairs = make_div(cache->kv_heads * P.alone.parts);
+    a.out = Q.out;
+    a.lse = Q.lse;
     a.scale2 = Q.scale * kLog2e;
     a.most = P.most;
     a.by_group = make_div(P.group);
@@ -1014,12 +1063,16 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     a.of_whole = P.of_whole;
     a.alone_whole = P.alone_whole;
     a.status = d_status;
-    for (int i = 0; i < 2; ++i) a.qs[i] = Q.q_stride[i];
+    for (int i = 0; i < 2; ++i) {
+        a.qs[i] = Q.q_stride[i];
+        a.os[i] = Q.out_stride[i];
+    }
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool bf16 = cache->dtype == SPLITZIP_KV_BF16;
     // a scale of 0 makes no order of logits, which k_shared goes by: every sequence on its own
-    if (P.shared_runs && a.scale2 == 0.f) a.groups = 0;
-    const bool many = P.shared_runs && a.groups;
+    const bool many = P.shared_runs && a.groups && a.scale2 != 0.f;
+    const bool apart = P.apart || (P.shared_runs && !many);
+    if (apart && a.groups > kGroupsHere) a.groups = 0;
     if (many) {
         a.from = reinterpret_cast<uint32_t *>(ws + P.from_at);
         a.runs = P.shared_runs;
@@ -1031,15 +1084,15 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
         const int rc = launched();
         if (rc) return rc;
     }
-    a.runs = P.both_runs;
-    a.by_runs = make_div(a.runs);
+    a.runs = P.whole ? 0 : P.both_runs;
+    a.by_runs = make_div(a.runs ? a.runs : 1);
     a.slots = P.both_slots;
     a.slot_rows = P.slot_rows;
-    if (bf16) launch_both<true>(a, P.blocks, s);
-    else launch_both<false>(a, P.blocks, s);
+    if (bf16) launch_both<true>(a, P.blocks, apart, s);
+    else launch_both<false>(a, P.blocks, apart, s);
     const int rc = launched();
-    if (rc) return rc;
-    JoinArgs j{a, Q.out, {Q.out_stride[0], Q.out_stride[1]}, Q.lse, P.rows, 2 * (many ? P.of.rows : P.slot_rows), 2 * P.slot_rows,
+    if (rc || P.whole) return rc;
+    JoinArgs j{a, P.rows, 2 * (many ? P.of.rows : P.slot_rows), 2 * P.slot_rows,
                (uint64_t)Q.heads * cache->batch >= 1024 ? kJoinWaves : 1};
     const dim3 joins((Q.heads - 1) / j.per + 1, cache->batch);
     if (bf16) k_join_shared<true><<<joins, kJoinThreads, 0, s>>>(j);
