@@ -963,10 +963,16 @@ bool shared_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t groups, Sh
     const uint64_t average = groups ? (uint64_t)c->batch * group / groups : 0;
     const double read = 4.0 * c->max_pages * c->page_size * c->kv_heads * c->head_dim * groups * (double)((average + 31) / 32);
     const bool many = groups > kGroupsHere || (average > 16 && read > (c->head_dim <= 128 ? 56e6 : 160e6));
-    // Few units a KV head are a workgroup's, without a join.
+    // Row tiles of k_both: of 16 rows for few rows, and for wide heads where that
+    // leaves a tile two sequences (2 groups of 6, 4096 tokens, 2 KV heads of 256, us
+    // with 16 and 32 rows: 8 query heads each 22.7 and 28.3, 12 each 33.3 and 28.1).
+    // Where no tile has two sequences, each attends all of its tokens (2 groups of 6,
+    // 5000 tokens, one KV head of 256 with 24 query heads 22.3 us, with the tokens in
+    // common apart 26.5), and few units a KV head are one workgroup's, without a join
+    // (4 groups of 8, 256 tokens in common of 512, 8 KV heads of 128: 15.0, 26.8).
     const uint64_t all = (uint64_t)c->max_pages * c->page_size;
     const bool whole = !many && whole_heads((uint64_t)c->batch * c->kv_heads * ((group - 1) / 32 + 1), all ? (uint32_t)((all - 1) / kUnit + 1) : 1);
-    if (!lay_out(c, heads, many, group <= 16 && (many || whole || average <= 16) ? 16 : 32, p)) return false;
+    if (!lay_out(c, heads, many, group <= 16 && (many || whole || average <= 16 || (c->head_dim > 128 && group <= 8)) ? 16 : 32, p)) return false;
     p.whole = whole;
     p.apart = whole || (!many && p.of.members == 1);
     return true;
