@@ -7,7 +7,8 @@ Hand-written HIP kernels behind the C ABI of include/splitzip.h
 * ``codec``  -- torch-tensor marshalling: Workspace, calibrate, encode, decode;
 * ``persist`` -- codebook / metadata JSON and the 0.99 coverage gate;
 * ``kv``      -- the paged key-value cache that decoded tensors go into:
-  append, gather, attention of one new token, eviction
+  append, gather, attention of one new token (also over sequences that begin
+  alike), eviction
   (``_lib/libsplitzip_kv.so``, include/splitzip_kv.h);
 * ``kv_pages`` -- who has which of its pages: counting, forking, resizing,
   compacting, copying.

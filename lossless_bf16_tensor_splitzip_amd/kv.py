@@ -8,6 +8,7 @@ kernels.
     lens += 1                              # the step's tokens
     cache.append(k, v, cu)                 # their K and V
     out = cache.attend(q, ws)              # one new token per sequence
+    out = cache.attend_shared(q, cu, shared, sws)    # where sequences begin alike
 
 The pools are [pages, kv_heads, page_size, head_dim]; a pool stored
 [pages, page_size, kv_heads, head_dim] is passed as its transpose(1, 2).

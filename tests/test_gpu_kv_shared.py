@@ -45,9 +45,13 @@ def widen(m):
 
 
 def check(m, scale=None, hidden=(), want_status=0):
-    """With few and, where there are enough of them, with many query rows."""
+    """With few units a KV head, with as many as a join is for, and, where there are enough rows, with many."""
     out = check_one(m, scale, hidden, want_status)
     table = m.table
+    if table.shape[1] * m.page <= 640:
+        m.table = torch.nn.functional.pad(table, (0, 640 // m.page + 1 - table.shape[1]), value=-1)
+        check_one(m, scale, hidden, want_status)
+        m.table = table
     if widen(m):
         check_one(m, scale, hidden, want_status)
         m.table = table
