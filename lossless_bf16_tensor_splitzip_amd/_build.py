@@ -6,6 +6,8 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +25,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # keep the compiler from forming packed fp32 instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -36,17 +37,27 @@ def hipcc() -> str:
     return cand if os.path.exists(cand) else "hipcc"
 
 
-def _compile(src, lib_path: str, verbose: bool) -> str:
-    os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = lib_path + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE] + ([src] if isinstance(src, str) else src) + ["-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _hipcc(args: list, verbose: bool) -> None:
+    res = subprocess.run([hipcc()] + HIPCC_FLAGS + args, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     msgs = [ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln]
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def _compile(src, lib_path: str, verbose: bool) -> str:
+    """One library of a source, or of several that are compiled side by side."""
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = lib_path + ".tmp%d" % os.getpid()
+    if isinstance(src, str):
+        _hipcc(["-shared", "-I", INCLUDE, src, "-o", tmp], verbose)
+    else:
+        with tempfile.TemporaryDirectory() as work, ThreadPoolExecutor(len(src)) as pool:
+            objects = [os.path.join(work, os.path.basename(s) + ".o") for s in src]
+            list(pool.map(lambda so: _hipcc(["-c", "-I", INCLUDE, so[0], "-o", so[1]], verbose), zip(src, objects)))
+            _hipcc(["-shared"] + objects + ["-o", tmp], verbose)
     os.replace(tmp, lib_path)
     return lib_path
 
