@@ -665,11 +665,11 @@ bool pools_ok(const splitzip_kv_pages *p) {
     splitzip_kv_cache c = *p->cache;
     if (!pages_shape_ok(&c) || (uint64_t)c.page_size * c.kv_heads * (c.head_dim / 8) >> 31) return false;
     c.batch = 0;
-    for (uint32_t i = 0; i < p->layers; ++i) {
-        c.k = p->k[i];
-        c.v = p->v[i];
-        if (!cache_ok(&c)) return false;
-    }
+    c.k = p->k[0];
+    c.v = p->v[0];
+    if (!cache_ok(&c)) return false;
+    for (uint32_t i = 1; i < p->layers; ++i)      // shape and strides are those of all layers
+        if (!p->k[i] || !p->v[i] || !aligned(p->k[i], 16) || !aligned(p->v[i], 16)) return false;
     return true;
 }
 

@@ -51,6 +51,7 @@ class KVPages:
             raise ValueError("a table of 2^31 entries")
         self.caches, self.device = caches, first.device
         self._apart_pools()
+        self._kind = tuple(getattr(first, k) for k in _SHARED[2:])
         nbytes = _abi.splitzip_kv_pages_state_size(a)
         self.state = self._buffer(nbytes, self.device)
         self.refs = self.state.view(torch.int32)[:a.num_pages]
@@ -70,6 +71,7 @@ class KVPages:
         pools = [(_span(t), (layer, name), t) for layer, c in enumerate(self.caches)
                  for name, t in (("k", c.k_pages), ("v", c.v_pages))]
         self._pools = sorted(pools, key=lambda x: x[0])
+        self._reach = self._pools[0][0][0], max(span[1] for span, _, _ in pools)
         for x, y in _crossing(self._pools):
             if _meet(x[2], y[2]):
                 raise ValueError("pools of the layers, or of K and V, share memory")
@@ -170,8 +172,7 @@ class KVPages:
         if to is None:
             to = self
         elif to is not self:
-            c = to.caches[0]
-            if len(to.caches) != len(self.caches) or any(getattr(c, k) != getattr(first, k) for k in _SHARED[2:]):
+            if len(to.caches) != len(self.caches) or to._kind != self._kind:
                 raise ValueError("the other pages differ in layers, shape, dtype or device")
             self._apart_from(to)
         n = src.shape[0]
@@ -181,7 +182,7 @@ class KVPages:
     def _apart_from(self, to: "KVPages") -> None:
         """Refuses pools that share memory with those of ``to`` without being them."""
         mine, other = self._pools, to._pools
-        if mine[0][0][0] >= max(p[0][1] for p in other) or other[0][0][0] >= max(p[0][1] for p in mine):
+        if self._reach[0] >= to._reach[1] or to._reach[0] >= self._reach[1]:
             return
         both = sorted([(*p, 0) for p in mine] + [(*p, 1) for p in other], key=lambda x: x[0])
         for (_, x, s, a), (_, y, t, b) in _crossing(both):
