@@ -270,8 +270,9 @@ int splitzip_kv_pages_count(const splitzip_kv_pages *pages, int32_t *d_status, v
 int splitzip_kv_pages_fork(const splitzip_kv_pages *pages, const int32_t *parents, int32_t *d_status, void *stream);
 
 /* Resize: the sequences' lengths become lens (device memory; may be the
- * cache's own, which frees the pages behind them).  Pages behind a new length
- * are freed first.  Then, in the order of sequences, each is given the pages
+ * cache's own, which frees the pages behind them).  Pages behind a sequence's
+ * new length, or behind its old one where that is shorter (a length that was cut
+ * in place, as an eviction does), are freed first.  Then, in the order of sequences, each is given the pages
  * that positions up to its new length need, and where it grows from within a
  * page that others name, a page of its own first, to which the slots in use
  * are copied in every layer (of the sequences that all grow in one page that

@@ -267,12 +267,15 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t widt
 // resize
 // ---------------------------------------------------------------------------
 
+// A sequence keeps the pages that its old or its new length needs, whichever is
+// shorter.  Entries behind an old length that was cut in the caches hold no
+// token, and a fork may have given them to others, who would write them too.
 // Pages are held from a row's start without a gap, so what a sequence drops and
-// misses is looked for from the border of its new length.  A wave looks at 64
+// misses is looked for from the border of what it keeps.  A wave looks at 64
 // entries a time: drops those behind, and returns the first that is missing.
-__device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32_t need, uint32_t width) {
+__device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32_t keep, uint32_t width) {
     const uint32_t lane = threadIdx.x & 63;
-    for (uint32_t i0 = need; i0 < width; i0 += 64) {
+    for (uint32_t i0 = keep; i0 < width; i0 += 64) {
         const int32_t page = i0 + lane < width ? row[i0 + lane] : -1;
         if (page >= 0) {
             if ((uint32_t)page < a.c.num_pages) drop_name(a.s, page, 1);
@@ -280,7 +283,7 @@ __device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32
         }
         if (!__ballot(page >= 0)) break;
     }
-    uint32_t first = need;
+    uint32_t first = keep;
     while (first) {
         const uint32_t n = min(first, 64u), i = first - n + lane;
         const uint64_t held = __ballot(lane < n && row[i] >= 0);
@@ -290,19 +293,19 @@ __device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32
     return 0;
 }
 
-// Lengths asked for and old, and the page that is begun and will be written,
-// of which the writers are counted.
+// Lengths asked for and old, and what is kept (in `first`).
 __device__ inline Want want_of(const PageArgs &a, uint32_t b, bool tell) {
     const uint32_t old_len = seq_len(a.c, b, tell ? a.status : nullptr);
     const int32_t asked = a.arg[b];
     const uint32_t new_len = asked < 0 ? 0 : min((uint32_t)asked, a.c.max_len);
     if (tell && (int32_t)new_len != asked) report(a.status, SPLITZIP_KV_BAD_LEN);
-    const uint32_t need = pages_for(a.c, new_len);
-    return Want{need, need, kNoPage, old_len, new_len, 0, 0, 0};
+    return Want{pages_for(a.c, min(old_len, new_len)), pages_for(a.c, new_len), kNoPage, old_len, new_len, 0, 0, 0};
 }
+
+// The page that is begun and will be written, whose writers are counted.
 __device__ inline void begin_writing(const PageArgs &a, uint32_t b, const int32_t *row, Want &w) {
     const uint32_t at = div(w.old_len, a.c.page);
-    if (w.new_len <= w.old_len || w.old_len == at * a.c.page.d) return;      // else `at` is below need
+    if (w.new_len <= w.old_len || w.old_len == at * a.c.page.d) return;      // else `at` is kept
     const uint32_t page = (uint32_t)row[at];
     if (page < a.c.num_pages) {
         w.page = page;
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void k_want(PageArgs a, uint32_t width) {
     if (b >= a.c.batch) return;
     int32_t *row = a.table + b * a.c.table_stride;
     Want w = want_of(a, b, lane == 0);
-    w.first = drop_and_find(a, row, w.need, width);
+    w.first = drop_and_find(a, row, w.first, width);
     if (lane == 0) {
         begin_writing(a, b, row, w);
         a.s.want[b] = w;
@@ -345,8 +348,8 @@ __device__ inline int32_t latest(const int32_t *p) { return __hip_atomic_load(p,
 
 // One workgroup: how many pages the sequences want, each its place among them,
 // and the first so many free pages, in order.  WANT: with what k_want does for
-// up to kChooseThreads sequences, a thread each where a sequence drops or
-// misses a page at most (a step's tokens), else a wave.  (64 sequences with 8
+// up to kChooseThreads sequences, a thread each where a sequence drops a page
+// at most (a step's tokens), else a wave.  (64 sequences with 8
 // drafts each, given back and made room for: 15.6 us, with k_want 20.8 to 25.5.)
 template <bool WANT>
 __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t width, uint32_t blocks) {
@@ -361,25 +364,24 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
         bool slow = false;
         if (tid < a.c.batch) {
             mine = want_of(a, tid, true);
-            const uint32_t need = mine.need;
-            const int32_t before2 = need > 1 ? row[need - 2] : 0, before1 = need ? row[need - 1] : 0;
-            const int32_t behind1 = need < width ? row[need] : -1, behind2 = need + 1 < width ? row[need + 1] : -1;
+            const uint32_t keep = mine.first;
+            const int32_t before2 = keep > 1 ? row[keep - 2] : 0, before1 = keep ? row[keep - 1] : 0;
+            const int32_t behind1 = keep < width ? row[keep] : -1, behind2 = keep + 1 < width ? row[keep + 1] : -1;
             slow = behind2 >= 0 || (before1 < 0 && before2 < 0);
             if (slow) {
                 s_take[atomicAdd(&s_slow, 1u)] = tid;
             } else {
-                if (before1 < 0) mine.first = need - 1;
+                if (before1 < 0) mine.first = keep - 1;
                 if (behind1 >= 0) {
                     if ((uint32_t)behind1 < a.c.num_pages) drop_name(a.s, behind1, 1);
-                    row[need] = -1;
+                    row[keep] = -1;
                 }
             }
         }
         __syncthreads();
         for (uint32_t i = wave; i < s_slow; i += kChooseThreads / 64) {
             const uint32_t b = s_take[i];
-            const uint32_t need = want_of(a, b, false).need;
-            const uint32_t first = drop_and_find(a, a.table + b * a.c.table_stride, need, width);
+            const uint32_t first = drop_and_find(a, a.table + b * a.c.table_stride, want_of(a, b, false).first, width);
             if (lane == 0) s_before[b] = first;
         }
         __syncthreads();

@@ -128,8 +128,8 @@ class KVPages:
 
     def resize(self, lens: torch.Tensor, status: torch.Tensor | None = None, stream=None) -> None:
         """The sequences' lengths become ``lens`` (int32 [batch]; it may be the
-        cache's own, after an eviction in place).  Pages behind them are freed,
-        then sequences that grow are given pages, the lowest free ones in the
+        cache's own, after an eviction in place).  Pages behind them, or behind
+        an old length that is shorter, are freed, then sequences that grow are given pages, the lowest free ones in the
         order of sequences; one that grows within a page that others name is
         given a copy of it (in every layer) first; where all that name it grow,
         the first of them keeps it.  The new tokens are the caller's to append.

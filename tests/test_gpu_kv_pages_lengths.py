@@ -1,0 +1,126 @@
+"""Lengths that change in the caches between two calls of the page operators (an
+eviction in place, tokens taken back): whatever a fork has shared before,
+``resize`` leaves no page that a sequence is about to write to another."""
+import random
+
+import pytest
+import torch
+
+import lossless_bf16_tensor_splitzip_amd as S
+from kv_pages_reference import NO_PAGE, Pool
+from test_gpu_kv_pages import Made, ints
+from test_gpu_parity import DEV, _say
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module(module):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+class Cut(Pool):
+    """A resize frees what lies behind the old length, too."""
+
+    def resize(self, lens):
+        most = len(self.table[0]) * self.page
+        old = list(self.lens)
+        for row, was, n in zip(self.table, self.lens, lens):
+            keep = self.need(min(was, max(n, 0), most))
+            row[keep:] = [-1] * (len(row) - keep)
+        super().resize(lens)
+        refs = self.refs()
+        for row, was, n in zip(self.table, old, self.lens):        # what will be written is one sequence's
+            assert all(refs[p] == 1 for p in row[was // self.page:self.need(n)] if n > was)
+
+
+def made(*args, **kw):
+    m = Made(*args, **kw)
+    m.ref.__class__ = Cut
+    m.count()
+    return m
+
+
+def set_lens(m, lens):
+    m.lens.copy_(ints(lens))
+    m.ref.lens = list(lens)
+
+
+# `far` sequences of no tokens between the others: more than one workgroup plans
+@pytest.mark.parametrize("far", [0, 1100])
+@pytest.mark.parametrize("cut,grown", [(20, 36), (16, 17), (17, 18), (0, 1), (0, 40), (32, 48), (31, 33), (40, 41)])
+def test_cut_forked_grown(cut, grown, far):
+    _say("cut to %d, forked, grown to %d, %d sequences between" % (cut, grown, far))
+    between = [0] * far
+    m = made([40] + between + [0], 12, 16, 3, layers=2, kv_heads=2)
+    set_lens(m, [cut] + between + [0])
+    m.fork([0] + list(range(1, far + 1)) + [0])
+    m.check("forked")
+    m.resize([grown] + between + [grown])
+    m.check("grown")
+    assert m.ref.status == 0
+
+
+@pytest.mark.parametrize("far", [0, 1100])
+@pytest.mark.parametrize("cut,grown", [(32, 33), (30, 33), (32, 160), (7, 8), (0, 1), (0, 160), (144, 145), (159, 160)])
+def test_forked_cut_grown(cut, grown, far):
+    _say("forked, one cut to %d and grown to %d, %d sequences between" % (cut, grown, far))
+    between = [0] * far
+    m = made([160] + between + [0], 30, 16, 10, layers=2, kv_heads=2)
+    m.fork([0] + list(range(1, far + 1)) + [0])
+    set_lens(m, [160] + between + [cut])
+    m.resize([160] + between + [grown])
+    m.check((cut, grown))
+    assert m.ref.status == 0
+
+
+def test_evicted_forked_grown():
+    """By an eviction, with the tokens that are appended behind it."""
+    _say("evicted in place, forked, grown")
+    m = made([40, 0, 25], 14, 16, 3, kv_heads=2, dim=64)
+    cache = m.caches[0]
+    mass = torch.rand(3, 2, 48, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    cache.evict(mass, 20)
+    m.ref.lens = [20, 0, 20]
+    m.fork([0, 0, 2])
+    m.resize([36, 37, 21])
+    torch.cuda.synchronize()
+    assert m.lens.tolist() == m.ref.lens and m.table.tolist() == m.ref.table and m.pages.refs.tolist() == m.ref.refs()
+    cu = ints([0, 16, 33, 34])
+    k = torch.randn(34, 2, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    cache.append(k, -k, cu, status=m.status)
+    got, back = torch.zeros_like(k), torch.zeros_like(k)
+    cache.gather(got, back, cu, status=m.status)
+    torch.cuda.synchronize()
+    assert int(m.status) == 0
+    assert torch.equal(got, k) and torch.equal(back, -k)
+
+
+@pytest.mark.parametrize("page", [1, 3, 16])
+@pytest.mark.parametrize("batch", [4, 33])
+def test_walks_with_cuts(batch, page):
+    """Forks, growth and cuts in place in any order; pools that sometimes run out."""
+    _say("walk with cuts, batch=%d page=%d" % (batch, page))
+    rng = random.Random(batch * 10 + page)
+    most = 60
+    lens = [rng.randint(0, most) for _ in range(batch)]
+    pages = sum(-(-n // page) for n in lens) + 10 + batch * (most // page) // 3
+    m = made(lens, pages, page, -(-most // page), layers=2, kv_heads=2, dim=16, layout="nhd", seed=page)
+    for step in range(40):
+        kind = rng.choice(["fork", "cut", "cut", "grow", "grow", "any", "own", "compact"])
+        if kind == "fork":
+            m.fork([rng.choice([b, b, rng.randrange(batch), -1]) for b in range(batch)])
+        elif kind == "cut":
+            set_lens(m, [rng.choice([n, max(0, n - rng.choice([1, 5, 30]))]) for n in m.ref.lens])
+        elif kind == "grow":
+            more = rng.choice([1, 1, 5, 40])
+            m.resize([min(most, n + (rng.random() < 0.8) * more) for n in m.ref.lens])
+        elif kind == "any":
+            m.resize([rng.choice([n, rng.randint(0, most)]) for n in m.ref.lens])
+        elif kind == "own":
+            m.pages.resize(m.lens, status=m.status)
+            m.ref.resize(list(m.ref.lens))
+        else:
+            m.compact()
+        m.check("%d %s" % (step, kind))
+    assert m.ref.status in (0, NO_PAGE)
