@@ -281,7 +281,11 @@ int splitzip_kv_pages_fork(const splitzip_kv_pages *pages, const int32_t *parent
  * pages hold, or stays as it was if its copy could not be had, or if it would
  * have kept a page that another still reads because that one's copy could not
  * be had (SPLITZIP_KV_NO_PAGE).  The tokens from the old length on are the
- * caller's to append. */
+ * caller's to append.  The old length is the cache's, or, where that was made
+ * greater in place since (lens += 1, and then resized to itself), the one that
+ * the last of these calls left.  Between two of them a length is cut in place or
+ * made greater, not the one and then the other: a growth back over pages that
+ * others name is not seen. */
 int splitzip_kv_pages_resize(const splitzip_kv_pages *pages, const int32_t *lens, int32_t *d_status, void *stream);
 
 /* Compact: with n pages in use, the pages in use from n on move to the free

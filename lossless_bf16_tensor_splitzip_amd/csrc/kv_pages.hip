@@ -30,7 +30,7 @@ struct Want {
     uint32_t old_len, new_len;
     uint32_t before;          // pages wanted by the sequences before it
     uint32_t copies;          // 1: the begun page is shared, a copy is wanted before the entries
-    uint32_t reserved;
+    uint32_t slots;           // in use of the begun page; before one is found, the cache's length
 };
 constexpr uint32_t kNoPage = 0xffffffffu;
 
@@ -43,6 +43,7 @@ struct State {
     uint32_t *rank;           // [pages] a moved page's place in from
     uint32_t *words;          // 0: pages in use; 1: moves; 2: pages given; 3: pages wanted
     Want *want;               // [batch]
+    int32_t *left;            // [batch] lengths as the last call left them
 };
 
 struct PageArgs {
@@ -120,7 +121,9 @@ __global__ __launch_bounds__(kThreads) void k_clear(PageArgs a) {
 __global__ __launch_bounds__(kThreads) void k_names(PageArgs a, uint32_t width, uint32_t parts) {
     for (uint32_t w = blockIdx.x; w < a.c.batch * parts; w += gridDim.x) {
         const uint32_t b = w / parts, part = w - b * parts;
-        const uint32_t held = pages_for(a.c, seq_len(a.c, b, part == 0 && threadIdx.x == 0 ? a.status : nullptr));
+        const bool first = part == 0 && threadIdx.x == 0;
+        const uint32_t len = seq_len(a.c, b, first ? a.status : nullptr), held = pages_for(a.c, len);
+        if (first) a.s.left[b] = (int32_t)len;
         int32_t *row = a.table + b * a.c.table_stride;
         for (uint32_t i = part * kThreads + threadIdx.x; i < width; i += parts * kThreads) {
             const uint32_t page = (uint32_t)row[i];
@@ -156,6 +159,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_count(PageArgs a, uint32_t wi
     __shared__ int32_t n[kSmallPages];
     const uint32_t tid = threadIdx.x;
     for (uint32_t p = tid; p < a.c.num_pages; p += kSmallThreads) n[p] = 0;
+    for (uint32_t b = tid; b < a.c.batch; b += kSmallThreads) a.s.left[b] = (int32_t)seq_len(a.c, b);
     __syncthreads();
     for (uint32_t i = tid; i < a.c.batch * width; i += kSmallThreads) {
         const uint32_t b = i / width, at = i - b * width;
@@ -229,11 +233,11 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t widt
         was[u] = next[u] = -1;
         if (!mine || b >= batch) continue;
         const int32_t parent = parent_of(b);
-        if (!is_lens) was[u] = a.table[b * a.c.table_stride + i];
+        if (is_lens) next[u] = parent < 0 ? 0 : a.c.lens[parent];
+        else was[u] = a.table[b * a.c.table_stride + i];
         if (parent == (int32_t)b) continue;
         changed |= 1ull << u;
-        if (is_lens) next[u] = parent < 0 ? 0 : a.c.lens[parent];
-        else if (parent >= 0) next[u] = a.table[parent * a.c.table_stride + i];
+        if (!is_lens && parent >= 0) next[u] = a.table[parent * a.c.table_stride + i];
     }
     __syncthreads();
     if (!is_lens) {
@@ -256,11 +260,13 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t widt
             else if (add[u] && before[u] == 0) atomicSub(&a.s.free_in[(uint32_t)was[u] / kBlock], 1);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+        if (is_lens && b0 + u < batch) a.s.left[b0 + u] = next[u];
         if (changed >> u & 1) {
             if (is_lens) a.c.lens[b0 + u] = next[u];
             else a.table[(b0 + u) * a.c.table_stride + i] = next[u];
         }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -293,13 +299,15 @@ __device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32
     return 0;
 }
 
-// Lengths asked for and old, and what is kept (in `first`).
+// Lengths asked for and old, and what is kept (in `first`).  A sequence that was
+// made longer in the cache (lens += 1 before the call) grows from the length that
+// the last call left: what lies behind is written after this one.
 __device__ inline Want want_of(const PageArgs &a, uint32_t b, bool tell) {
-    const uint32_t old_len = seq_len(a.c, b, tell ? a.status : nullptr);
+    const uint32_t len = seq_len(a.c, b, tell ? a.status : nullptr);
     const int32_t asked = a.arg[b];
     const uint32_t new_len = asked < 0 ? 0 : min((uint32_t)asked, a.c.max_len);
     if (tell && (int32_t)new_len != asked) report(a.status, SPLITZIP_KV_BAD_LEN);
-    return Want{pages_for(a.c, min(old_len, new_len)), pages_for(a.c, new_len), kNoPage, old_len, new_len, 0, 0, 0};
+    return Want{pages_for(a.c, min(len, new_len)), pages_for(a.c, new_len), kNoPage, min(len, (uint32_t)a.s.left[b]), new_len, 0, 0, len};
 }
 
 // The page that is begun and will be written, whose writers are counted.
@@ -309,6 +317,7 @@ __device__ inline void begin_writing(const PageArgs &a, uint32_t b, const int32_
     const uint32_t page = (uint32_t)row[at];
     if (page < a.c.num_pages) {
         w.page = page;
+        w.slots = min(w.slots - at * a.c.page.d, a.c.page.d);
         atomicAdd(&a.s.writers[page], 1);
         atomicMin(&a.s.lowest[page], (int32_t)b);
     } else {
@@ -502,7 +511,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, 
                 len = w.old_len;
             }
             if (got < n || kept || (w.copies && !copied)) report(a.status, SPLITZIP_KV_NO_PAGE);
-            a.c.lens[b] = (int32_t)len;
+            a.c.lens[b] = a.s.left[b] = (int32_t)len;
             if (w.page != kNoPage) {
                 a.s.writers[w.page] = 0;
                 a.s.lowest[w.page] = 0x7fffffff;
@@ -511,8 +520,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, 
     }
     if (!copied) return;
     const uint64_t step = pool & 1 ? page_v : page_k;
-    copy_page<8>(pools.p[pool] + w.page * step, pools.p[pool] + copy * step, pool & 1 ? gv : gk,
-                 w.old_len - div(w.old_len, a.c.page) * a.c.page.d);
+    copy_page<8>(pools.p[pool] + w.page * step, pools.p[pool] + copy * step, pool & 1 ? gv : gk, w.slots);
 }
 
 // ---------------------------------------------------------------------------
@@ -658,7 +666,9 @@ size_t place_state(const splitzip_kv_cache *c, void *base, State &s) {
     s.want = reinterpret_cast<Want *>(p + 6 * n + 16);
     size_t at = 6 * n + 16 + sizeof(Want) * (size_t)c->batch;
     s.free_in = reinterpret_cast<int32_t *>(p + at);
-    return at + up16(4 * (size_t)blocks_of(c->num_pages));
+    at += up16(4 * (size_t)blocks_of(c->num_pages));
+    s.left = reinterpret_cast<int32_t *>(p + at);
+    return at + up16(4 * (size_t)c->batch);
 }
 
 // The pools alone: shape, strides, alignment, reach.

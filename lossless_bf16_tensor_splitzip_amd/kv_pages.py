@@ -135,7 +135,13 @@ class KVPages:
         the first of them keeps it.  The new tokens are the caller's to append.
         With no page left a sequence gets as long as its pages hold, and stays
         as it was where the page it would write in is still another's
-        (KV_NO_PAGE; compare ``lens`` of the cache)."""
+        (KV_NO_PAGE; compare ``lens`` of the cache).
+
+        A length that was made greater in place (``lens += 1``, then
+        ``resize(lens)``) grows from the one that the last call here left.
+        Between two calls a length may be cut in place or made greater, not cut
+        and then made greater: that it grew back over pages that others name
+        is not seen."""
         self._ready()
         first = self.caches[0]
         own = lens.data_ptr() == first.args.lens and first.batch > 0

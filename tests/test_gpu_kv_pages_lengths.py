@@ -1,6 +1,6 @@
 """Lengths that change in the caches between two calls of the page operators (an
-eviction in place, tokens taken back): whatever a fork has shared before,
-``resize`` leaves no page that a sequence is about to write to another."""
+eviction in place, tokens taken back, lens += 1): whatever a fork has shared
+before, ``resize`` leaves no page that a sequence is about to write to another."""
 import random
 
 import pytest
@@ -20,18 +20,36 @@ def setup_module(module):
 
 
 class Cut(Pool):
-    """A resize frees what lies behind the old length, too."""
+    """A resize frees what lies behind the length in the cache, too, and a sequence grows from that length or from the
+    one that the last call left."""
+
+    def count(self):
+        super().count()
+        self.left = list(self.lens)
+
+    def fork(self, parents):
+        super().fork(parents)
+        self.left = list(self.lens)
 
     def resize(self, lens):
         most = len(self.table[0]) * self.page
-        old = list(self.lens)
-        for row, was, n in zip(self.table, self.lens, lens):
+        now, old = self.lens, [min(n, was) for n, was in zip(self.lens, self.left)]
+        for row, was, n in zip(self.table, now, lens):
             keep = self.need(min(was, max(n, 0), most))
             row[keep:] = [-1] * (len(row) - keep)
+        before = [list(row) for row in self.table]
+        self.lens = list(old)
         super().resize(lens)
         refs = self.refs()
-        for row, was, n in zip(self.table, old, self.lens):        # what will be written is one sequence's
-            assert all(refs[p] == 1 for p in row[was // self.page:self.need(n)] if n > was)
+        for row, had, was, long, n in zip(self.table, before, old, now, self.lens):
+            at = was // self.page
+            if n <= was:
+                continue
+            assert all(refs[p] == 1 for p in row[at:self.need(n)])       # what will be written is one sequence's
+            if was % self.page and row[at] != had[at]:                  # all that the cache says is in use
+                slots = min(long - at * self.page, self.page)
+                self.kv[:, :, row[at], :, :slots] = self.kv[:, :, had[at], :, :slots]
+        self.left = list(self.lens)
 
 
 def made(*args, **kw):
@@ -107,7 +125,7 @@ def test_walks_with_cuts(batch, page):
     pages = sum(-(-n // page) for n in lens) + 10 + batch * (most // page) // 3
     m = made(lens, pages, page, -(-most // page), layers=2, kv_heads=2, dim=16, layout="nhd", seed=page)
     for step in range(40):
-        kind = rng.choice(["fork", "cut", "cut", "grow", "grow", "any", "own", "compact"])
+        kind = rng.choice(["fork", "cut", "cut", "grow", "grow", "longer", "longer", "any", "own", "compact"])
         if kind == "fork":
             m.fork([rng.choice([b, b, rng.randrange(batch), -1]) for b in range(batch)])
         elif kind == "cut":
@@ -115,6 +133,11 @@ def test_walks_with_cuts(batch, page):
         elif kind == "grow":
             more = rng.choice([1, 1, 5, 40])
             m.resize([min(most, n + (rng.random() < 0.8) * more) for n in m.ref.lens])
+        elif kind == "longer":
+            m.ref.lens = list(m.ref.left)
+            set_lens(m, [min(most, n + rng.choice([0, 1, 1, 20])) for n in m.ref.lens])
+            m.pages.resize(rng.choice([m.lens, m.lens.clone()]), status=m.status)
+            m.ref.resize(list(m.ref.lens))
         elif kind == "any":
             m.resize([rng.choice([n, rng.randint(0, most)]) for n in m.ref.lens])
         elif kind == "own":
@@ -124,3 +147,76 @@ def test_walks_with_cuts(batch, page):
             m.compact()
         m.check("%d %s" % (step, kind))
     assert m.ref.status in (0, NO_PAGE)
+
+
+@pytest.mark.parametrize("far", [0, 1100])
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("more,ask", [(1, 0), (12, 0), (13, 0), (40, 0), (1, 5), (20, 1), (3, -2)])
+def test_made_longer_in_place(more, ask, own, far):
+    """lens += 1 comes before the resize: the page that all of them begin is still copied."""
+    _say("longer in place by %d, asked for %d more, own=%s, %d sequences between" % (more, ask, own, far))
+    between = [0] * far
+    m = made([20] + between + [0, 0], 20, 16, 5, layers=2, kv_heads=2)
+    m.fork([0] + list(range(1, far + 1)) + [0, 0])
+    set_lens(m, [20 + more] + between + [20 + more, 20])
+    target = ints([n + ask if n > 20 else n for n in m.ref.lens])
+    if own and not ask:
+        target = m.lens
+    m.ref.resize(target.tolist())
+    m.pages.resize(target, status=m.status)
+    m.check((more, ask))
+    assert m.ref.status == 0 and m.ref.lens == [20 + more + ask] + between + [20 + more + ask, 20]
+
+
+@pytest.mark.parametrize("lens,want", [([4, 2, 3], [3, 1, 2]), ([3, 2, 2], [3, 1, 2]), ([4, 1, 0], [3, 1, 0])])
+def test_longer_in_place_and_no_page(lens, want):
+    """A copy that is not to be had: the length that the last call left, not the one that was written into the cache."""
+    m = made([3, 0, 0], 1, 4, 1, layers=2, kv_heads=2)
+    m.fork([0, 0, 0])
+    m.resize([3, 1, 2])
+    set_lens(m, lens)
+    m.pages.resize(m.lens, status=m.status)
+    m.ref.resize(lens)
+    m.check(lens)
+    assert m.lens.tolist() == want and m.ref.status == NO_PAGE
+
+
+def test_room_that_is_used_later():
+    """Room is made, the length taken back and made longer again as tokens come, without a call; a fork of others, and of
+    that sequence, comes between."""
+    _say("room that is used later")
+    m = made([40, 17, 0], 20, 16, 6, kv_heads=2, dim=64)
+    cache, rows = m.caches[0], torch.randn(96, 2, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(DEV)
+    m.pages.resize(ints([90, 17, 0]))
+
+    def append(first, last, sequence=0):
+        cu = [0] * (sequence + 1) + [last - first] * (3 - sequence)
+        cache.lens[sequence] = last
+        cache.append(rows[first:last], -rows[first:last], ints(cu), status=m.status)
+
+    def cached(sequence, n):
+        cu = ints([0] * (sequence + 1) + [n] * (3 - sequence))
+        k, v = torch.zeros_like(rows[:n]), torch.zeros_like(rows[:n])
+        cache.gather(k, v, cu, start=ints([0, 0, 0]), status=m.status)
+        assert torch.equal(k, rows[:n]) and torch.equal(v, -rows[:n])
+
+    append(0, 20)
+    append(0, 17, 1)
+    m.pages.fork(ints([0, 1, 1]))             # of another
+    for last in range(21, 42):
+        append(last - 1, last)
+    m.pages.resize(ints([42, 17, 18]))        # in use: none of it goes
+    append(41, 42)
+    append(17, 18, 2)
+    cached(0, 42)
+    cached(1, 17)
+    cached(2, 18)
+    m.pages.fork(ints([0, 0, 2]))             # of this one
+    m.pages.resize(ints([43, 44, 18]))
+    append(42, 43)
+    append(42, 44, 1)
+    cached(0, 43)
+    cached(1, 44)
+    cached(2, 18)
+    torch.cuda.synchronize()
+    assert int(m.status) == 0
