@@ -41,7 +41,7 @@ struct State {
     uint32_t *list;           // [pages] free pages, ascending
     uint32_t *from;           // [pages] pages to be moved, from the top
     uint32_t *rank;           // [pages] a moved page's place in from
-    uint32_t *words;          // 0: pages in use; 1: moves; 2: pages given; 3: pages wanted
+    uint32_t *words;          // 0: pages in use; 1: moves; 2: pages given; 3: pages wanted; 4: 1 if rows have gaps
     Want *want;               // [batch]
     int32_t *left;            // [batch] lengths as the last call left them
 };
@@ -115,6 +115,7 @@ __global__ __launch_bounds__(kThreads) void k_clear(PageArgs a) {
         a.s.writers[p] = 0;
         a.s.lowest[p] = 0x7fffffff;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.s.words[4] = 0;
 }
 
 // A row's entries within the sequence's length name their pages, those behind it none.
@@ -130,7 +131,10 @@ __global__ __launch_bounds__(kThreads) void k_names(PageArgs a, uint32_t width, 
             if (i < held && page < a.c.num_pages) {
                 atomicAdd(&a.s.refs[page], 1);
             } else {
-                if (i < held) report(a.status, SPLITZIP_KV_BAD_PAGE);
+                if (i < held) {
+                    report(a.status, SPLITZIP_KV_BAD_PAGE);
+                    a.s.words[4] = 1;
+                }
                 row[i] = -1;
             }
         }
@@ -157,7 +161,9 @@ constexpr int kSmallThreads = 1024;
 // rows of 13 entries: one launch instead of three).
 __global__ __launch_bounds__(kSmallThreads) void k_count(PageArgs a, uint32_t width) {
     __shared__ int32_t n[kSmallPages];
+    __shared__ uint32_t s_gaps;
     const uint32_t tid = threadIdx.x;
+    if (tid == 0) s_gaps = 0;
     for (uint32_t p = tid; p < a.c.num_pages; p += kSmallThreads) n[p] = 0;
     for (uint32_t b = tid; b < a.c.batch; b += kSmallThreads) a.s.left[b] = (int32_t)seq_len(a.c, b);
     __syncthreads();
@@ -169,11 +175,15 @@ __global__ __launch_bounds__(kSmallThreads) void k_count(PageArgs a, uint32_t wi
         if (at < held && page < a.c.num_pages) {
             atomicAdd(&n[page], 1);
         } else {
-            if (at < held) report(a.status, SPLITZIP_KV_BAD_PAGE);
+            if (at < held) {
+                report(a.status, SPLITZIP_KV_BAD_PAGE);
+                s_gaps = 1;
+            }
             *entry = -1;
         }
     }
     __syncthreads();
+    if (tid == 0) a.s.words[4] = s_gaps;
     for (uint32_t p = tid; p < a.c.num_pages; p += kSmallThreads) {
         a.s.refs[p] = n[p];
         a.s.writers[p] = 0;
@@ -279,7 +289,9 @@ __global__ __launch_bounds__(kForkThreads) void k_fork(PageArgs a, uint32_t widt
 // Pages are held from a row's start without a gap, so what a sequence drops and
 // misses is looked for from the border of what it keeps.  A wave looks at 64
 // entries a time: drops those behind, and returns the first that is missing.
-__device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32_t keep, uint32_t width) {
+// Where the count found page numbers outside the pool rows may have gaps, and all
+// that lies behind is looked at.
+__device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32_t keep, uint32_t width, bool gaps) {
     const uint32_t lane = threadIdx.x & 63;
     for (uint32_t i0 = keep; i0 < width; i0 += 64) {
         const int32_t page = i0 + lane < width ? row[i0 + lane] : -1;
@@ -287,7 +299,7 @@ __device__ inline uint32_t drop_and_find(const PageArgs &a, int32_t *row, uint32
             if ((uint32_t)page < a.c.num_pages) drop_name(a.s, page, 1);
             row[i0 + lane] = -1;
         }
-        if (!__ballot(page >= 0)) break;
+        if (!gaps && !__ballot(page >= 0)) break;
     }
     uint32_t first = keep;
     while (first) {
@@ -331,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void k_want(PageArgs a, uint32_t width) {
     if (b >= a.c.batch) return;
     int32_t *row = a.table + b * a.c.table_stride;
     Want w = want_of(a, b, lane == 0);
-    w.first = drop_and_find(a, row, w.first, width);
+    w.first = drop_and_find(a, row, w.first, width, a.s.words[4] != 0);
     if (lane == 0) {
         begin_writing(a, b, row, w);
         a.s.want[b] = w;
@@ -370,13 +382,14 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
         if (tid == 0) s_slow = 0;
         __syncthreads();
         int32_t *row = a.table + tid * a.c.table_stride;
+        const bool gaps = a.s.words[4] != 0;
         bool slow = false;
         if (tid < a.c.batch) {
             mine = want_of(a, tid, true);
             const uint32_t keep = mine.first;
             const int32_t before2 = keep > 1 ? row[keep - 2] : 0, before1 = keep ? row[keep - 1] : 0;
             const int32_t behind1 = keep < width ? row[keep] : -1, behind2 = keep + 1 < width ? row[keep + 1] : -1;
-            slow = behind2 >= 0 || (before1 < 0 && before2 < 0);
+            slow = gaps || behind2 >= 0 || (before1 < 0 && before2 < 0);
             if (slow) {
                 s_take[atomicAdd(&s_slow, 1u)] = tid;
             } else {
@@ -390,7 +403,7 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
         __syncthreads();
         for (uint32_t i = wave; i < s_slow; i += kChooseThreads / 64) {
             const uint32_t b = s_take[i];
-            const uint32_t first = drop_and_find(a, a.table + b * a.c.table_stride, want_of(a, b, false).first, width);
+            const uint32_t first = drop_and_find(a, a.table + b * a.c.table_stride, want_of(a, b, false).first, width, gaps);
             if (lane == 0) s_before[b] = first;
         }
         __syncthreads();
@@ -663,8 +676,8 @@ size_t place_state(const splitzip_kv_cache *c, void *base, State &s) {
     s.from = reinterpret_cast<uint32_t *>(p + 4 * n);
     s.rank = reinterpret_cast<uint32_t *>(p + 5 * n);
     s.words = reinterpret_cast<uint32_t *>(p + 6 * n);
-    s.want = reinterpret_cast<Want *>(p + 6 * n + 16);
-    size_t at = 6 * n + 16 + sizeof(Want) * (size_t)c->batch;
+    s.want = reinterpret_cast<Want *>(p + 6 * n + 32);
+    size_t at = 6 * n + 32 + sizeof(Want) * (size_t)c->batch;
     s.free_in = reinterpret_cast<int32_t *>(p + at);
     at += up16(4 * (size_t)blocks_of(c->num_pages));
     s.left = reinterpret_cast<int32_t *>(p + at);

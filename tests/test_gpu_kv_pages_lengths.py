@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import lossless_bf16_tensor_splitzip_amd as S
-from kv_pages_reference import NO_PAGE, Pool
+from kv_pages_reference import BAD_PAGE, NO_PAGE, Pool
 from test_gpu_kv_pages import Made, ints
 from test_gpu_parity import DEV, _say
 
@@ -220,3 +220,27 @@ def test_room_that_is_used_later():
     cached(2, 18)
     torch.cuda.synchronize()
     assert int(m.status) == 0
+
+
+@pytest.mark.parametrize("far", [0, 1100])
+@pytest.mark.parametrize("gap,width", [((1, 3), 5), ((2, 4), 5), ((1, 70), 100), ((3, 90), 100), ((0, 65), 200)])
+def test_rows_with_gaps(gap, width, far):
+    """Page numbers outside the pool leave gaps in a row; what is behind them is freed all the same."""
+    _say("a row without its entries %d to %d, %d sequences between" % (gap[0], gap[1] - 1, far))
+    between, page = [0] * far, 4
+    lens = [page * (width - 1)] + between + [7]
+    m = Made(lens, 2 * width + 5, page, width, layers=2)
+    m.ref.__class__ = Cut
+    for i in range(*gap):
+        m.ref.table[0][i] = -1 if i % 2 else 1 << 20
+    m.table.copy_(ints(m.ref.table))
+    m.count()
+    m.check("counted")
+    assert m.ref.status == BAD_PAGE
+    m.fork([0] + list(range(1, far + 1)) + [0])
+    for n in (lens[0] - 1, page * gap[1] + 2, page * gap[0] + 1, page * gap[0] + 3, page, 1, 0, 2 * page + 1):
+        m.resize([n] + between + [max(0, n - 3)])
+        m.check(n)
+    m.count()
+    assert sum(m.ref.refs()) == m.ref.need(2 * page + 1) + m.ref.need(2 * page - 2)
+    m.check("counted again")
