@@ -198,7 +198,9 @@ int splitzip_kv_attend(const splitzip_kv_cache *cache, const splitzip_kv_query *
  * a `to` that shares its table or lens or a pool's start with the cache is
  * taken as in place and must be equal to it in all fields.  Its K and V pools
  * share no memory in place.  to's table must
- * hold budget tokens, or its width the whole cache's.
+ * hold budget tokens, or its width the whole cache's.  Caches of several layers
+ * that have one lens: in place the first call sets it, and what it was is put
+ * back before each further one.
  * Errors: INVALID (also sinks + recent > budget, budget 0), HIP. */
 int splitzip_kv_evict(const splitzip_kv_cache *cache, const splitzip_kv_cache *to,
                       const splitzip_kv_budget *budget, int32_t *d_status, void *stream);

@@ -461,7 +461,13 @@ class KVCache:
         share no memory with this cache; ``lens`` (of ``to``) becomes
         min(length, budget), and the mass moves along (in place, or into
         ``mass_out``), 0 behind it.  Returns ``kept``, int32 [batch, kv_heads,
-        budget]: the old position of each kept token, -1 behind them."""
+        budget]: the old position of each kept token, -1 behind them.
+
+        Caches of several layers with one ``lens`` (``KVPages``): the first
+        eviction in place sets it, so put the lengths back before each further
+        layer (``lens.copy_(before)``), or that one finds nothing to evict; then
+        ``KVPages.resize(lens)`` frees the pages behind them.  In place, pages
+        are written: none that several sequences name (after a fork)."""
         if budget < 1 or budget >= 1 << 31 or sinks < 0 or recent < 0 or sinks + recent > budget:
             raise ValueError("the budget %d must be positive and hold %d sinks and %d recent tokens"
                              % (budget, sinks, recent))

@@ -141,7 +141,8 @@ class KVPages:
         ``resize(lens)``) grows from the one that the last call here left.
         Between two calls a length may be cut in place or made greater, not cut
         and then made greater: that it grew back over pages that others name
-        is not seen."""
+        is not seen.  Layers are evicted from in place one after another, each
+        with the lengths of before put back (see ``KVCache.evict``)."""
         self._ready()
         first = self.caches[0]
         own = lens.data_ptr() == first.args.lens and first.batch > 0

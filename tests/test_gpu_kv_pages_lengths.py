@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import lossless_bf16_tensor_splitzip_amd as S
+import kv_reference as R
 from kv_pages_reference import BAD_PAGE, NO_PAGE, Pool
 from test_gpu_kv_pages import Made, ints
 from test_gpu_parity import DEV, _say
@@ -244,3 +245,36 @@ def test_rows_with_gaps(gap, width, far):
     m.count()
     assert sum(m.ref.refs()) == m.ref.need(2 * page + 1) + m.ref.need(2 * page - 2)
     m.check("counted again")
+
+
+def test_layers_evicted():
+    """In place, one layer after another with the lengths of before; then the pages behind are free, and the samples of a
+    sequence go on in pages of their own."""
+    _say("layers evicted in place")
+    lens, budget, kvh, dim = [90, 33, 50, 0], 40, 2, 64
+    m = made(lens, 24, 16, 6, layers=3, kv_heads=kvh, dim=dim)
+    gen = torch.Generator().manual_seed(4)
+    old, masses = m.ref.kv.clone(), [torch.rand(4, kvh, 96, generator=gen) for _ in m.caches]
+    table = [list(r) for r in m.ref.table]
+    before = m.lens.clone()
+    for c, mass in zip(m.caches, masses):
+        m.lens.copy_(before)
+        c.evict(mass.to(DEV), budget, sinks=2, recent=5, status=m.status)
+    short = [min(n, budget) for n in lens]
+    m.pages.resize(m.lens, status=m.status)
+    m.pages.fork(ints([0, 1, 2, 0]), status=m.status)
+    m.pages.resize(ints([41, 33, 40, 47]), status=m.status)
+    torch.cuda.synchronize()
+    assert int(m.status) == 0
+    assert m.pages.refs.sum().item() == sum(m.ref.need(n) for n in [41, 33, 40, 47])
+    now, kv = m.table.tolist(), m.kv.cpu()
+    for i, mass in enumerate(masses):
+        for b, parent in enumerate([0, 1, 2, 0]):
+            n = lens[parent]
+            for h in range(kvh):
+                kept = R.evict(mass[parent, h], n, budget, 2, 5) if n > budget else range(n)
+                assert len(kept) == short[parent]
+                for to, t in enumerate(kept):
+                    want = old[i, :, table[parent][t // 16], h, t % 16]
+                    got = kv[i, :, now[b][to // 16], h, to % 16]
+                    assert torch.equal(want.view(torch.int16), got.view(torch.int16)), (i, b, h, to)
