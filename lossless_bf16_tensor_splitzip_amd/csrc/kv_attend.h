@@ -851,9 +851,17 @@ struct AttendPlan {
 // registers of k_attend decide.  16 sequences of 8192 tokens, 8 KV heads, us with
 // 256, 512, 768 and 1024 runs: dim 64 71, 54, 52, 57; dim 128 96, 91, 94, 92;
 // dim 256 171, 175, 185, 185; 2 sequences, dim 256 31, 36, 43, 48.
-inline uint32_t runs_for(uint32_t dim, uint32_t blocks) {
+constexpr uint32_t runs_for(uint32_t dim, uint32_t blocks) {
     return dim <= 64 ? (blocks == 1 ? 768 : blocks == 2 ? 512 : 256) : dim <= 128 && blocks == 1 ? 512 : 256;
 }
+constexpr uint32_t most_runs() {
+    uint32_t most = 0;
+    for (uint32_t dim = 64; dim <= 256; dim += 64)
+        for (uint32_t blocks = 1; blocks <= 4; blocks *= 2)
+            if (runs_for(dim, blocks) > most) most = runs_for(dim, blocks);
+    return most;
+}
+static_assert(most_runs() <= kMaxRuns, "a query head's shares fit the joins");
 
 inline bool attend_plan(const splitzip_kv_cache *c, uint32_t heads, uint32_t mass_len, AttendPlan &p) {
     if (heads == 0 || heads > SPLITZIP_KV_MAX_HEADS || heads % c->kv_heads) return false;

@@ -22,15 +22,13 @@ namespace {
 
 constexpr int kSharedWaves = 4, kSharedThreads = 64 * kSharedWaves;
 constexpr uint32_t kRows = 32 * kSharedWaves;      // query rows a workgroup of k_shared takes
-// Runs of k_shared: as many as are resident.  One writes up to 128 rows of
-// shares of every row tile that it has part of, which few tokens do not repay
-// (8 KV heads of 128, 128 query rows each, us with runs of at least 1, 2, 4 and 8
-// tiles: 1024 tokens 26, 25, 27 and 33, 4096 39, 33, 32 and 36, 12000 48, 49, 40
-// and 44).
-constexpr uint32_t kSharedRuns = 512;
+constexpr uint32_t kSharedRuns = 512;  // of k_shared: as many as are resident (wide heads: half of that)
 constexpr uint32_t kGroupsHere = 2048; // groups that k_both holds in LDS
-
-constexpr uint32_t kLeast = 4;         // tiles of a run, at least
+// Tiles of a run, at least: one writes up to 128 rows of shares of every row
+// tile that it has part of, which few tokens do not repay (8 KV heads of 128, 128
+// query rows each, us with runs of at least 1, 2, 4 and 8 tiles: 1024 tokens 26,
+// 25, 27 and 33, 4096 39, 33, 32 and 36, 12000 48, 49, 40 and 44).
+constexpr uint32_t kLeast = 4;
 
 // Tokens that k_shared's workgroups take at a time: 16 KB of K and of V, or less.
 constexpr int tile_tokens(int dp) { return dp <= 128 ? 64 : 32; }
@@ -750,7 +748,9 @@ __global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(Sh
 // join
 // ---------------------------------------------------------------------------
 
-constexpr uint32_t kMaxShares = kSharedRuns + 1024;      // of a query head: runs of both launches
+// Shares of a query head: of its group's tokens, from k_shared or k_both, and of
+// its own, from k_both; a run has one of each at most.
+constexpr uint32_t kMaxOwn = most_runs(), kMaxOf = kSharedRuns > kMaxOwn ? kSharedRuns : kMaxOwn;
 constexpr uint32_t kJoinWaves = kJoinThreads / 64;
 constexpr int kAhead = 12;                               // shares a thread loads before their weights are known
 
@@ -772,8 +772,8 @@ struct HeadShares {
         const u32x4 of = ((const u32x4 *)a.of_notes)[pair * a.of.parts + of_part];
         const u32x4 alone = ((const u32x4 *)a.alone_notes)[pair * a.alone.parts + alone_part];
         // (bounded, where arguments that changed meanwhile left notes unwritten)
-        n0 = alone[3] ? min(of[2], kMaxShares / 2) : 0;
-        n = n0 + min(alone[2], kMaxShares / 2);
+        n0 = alone[3] ? min(of[2], kMaxOf) : 0;
+        n = n0 + min(alone[2], kMaxOwn);
         const uint32_t of_row = in_group - of_part * a.of.rows, alone_row = in_group - alone_part * a.alone.rows;
         of_first = of[0] + of_row, of_rest = of[1] + of_row, of_step = j.of_step;
         alone_first = alone[0] + alone_row, alone_rest = alone[1] + alone_row, alone_step = j.alone_step;
@@ -816,7 +816,7 @@ __device__ inline void weigh(const float *shares_ml, const HeadShares &sh, float
 // with 13 and more, a workgroup each 5.2, four a workgroup 12.9.)
 template <bool BF16>
 __global__ __launch_bounds__(kJoinThreads) void k_join_shared(JoinArgs j) {
-    __shared__ float s_w[kMaxShares];
+    __shared__ float s_w[kMaxOf + kMaxOwn];
     __shared__ f32x4 s_o[kJoinThreads];
     __shared__ float s_top, s_sum;
     __shared__ bool s_many[kJoinWaves];
@@ -900,7 +900,7 @@ struct SharedPlan {
     bool apart, whole;                                  // k_both has all tokens of every sequence; by a workgroup for each KV head
     Tiling of, alone;
     uint32_t most;                                      // units of the groups' tokens, at most
-    uint32_t of_slots, of_whole, both_slots, alone_whole, rows, slot_rows;
+    uint32_t of_whole, both_slots, alone_whole, rows, slot_rows;
     size_t from_at, of_notes_at, alone_notes_at, ml_at, o_at, bytes;
 };
 
@@ -935,7 +935,6 @@ bool lay_out(const splitzip_kv_cache *c, uint32_t heads, bool many, uint32_t mos
     const uint64_t per = (uint64_t)batch * heads, of_slots = (uint64_t)p.shared_runs * 2 * p.of.rows,
                    both_slots = (uint64_t)p.both_runs * 2 * p.slot_rows, rows = of_slots + both_slots + 2 * per;
     if (rows >> 31) return false;
-    p.of_slots = 0;
     p.of_whole = (uint32_t)of_slots;
     p.both_slots = p.of_whole + (uint32_t)per;
     p.alone_whole = p.both_slots + (uint32_t)both_slots;
@@ -1090,7 +1089,7 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
         a.from = reinterpret_cast<uint32_t *>(ws + P.from_at);
         a.runs = P.shared_runs;
         a.by_runs = make_div(a.runs);
-        a.slots = P.of_slots;
+        a.slots = 0;
         a.slot_rows = P.of.rows;
         if (bf16) launch_shared<true>(a, s);
         else launch_shared<false>(a, s);
