@@ -202,7 +202,10 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = EXACT ? DP : a.c.dim, kvh = a.c.kv_heads;
     int32_t *status0 = blockIdx.x == 0 ? a.status : nullptr;
-    const uint32_t groups = a.from ? 0 : a.groups;       // that are looked up here
+    const bool unseen = APART && a.groups > kGroupsHere;      // more than are looked up: every sequence on its own
+    const uint32_t groups = a.from || unseen ? 0 : a.groups;  // that are looked up here
+    if (unseen && status0)
+        for (uint32_t g = tid; g < a.groups; g += kAttendThreads) group_of(a, g, status0);
 
     Block64Groups gblk{};
     auto block_of_groups = [&](uint32_t base, uint32_t carry) {
@@ -1084,7 +1087,6 @@ int splitzip_kv_attend_shared(const splitzip_kv_cache *cache, const splitzip_kv_
     // a scale of 0 makes no order of logits, which k_shared goes by: every sequence on its own
     const bool many = P.shared_runs && a.groups && a.scale2 != 0.f;
     const bool apart = P.apart || (P.shared_runs && !many);
-    if (apart && a.groups > kGroupsHere) a.groups = 0;
     if (many) {
         a.from = reinterpret_cast<uint32_t *>(ws + P.from_at);
         a.runs = P.shared_runs;

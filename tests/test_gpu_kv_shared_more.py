@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import kv_shared_reference as H
+from lossless_bf16_tensor_splitzip_amd import _abi
 from test_gpu_kv_shared import check_one, widen
 from test_gpu_parity import _say
 
@@ -24,3 +25,18 @@ def test_every_run_has_a_share():
     check_one(m, None, (), 0)
     assert widen(m)
     check_one(m, None, (), 0)
+
+
+@pytest.mark.parametrize("groups", [2047, 2048, 2049, 65535])
+@pytest.mark.parametrize("scale", [0.0, 0.125])
+def test_findings_in_many_groups(groups, scale):
+    """Ranges that leave the batch or decrease, and fewer than no tokens in common, are reported however many groups there
+    are, also where the scale makes no order of logits."""
+    _say("shared: findings in %d groups, scale %g" % (groups, scale))
+    m = H.make([(100, [120, 100, 130]), (64, [64, 70])], 2, 64, 16, BF16, 4, seed=1)
+    m.cu, m.shared = [0, 3, 5] + [5] * (groups - 2), [100, 64] + [0] * (groups - 2)
+    check_one(m, scale, (), 0)
+    m.shared[-1] = -1
+    check_one(m, scale, (), _abi.KV_BAD_LEN)
+    m.cu[-2:], m.shared[-1] = [6, 5], 0
+    check_one(m, scale, (), _abi.KV_BAD_ROWS)
