@@ -5,7 +5,7 @@ import torch
 
 import kv_shared_reference as H
 from lossless_bf16_tensor_splitzip_amd import _abi
-from test_gpu_kv_shared import check_one, widen
+from test_gpu_kv_shared import check_one, close, widen
 from test_gpu_parity import _say
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +40,18 @@ def test_findings_in_many_groups(groups, scale):
     check_one(m, scale, (), _abi.KV_BAD_LEN)
     m.cu[-2:], m.shared[-1] = [6, 5], 0
     check_one(m, scale, (), _abi.KV_BAD_ROWS)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("dim", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("group", [1, 3, 8, 20])
+def test_weights_that_are_not_rounded(dtype, dim, group):
+    """Where query rows are few the weights of tokens in common are held like the others': bounds without their rounding."""
+    _say("shared: weights in 32 bits, dim=%d group=%d %s" % (dim, group, dtype))
+    m = H.make([(500, [520, 500, 533, 700]), (140, [141, 600])], 2, dim, 16, dtype, 2 * group, seed=dim + group, width=45)
+    common, m.shared = m.shared, [0, 0]
+    want = H.attend(m)
+    m.shared = common
+    out = check_one(m, None, (), 0)
+    for b, (o, tol, _, _) in enumerate(want):
+        close(out[b], o, tol, "out %d" % b)
