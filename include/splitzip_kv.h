@@ -222,12 +222,19 @@ size_t splitzip_kv_groups_struct_size(void);
 size_t splitzip_kv_shared_workspace_size(const splitzip_kv_cache *cache, uint32_t heads, uint32_t groups);
 
 /* What splitzip_kv_attend computes (window ALL, no mass), where K and V of the
- * tokens that a group has in common are read once for all its sequences,
- * through the table row of its first one: the others need only have the same
- * values there, mostly in the same pages.  A sequence that is shorter than the
- * tokens in common attends on its own.  The weights of the tokens in common
- * are rounded to the cache's type once (half a step of it each); all other
- * sums are held as in splitzip_kv_attend.  Ranges that decrease or leave the
+ * tokens that a group has in common are read through the table row of its first
+ * sequence: the others need only have the same values there, mostly in the same
+ * pages.  They are read once for as many query rows of a KV head as a workgroup
+ * takes: 128 of the group's sequences, or 16 or 32 where little would be read
+ * again; by every sequence where those have no room for two of them, or where a
+ * KV head's tokens are few.  A sequence that is shorter than the tokens in common
+ * attends on its own; when the first one ends, so do all, until cu begins a group
+ * with one that goes on.  With 128 rows the weights of the tokens in common are
+ * rounded to the cache's type once (half a step of it each); all other sums, and
+ * those of the other forms, are held as in splitzip_kv_attend.  The form goes by
+ * the shapes, the number of groups and what the table can hold, not by lengths,
+ * which are on the device: a table much wider than its sequences takes the form
+ * for long ones.  Ranges that decrease or leave the
  * batch: BAD_ROWS, no tokens in common (where ranges overlap by that, outputs
  * mean nothing); shared below 0: BAD_LEN, taken as 0.
  * Errors: INVALID (also a window or mass), WORKSPACE, HIP. */

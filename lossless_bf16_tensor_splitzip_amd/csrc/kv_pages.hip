@@ -477,7 +477,7 @@ __global__ __launch_bounds__(kChooseThreads) void k_choose(PageArgs a, uint32_t 
 // with the pool's size wherever it comes from the state.)
 // The chosen pages are entered and the shared ones' slots in use copied, a
 // workgroup for every sequence and pool, of which the first sees to the table.
-// (64 sequences that copy no page 2.6 us; 7 MB of copies in 16 layers 8.2, a chain
+// (64 sequences that copy no page 2.7 us; 7 MB of copies in 16 layers 8 to 9, a chain
 // of three loads in each of 2048 workgroups.)
 __global__ __launch_bounds__(kCopyThreads) void k_give(PageArgs a, Pools pools, Geometry gk, Geometry gv,
                                                        uint64_t page_k, uint64_t page_v, bool first_launch) {

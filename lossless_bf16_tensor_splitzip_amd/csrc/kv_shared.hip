@@ -377,7 +377,7 @@ __global__ __launch_bounds__(kAttendThreads) void k_both(SharedArgs a) {
 // `to` on, without registers.  The compiler does not know of these: what waits
 // for them is written out (until_loads), and the loop that has them under way
 // has no other loads from memory.  (M0 holds the place in LDS, and is read one
-// state after it is written.)
+// state after it is written; the compiler reserves it and keeps nothing in it.)
 __device__ inline uint32_t lds_place(const void *p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
@@ -410,11 +410,16 @@ __device__ inline void meet() {
 // of which the loads alone take 57 and the arithmetic alone 77.  Tiles through
 // registers instead of straight into LDS took 120, 64 rows a wave 165.)
 //
-// The weights enter the second product as one 16-bit number each: with many
-// rows the matrix cores bound this kernel, and a second number would cost half
-// as much again.  The error, half a step of the type for each weight, is as
-// large as that of rounding the output where V has no mean (1.4 times that
-// error together), and smaller where it has (1.18 times there).
+// The weights enter the second product as one 16-bit number each.  A second one
+// is not hidden, though the matrix cores are busy for a quarter of the time only:
+// a wave's loads, products and weights come one after another, and the two waves
+// of a SIMD overlap little of them.  The whole call, us, with one number and with
+// two (64 sequences behind 32768 tokens): bf16 131 and 153, fp16 137 and 167,
+// heads of 64 82 and 99, 2 KV heads of 256 120 and 130.  The error of one, half a
+// step of the type for each weight, is as large as that of rounding the output
+// where V has no mean (1.4 times that error together), and smaller where it has:
+// against 64 bits 0.00197 of the outputs' size, with two numbers 0.00165, what
+// rounding the output alone leaves.
 template <bool BF16, int DP, bool EXACT>
 __global__ __launch_bounds__(kSharedThreads, DP <= 128 ? 2 : 1) void k_shared(SharedArgs a) {
     constexpr int NT = 2;                    // blocks of 16 query rows a wave has

@@ -396,12 +396,17 @@ class KVCache:
         """``attend`` over all cached tokens for a batch whose sequences begin
         alike: sequences cu[g] .. cu[g+1]-1 (``cu`` int32 [groups + 1],
         ascending) have their first ``shared``[g] tokens (int32 [groups], no
-        more than the first of them has) in common, and these are read once for
-        the group, through the table row of its first sequence.  The others
-        need the same values there, as after ``KVPages.fork``; one that is
-        shorter attends on its own, as do sequences outside ``cu``.  The
-        weights of tokens in common are rounded to the cache's type.  ``out``
-        and ``lse`` as in ``attend``."""
+        more than the first of them has) in common, and these are read through
+        the table row of the group's first sequence, once for up to 128 query
+        rows of a KV head where they are many (their weights are rounded to the
+        cache's type then), for 16 or 32 where they are few, by each sequence
+        where those have no room for two.  The others need the same values
+        there, as after ``KVPages.fork``; one that is shorter attends on its
+        own, as do sequences outside ``cu``, and all of a group whose first
+        sequence has ended: begin it with one that goes on.  Which form is
+        taken goes by the shapes, the groups and the table's width, not by the
+        lengths: a table much wider than its sequences gets the form for long
+        ones.  ``out`` and ``lse`` as in ``attend``."""
         size, index = q.shape, self._index
         if q.dtype is not self.dtype or len(size) != 3 or size[0] != self.batch or size[2] != self.head_dim:
             raise ValueError("the queries must be %s [%d, heads, %d], got %s %s"
