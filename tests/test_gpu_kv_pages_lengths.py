@@ -278,3 +278,24 @@ def test_layers_evicted():
                     want = old[i, :, table[parent][t // 16], h, t % 16]
                     got = kv[i, :, now[b][to // 16], h, to % 16]
                     assert torch.equal(want.view(torch.int16), got.view(torch.int16)), (i, b, h, to)
+
+
+@pytest.mark.parametrize("batch,width", [(300, 130), (1025, 70), (5000, 3), (17000, 2), (65535, 1)])
+def test_wide_batches_cut_and_made_longer(batch, width):
+    """Every form of the count, the fork and the choice keeps the lengths that it left."""
+    _say("lengths of %d sequences" % batch)
+    rng = random.Random(batch)
+    page, most = 3, 3 * width
+    lens = [rng.randint(0, most) for _ in range(batch)]
+    m = made(lens, sum(-(-n // page) for n in lens) + 3 * batch, page, width, seed=batch)
+    for turn in range(3):
+        if turn:
+            m.fork([rng.choice([b, rng.randrange(batch), rng.randrange(3)]) for b in range(batch)])
+        longer = turn != 1
+        set_lens(m, [min(most, n + rng.randrange(3)) if longer else rng.randint(0, n) for n in m.ref.lens])
+        m.pages.resize(m.lens, status=m.status)
+        m.ref.resize(list(m.ref.lens))
+        m.check(("itself", turn))
+        m.resize([min(most, n + 1) for n in m.ref.lens])
+        m.check(("one more", turn))
+    assert m.ref.status == 0
